@@ -45,7 +45,8 @@
  * Besides the step, pa_append_kv writes a step's new K/V rows into their pages
  * (quantising them to fp8 where the cache is fp8), and pa_gather_kv copies a batch's
  * cached K and V rows out of the pages into contiguous buffers (the workspace copy of
- * the HSTU paged attention), with the same calling convention.
+ * the HSTU paged attention), with the same calling convention.  pa_build_tables grows and
+ * shrinks block tables from the requests' lengths.
  */
 #ifndef PA_H_
 #define PA_H_
@@ -103,8 +104,10 @@ enum {
                                 or context_lens[b] > max_blocks_per_seq * block_size */
   PA_FLAG_BAD_BLOCK_ID = 2,  /* a block_tables entry in use lies outside [0, num_blocks) */
   PA_FLAG_WAIT_TIMEOUT = 4,  /* a kernel gave up a bounded wait on its own copies */
-  PA_FLAG_STALE_PLAN = 8     /* pa_decode read lengths other than those pa_plan planned for
+  PA_FLAG_STALE_PLAN = 8,    /* pa_decode read lengths other than those pa_plan planned for
                                 (they changed between the two calls); outputs unspecified */
+  PA_FLAG_NO_FREE_BLOCKS = 32, /* pa_build_tables: fewer free pages than the lengths need */
+  PA_FLAG_BAD_FREE_LIST = 64 /* pa_build_tables: a held or free page count that cannot be */
 };
 
 typedef struct {
@@ -279,6 +282,48 @@ PA_API pa_status pa_append_kv(const pa_config *cfg, const void *k_new, const voi
                               const int32_t *block_tables, const int32_t *context_lens,
                               const int32_t *q_lens, void *k_cache, void *v_cache,
                               float *k_scale, float *v_scale, int32_t *flags, pa_stream stream);
+
+/* Grow and shrink block tables from the requests' lengths, on the GPU.  (The pages cited above
+ * have no counterpart.)
+ *
+ * Row b of block_tables holds held_blocks[b] pages; sequence b needs ceil(context_lens[b] /
+ * block_size).  A row that holds too many gives its last pages to the free list, one that holds
+ * too few takes pages from it, and a finished request is a row with context_lens[b] =
+ * q_lens[b] = 0.  The free list is a stack: free_blocks[0 .. free_count[0]).  The pages given
+ * are pushed first (ascending b, then ascending page), then the pages taken are popped one by
+ * one (ascending b, then ascending page), so the result does not depend on timing.
+ * slot_map[b][i], for new token i < q_lens[b] at position p = context_lens[b] - q_lens[b] + i,
+ * is block_tables[b][p / block_size] * block_size + p % block_size in the tables after the
+ * call, and -1 for i >= q_lens[b].
+ * Reads cfg's batch, max_q_len, block_size, max_blocks_per_seq and num_blocks.
+ *
+ *   context_lens, q_lens, held_blocks   device int32 [batch], read
+ *   block_tables    device int32 [batch, max_blocks_per_seq]: the taken pages' entries are
+ *                   written, all others (those of given pages too) are left as they were
+ *   free_blocks     device int32 [num_blocks]: entries at and above free_count[0] may be written
+ *   free_count      device int32, read
+ *   new_held, new_free_count   device int32 [batch] and int32, written; the next call's
+ *                   held_blocks and free_count.  They may not be the arrays of this call, so
+ *                   that the call reads only what it does not write: with the same inputs it
+ *                   can be run again and gives the same result
+ *   slot_map        NULL, or device int64 [batch, max_q_len], written, 16-byte aligned
+ *   flags           NULL, or a device int32 the call ORs PA_FLAG_* bits into.  PA_FLAG_BAD_LENGTHS
+ *                   (lengths that break the rules of pa_plan), PA_FLAG_BAD_FREE_LIST (a held
+ *                   count outside [0, max_blocks_per_seq], a free count outside [0, num_blocks],
+ *                   or more free pages than num_blocks after the pushes) and
+ *                   PA_FLAG_NO_FREE_BLOCKS: nothing is given or taken, new_held and
+ *                   new_free_count are copies and every slot is -1.  PA_FLAG_BAD_BLOCK_ID: a page
+ *                   in use lies outside [0, num_blocks); its tokens' slots are -1
+ *
+ * Stream-ordered, allocates nothing, never synchronises.  No two arrays may overlap.
+ * PA_ERR_UNSUPPORTED for batch > 4096, a block_size outside the decode's set, or tables or slot
+ * maps of 2^31 entries or more. */
+PA_API pa_status pa_build_tables(const pa_config *cfg, const int32_t *context_lens,
+                                 const int32_t *q_lens, const int32_t *held_blocks,
+                                 int32_t *block_tables, int32_t *free_blocks,
+                                 const int32_t *free_count, int32_t *new_held,
+                                 int32_t *new_free_count, int64_t *slot_map, int32_t *flags,
+                                 pa_stream stream);
 
 /* A static, human-readable name of a status. */
 PA_API const char *pa_status_string(pa_status status);

@@ -16,9 +16,11 @@ from typing import Optional
 
 __all__ = ["PaConfig", "PaError", "load", "workspace_size", "plan", "decode", "reduce",
            "decode_step_static", "STATIC_SCRATCH_BYTES", "append_kv", "gather_kv",
+           "build_tables",
            "read_flags", "status_string", "config_for", "paged_attention", "LIB_PATH",
            "BF16", "FP16", "FP8_E4M3", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
            "FLAG_BAD_LENGTHS", "FLAG_BAD_BLOCK_ID", "FLAG_WAIT_TIMEOUT", "FLAG_STALE_PLAN",
+           "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST",
            "EXPORTED_SYMBOLS",
            "MERGE_AUTO", "MERGE_IN_DECODE", "MERGE_IN_REDUCE"]
 
@@ -31,10 +33,12 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = rang
 BF16, FP16, FP8_E4M3 = 0, 1, 2
 SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN = 0, 1, 2
 FLAG_BAD_LENGTHS, FLAG_BAD_BLOCK_ID, FLAG_WAIT_TIMEOUT, FLAG_STALE_PLAN = 1, 2, 4, 8
+FLAG_NO_FREE_BLOCKS, FLAG_BAD_FREE_LIST = 32, 64
 MERGE_AUTO, MERGE_IN_DECODE, MERGE_IN_REDUCE = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("pa_workspace_size", "pa_plan", "pa_decode", "pa_reduce", "pa_read_flags",
-                    "pa_status_string", "pa_decode_step_static", "pa_gather_kv", "pa_append_kv")
+                    "pa_status_string", "pa_decode_step_static", "pa_gather_kv", "pa_append_kv",
+                    "pa_build_tables")
 
 # Bytes of the device array behind pa_decode_step_static (PA_STATIC_SCRATCH_BYTES).
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -81,6 +85,8 @@ def load(path: str = LIB_PATH):
     L.pa_gather_kv.restype = ctypes.c_int
     L.pa_append_kv.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.pa_append_kv.restype = ctypes.c_int
+    L.pa_build_tables.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.pa_build_tables.restype = ctypes.c_int
     L.pa_status_string.argtypes = [ctypes.c_int]
     L.pa_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -178,6 +184,51 @@ def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k
     _check("pa_append_kv", load().pa_append_kv(
         ctypes.byref(cfg), _ptr(k_new), _ptr(v_new), _ptr(block_tables), _ptr(context_lens),
         _ptr(q_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(flags),
+        _stream(stream)))
+
+
+_type_cache = None
+_current_device = None
+
+
+def _types():
+    """The torch types of int32, int64 and fp32 arrays and, by pa_dtype, of q and of a cache."""
+    global _type_cache, _current_device
+    if _type_cache is None:
+        import torch
+        _current_device = torch.cuda.current_device
+        _type_cache = ((torch.int32,), (torch.int64,), (torch.float32,),
+                       {BF16: (torch.bfloat16,), FP16: (torch.float16,),
+                        FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)})
+    return _type_cache
+
+
+def _dense(call: str, count: int, t, dtypes, optional: bool = False) -> Optional[int]:
+    """Address of a contiguous tensor of at least `count` elements of one of `dtypes` on the
+    current GPU (an int address passes as it is); PaError otherwise."""
+    if isinstance(t, int) or (t is None and optional):
+        return t
+    if t is None or t.dtype not in dtypes or t.numel() < count or not t.is_cuda \
+            or not t.is_contiguous() or t.get_device() != _current_device():
+        raise PaError(call, ERR_INVALID_ARG)
+    return t.data_ptr()
+
+
+def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables, free_blocks,
+                 free_count, new_held, new_free_count, slot_map=None, flags=None, stream=None):
+    """Grow and shrink the rows of block_tables to the pages that context_lens need, out of and
+    back into the free stack free_blocks[:free_count], and write the new tokens' slots (see
+    pa_build_tables in pa.h).  The held and free counts after the call go to new_held and
+    new_free_count, which are the next call's held_blocks and free_count."""
+    i32, i64, _, _ = _types()
+    name, B = "pa_build_tables", cfg.batch
+    _check(name, load().pa_build_tables(
+        ctypes.byref(cfg), _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
+        _dense(name, B, held_blocks, i32),
+        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, cfg.num_blocks, free_blocks, i32), _dense(name, 1, free_count, i32),
+        _dense(name, B, new_held, i32), _dense(name, 1, new_free_count, i32),
+        _dense(name, B * cfg.max_q_len, slot_map, i64, True), _dense(name, 1, flags, i32, True),
         _stream(stream)))
 
 
