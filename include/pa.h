@@ -23,8 +23,9 @@
  * decode kernel processes it, writing whole results directly and per-range
  * partials (o_s, lse_s) otherwise; a reducer merges the partials by
  *     m* = max_s lse_s,  w_s = exp(lse_s - m*),  out = sum_s w_s o_s / sum_s w_s.
- * fp8 caches hold OCP E4M3 codes with one fp32 scale per tensor or one per
- * (block, slot, kv-head) row (FlyDSL PR #910, per_token_kv scale mode).
+ * fp8 caches hold OCP E4M3 codes with one fp32 scale per tensor, one per
+ * (block, slot, kv-head) row (FlyDSL PR #910, per_token_kv scale mode) or one per
+ * (block, kv-head).
  *
  * Calling convention.  The caller owns all memory.  pa_plan, pa_decode and
  * pa_reduce allocate nothing, never synchronise the host and never abort: each
@@ -82,7 +83,8 @@ typedef enum { PA_BF16 = 0, PA_FP16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
 typedef enum {
   PA_SCALE_NONE = 0,       /* 16-bit cache, or fp8 codes used as they are */
   PA_SCALE_PER_TENSOR = 1, /* k_scale, v_scale: one fp32 each */
-  PA_SCALE_PER_TOKEN = 2   /* k_scale, v_scale: fp32 [num_blocks, block_size, num_kv_heads] */
+  PA_SCALE_PER_TOKEN = 2,  /* k_scale, v_scale: fp32 [num_blocks, block_size, num_kv_heads] */
+  PA_SCALE_PER_BLOCK = 3   /* k_scale, v_scale: fp32 [num_blocks, num_kv_heads] */
 } pa_scale_mode;
 
 /* Where the log-sum-exp merge of split units runs.  A unit cut into ns pieces can be merged
@@ -260,6 +262,16 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *                          and WRITTEN to k_scale / v_scale [num_blocks, block_size, Hkv];
  *     PA_SCALE_PER_TENSOR  scale = k_scale[0] / v_scale[0], READ (one fp32 each);
  *     PA_SCALE_NONE        scale 1; k_scale / v_scale may be NULL.
+ *     PA_SCALE_PER_BLOCK   one scale for each (block, kv head) in k_scale / v_scale
+ *                          [num_blocks, Hkv], READ and WRITTEN.  With w = the largest finite
+ *                          magnitude among the call's new rows in the page / 448 (at least
+ *                          2^-126; 0 if they are all zero): a page whose slot 0 is among the
+ *                          new rows gets scale w (1 for w = 0); any other page keeps its scale
+ *                          unless w is larger.  Then the page's scale becomes w and the codes c
+ *                          of its older tokens become E4M3(c * old scale / w), the product and
+ *                          the quotient each rounded to fp32.  The older scale has to be one
+ *                          that an earlier append wrote (positive and finite).  No two
+ *                          sequences may append to one page in one call.
  *   Quotients are IEEE fp32 divisions.  A NaN element gives a NaN code (0x7f or 0xff).
  * Reads cfg's batch, max_q_len, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
  * num_blocks, q_dtype, kv_dtype and kv_scale_mode.

@@ -19,6 +19,7 @@ __all__ = ["PaConfig", "PaError", "load", "workspace_size", "plan", "decode", "r
            "build_tables",
            "read_flags", "status_string", "config_for", "paged_attention", "LIB_PATH",
            "BF16", "FP16", "FP8_E4M3", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
+           "SCALE_PER_BLOCK",
            "FLAG_BAD_LENGTHS", "FLAG_BAD_BLOCK_ID", "FLAG_WAIT_TIMEOUT", "FLAG_STALE_PLAN",
            "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST",
            "EXPORTED_SYMBOLS",
@@ -31,7 +32,7 @@ LIB_PATH = os.path.join(_PKG, "libpa103.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = range(6)
 # pa_dtype, pa_scale_mode, flags
 BF16, FP16, FP8_E4M3 = 0, 1, 2
-SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN = 0, 1, 2
+SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN, SCALE_PER_BLOCK = 0, 1, 2, 3
 FLAG_BAD_LENGTHS, FLAG_BAD_BLOCK_ID, FLAG_WAIT_TIMEOUT, FLAG_STALE_PLAN = 1, 2, 4, 8
 FLAG_NO_FREE_BLOCKS, FLAG_BAD_FREE_LIST = 32, 64
 MERGE_AUTO, MERGE_IN_DECODE, MERGE_IN_REDUCE = 0, 1, 2
@@ -180,7 +181,9 @@ def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k
               k_scale=None, v_scale=None, flags=None, stream=None):
     """Write a step's new K/V rows into their pages, quantised to fp8 for an fp8 cache (see
     pa_append_kv in pa.h): new row i of sequence b lands at position
-    context_lens[b] - q_lens[b] + i.  Per-token scales are written into k_scale / v_scale."""
+    context_lens[b] - q_lens[b] + i.  Per-token scales are written into k_scale / v_scale; a
+    page's one scale (SCALE_PER_BLOCK) is raised where a new row needs it, and the page's older
+    codes follow."""
     _check("pa_append_kv", load().pa_append_kv(
         ctypes.byref(cfg), _ptr(k_new), _ptr(v_new), _ptr(block_tables), _ptr(context_lens),
         _ptr(q_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(flags),
@@ -233,7 +236,8 @@ def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables,
 
 
 _DT = {"bf16": BF16, "fp16": FP16, "fp8": FP8_E4M3}
-_SM = {"none": SCALE_NONE, "tensor": SCALE_PER_TENSOR, "token": SCALE_PER_TOKEN}
+_SM = {"none": SCALE_NONE, "tensor": SCALE_PER_TENSOR, "token": SCALE_PER_TOKEN,
+       "block": SCALE_PER_BLOCK}
 
 
 def config_for(inp: dict, num_ctas: int = 0, grid_mult: int = 0,

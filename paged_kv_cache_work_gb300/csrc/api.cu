@@ -29,7 +29,7 @@ pa_status validate(const pa_config* c) {
   if (c->q_dtype < PA_BF16 || c->q_dtype > PA_FP8_E4M3 || c->kv_dtype < PA_BF16 ||
       c->kv_dtype > PA_FP8_E4M3)
     return PA_ERR_INVALID_ARG;
-  if (c->kv_scale_mode < PA_SCALE_NONE || c->kv_scale_mode > PA_SCALE_PER_TOKEN)
+  if (c->kv_scale_mode < PA_SCALE_NONE || c->kv_scale_mode > PA_SCALE_PER_BLOCK)
     return PA_ERR_INVALID_ARG;
   if (c->causal != 0 && c->causal != 1) return PA_ERR_INVALID_ARG;
   if (!std::isfinite(c->sm_scale)) return PA_ERR_INVALID_ARG;

@@ -10,7 +10,7 @@
 // paged-attention metadata decode" (FlyDSL PR #910, Breaking Changes: per_token_kv):
 // per-token, the row's scale is amax / 448 (1 for an all-zero row) and is written beside the
 // codes; per-tensor, the caller's one scale is read; with no scale the values are encoded as
-// they are.  The scale and every quotient are IEEE fp32 operations (correctly rounded
+// they are.  (One scale for each page and kv head: append_block.cu.)  The scale and every quotient are IEEE fp32 operations (correctly rounded
 // division), and the code is the E4M3 value nearest to the quotient, ties to even, magnitudes
 // past 448 saturating to 448.
 //
@@ -23,7 +23,7 @@
 
 #include <cstdint>
 
-#include "pa_internal.cuh"
+#include "append_block.cuh"
 
 namespace pa {
 namespace {
@@ -51,15 +51,6 @@ __device__ __forceinline__ float to_f32(uint16_t h) {
     return __uint_as_float((uint32_t)h << 16);
   else
     return __half2float(__ushort_as_half(h));
-}
-
-// Two fp32 values to two E4M3 codes (lo -> low byte): round to nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2_rn_sat(float lo, float hi) {
-  uint16_t r;
-  asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n mov.b16 %0, t;\n}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
-  return r;
 }
 
 template <int D, int QK, bool FP8>
@@ -194,7 +185,7 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
   if (c.batch < 1 || c.max_q_len < 1 || c.num_kv_heads < 1 || c.max_blocks_per_seq < 1 ||
       c.num_blocks < 1 || c.head_dim < 1 || c.block_size < 1)
     return PA_ERR_INVALID_ARG;
-  if (c.kv_scale_mode < PA_SCALE_NONE || c.kv_scale_mode > PA_SCALE_PER_TOKEN)
+  if (c.kv_scale_mode < PA_SCALE_NONE || c.kv_scale_mode > PA_SCALE_PER_BLOCK)
     return PA_ERR_INVALID_ARG;
   if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return PA_ERR_UNSUPPORTED;
   if (c.block_size < 16 || c.block_size > 1024 || (c.block_size & (c.block_size - 1)))
@@ -212,6 +203,9 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
   if ((k_scale && !aligned(k_scale, 4)) || (v_scale && !aligned(v_scale, 4)) ||
       (flags && !aligned(flags, 4)))
     return PA_ERR_INVALID_ARG;
+  if (fp8 && c.kv_scale_mode == PA_SCALE_PER_BLOCK)
+    return append_block(c, k_new, v_new, block_tables, context_lens, q_lens, k_cache, v_cache,
+                        k_scale, v_scale, flags, reinterpret_cast<cudaStream_t>(stream));
   AppendParams p;
   p.k_new = static_cast<const char*>(k_new);
   p.v_new = static_cast<const char*>(v_new);

@@ -1,0 +1,240 @@
+// A step's new K/V rows into an fp8 cache with one scale for each (page, kv head).
+//
+// Quantise-on-write.  A page's codes share one scale s, so a new row with a larger magnitude
+// raises it: with a the largest finite magnitude of the call's new rows in the page, w = a / 448,
+//     fresh page (its slot 0 is new):  s = w (1 for a = 0)
+//     else                             s = max(s_old, w); for w > s_old the older codes c become
+//                                      E4M3(c s_old / s), for w <= s_old they stay
+// and the new codes are E4M3(x / s).  An infinite element does not set the scale (it saturates to
+// 448 s), so it cannot wipe out its neighbours.  All of a page's new rows of one call are taken
+// together: the order of rows does not enter.
+//
+// One CTA per (sequence, touched page, kv head, K or V): nobody else writes that page's codes of
+// that head or its scale, so there is nothing to join.  A thread keeps up to kKeep 16-byte pieces
+// of the new rows in registers between the pass for a and the pass for the codes; only pages
+// with more new rows than that are read twice (the second time from L2).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "append_block.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeep = 4;  // 16-byte pieces of new rows a thread keeps in registers
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+struct AppendBlockParams {
+  const char* k_new;
+  const char* v_new;
+  const int32_t* bt;
+  const int32_t* ctx;
+  const int32_t* qlens;
+  char* k_cache;
+  char* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int32_t* flags;
+  int Sq, Hkv, bs, bs_shift, maxb, nblocks;
+  FastDiv head_div, page_div;  // by Hkv and by the pages a sequence can touch
+};
+
+// A touched page: the new rows [i0, i0 + rows) of sequence b go to slots [slot0, slot0 + rows)
+// of block blk.  False when there is none (or it is flagged).
+struct TouchedPage {
+  int i0, rows, slot0, blk;
+};
+__device__ __forceinline__ bool touched_page(const AppendBlockParams& p, int b, int j,
+                                             bool reports, TouchedPage* t) {
+  const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
+  const long long cap = (long long)p.maxb << p.bs_shift;
+  if (ql < 0 || ql > p.Sq || n < ql || (long long)n > cap) {
+    if (reports && j == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
+    return false;
+  }
+  const int first = n - ql, page = (first >> p.bs_shift) + j;
+  const long long start = (long long)page << p.bs_shift;
+  if (ql == 0 || start >= n) return false;
+  const int lo = max((int)start, first), hi = (int)min(start + p.bs, (long long)n);
+  t->i0 = lo - first;
+  t->rows = hi - lo;
+  t->slot0 = lo - (int)start;
+  t->blk = __ldg(p.bt + (size_t)b * p.maxb + page);
+  if (t->blk < 0 || t->blk >= p.nblocks) {
+    if (reports && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
+    return false;
+  }
+  return true;
+}
+
+template <int QK>
+__device__ __forceinline__ float2 pair_to_f2(uint32_t w) {
+  if constexpr (QK == Q_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+__device__ __forceinline__ float finite_amax(float a, float x) {
+  const float m = fabsf(x);
+  return m <= 3.402823466e38f ? fmaxf(a, m) : a;  // false for inf and NaN
+}
+
+template <int D, int QK>
+__global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBlockParams p) {
+  constexpr int PPR = D / 8;  // 16-byte pieces (8 elements) of a new row
+  constexpr int NW = kThreads / 32;
+  __shared__ float s_max[NW];
+  const int tid = threadIdx.x;
+  uint32_t u = blockIdx.x;
+  const bool is_v = u & 1;
+  u >>= 1;
+  const uint32_t bj = p.head_div.div(u);
+  const int g = (int)(u - bj * p.Hkv);
+  const int b = (int)p.page_div.div(bj), j = (int)p.page_div.mod(bj);
+  grid_dependency_wait();
+  TouchedPage t;
+  if (!touched_page(p, b, j, tid == 0 && !is_v, &t)) return;
+  const size_t page_head = (size_t)t.blk * p.Hkv + g;
+  float* scale = (is_v ? p.v_scale : p.k_scale) + page_head;
+  const bool fresh = t.slot0 == 0;
+  const float s_old = fresh ? 0.f : *scale;
+  const size_t row_stride = (size_t)p.Hkv * D;  // elements between a head's rows (new and cached)
+  const uint4* src = reinterpret_cast<const uint4*>(
+      (is_v ? p.v_new : p.k_new) + (((size_t)b * p.Sq + t.i0) * row_stride + (size_t)g * D) * 2);
+  auto piece = [&](int e) {  // piece e of the page's new rows
+    return __ldg(src + (size_t)(e / PPR) * (row_stride / 8) + e % PPR);
+  };
+
+  // ---- largest finite magnitude of the page's new rows
+  const int pieces = t.rows * PPR;
+  uint4 keep[kKeep];
+  float a = 0.f;
+  auto amax_of = [&](const uint4& w) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = pair_to_f2<QK>(v[k]);
+      a = finite_amax(finite_amax(a, f.x), f.y);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int e = tid + k * kThreads;
+    keep[k] = e < pieces ? piece(e) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) amax_of(keep[k]);
+  for (int e = tid + kKeep * kThreads; e < pieces; e += kThreads) amax_of(piece(e));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
+  if ((tid & 31) == 0) s_max[tid >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) a = fmaxf(a, s_max[w]);
+
+  const float w = a > 0.f ? fmaxf(__fdiv_rn(a, 448.f), kMinScale) : 0.f;
+  const bool grown = !fresh && w > s_old;
+  const float s = fresh ? (w > 0.f ? w : 1.f) : (grown ? w : s_old);
+  if (tid == 0 && (fresh || grown)) *scale = s;  // every thread has read s_old
+
+  // ---- the older codes under the larger scale
+  char* cache = (is_v ? p.v_cache : p.k_cache) +
+                ((size_t)t.blk * p.bs) * row_stride + (size_t)g * D;  // slot 0, this head
+  if (grown) {
+    for (int e = tid; e < t.slot0 * PPR; e += kThreads) {
+      uint2* at = reinterpret_cast<uint2*>(cache + (size_t)(e / PPR) * row_stride + (e % PPR) * 8);
+      uint2 c = *at;
+      c.x = rescale4(c.x, s_old, s);
+      c.y = rescale4(c.y, s_old, s);
+      *at = c;
+    }
+  }
+  // ---- the new codes
+  auto put = [&](int e, const uint4& v) {
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = pair_to_f2<QK>(h[k]);
+      c[k] = e4m3x2_rn_sat(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    }
+    *reinterpret_cast<uint2*>(cache + (size_t)(t.slot0 + e / PPR) * row_stride + (e % PPR) * 8) =
+        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int e = tid + k * kThreads;
+    if (e < pieces) put(e, keep[k]);
+  }
+  for (int e = tid + kKeep * kThreads; e < pieces; e += kThreads) put(e, piece(e));
+}
+
+template <class K>
+cudaError_t launch(K kernel, const AppendBlockParams& p, uint32_t grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// The pages a sequence can touch with Sq new rows: they start anywhere in a page.
+long long pages_touched(const pa_config& c) {
+  return ((long long)c.max_q_len + c.block_size - 2) / c.block_size + 1;
+}
+
+AppendBlockParams block_params(const pa_config& c, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* q_lens,
+                               int32_t* flags) {
+  AppendBlockParams p{};
+  p.bt = block_tables;
+  p.ctx = context_lens;
+  p.qlens = q_lens;
+  p.flags = flags;
+  p.Sq = c.max_q_len;
+  p.Hkv = c.num_kv_heads;
+  p.bs = c.block_size;
+  p.bs_shift = ilog2((uint32_t)c.block_size);
+  p.maxb = c.max_blocks_per_seq;
+  p.nblocks = c.num_blocks;
+  p.head_div = FastDiv((uint32_t)c.num_kv_heads);
+  p.page_div = FastDiv((uint32_t)pages_touched(c));
+  return p;
+}
+
+}  // namespace
+
+pa_status append_block(const pa_config& c, const void* k_new, const void* v_new,
+                       const int32_t* block_tables, const int32_t* context_lens,
+                       const int32_t* q_lens, void* k_cache, void* v_cache, float* k_scale,
+                       float* v_scale, int32_t* flags, cudaStream_t s) {
+  const double ctas = 2.0 * c.batch * (double)pages_touched(c) * c.num_kv_heads;
+  if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  AppendBlockParams p = block_params(c, block_tables, context_lens, q_lens, flags);
+  p.k_new = static_cast<const char*>(k_new);
+  p.v_new = static_cast<const char*>(v_new);
+  p.k_cache = static_cast<char*>(k_cache);
+  p.v_cache = static_cast<char*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  const bool half = c.q_dtype == PA_FP16;
+  const uint32_t grid = (uint32_t)ctas;
+  cudaError_t e;
+  switch (c.head_dim) {
+    case 64: e = launch(half ? append_block_kernel<64, Q_FP16> : append_block_kernel<64, Q_BF16>, p, grid, s); break;
+    case 128: e = launch(half ? append_block_kernel<128, Q_FP16> : append_block_kernel<128, Q_BF16>, p, grid, s); break;
+    default: e = launch(half ? append_block_kernel<256, Q_FP16> : append_block_kernel<256, Q_BF16>, p, grid, s); break;
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa

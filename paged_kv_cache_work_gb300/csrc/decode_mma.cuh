@@ -21,19 +21,22 @@
 // Q K^T each lane's four consecutive fp8 dimensions become its two k-pairs (the query
 // fragments use the same permuted k order); for P V the transposed pairs hold two tokens
 // of two adjacent dimensions, and a byte permute splits them into the fragments of an
-// even-dimension and an odd-dimension n-block.
+// even-dimension and an odd-dimension n-block.  Scales: a per-tensor one enters the logit scale
+// and the normalisation, a token's its logit and weight; with one for each (page, kv head) a
+// chunk of 16 tokens has one K and one V scale, two scalars a chunk.
 #pragma once
 
 #include "decode_common.cuh"
 
 namespace pa {
 
-template <int D_, int MP_, int KVK_, bool TOKS_>
+template <int D_, int MP_, int KVK_, int SC_>
 struct MmaTraits {
   static constexpr int D = D_;
   static constexpr int MP = MP_;
   static constexpr int KVK = KVK_;
-  static constexpr bool TOKS = TOKS_;
+  static constexpr bool TOKS = SC_ != SC_NONE;   // scales are staged with the tile
+  static constexpr bool BLKS = SC_ == SC_BLOCK;  // one for each page
   static constexpr bool FP8 = KVK == KV_FP8;
   static constexpr int BPE = FP8 ? 1 : 2;
   static constexpr int NW = 4;
@@ -136,11 +139,11 @@ __device__ __forceinline__ uint32_t tile_chunk_addr(uint32_t tile, int row, int 
   return tile + slab * T::SLAB + row * T::ROWB + ((chunk ^ (row & 7)) << 4);
 }
 
-template <int D, int MP, int KVK, int QK, bool TOKS>
-__global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
+template <int D, int MP, int KVK, int QK, int SC>
+__global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
     decode_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const KernelParams p) {
-  using T = MmaTraits<D, MP, KVK, TOKS>;
+  using T = MmaTraits<D, MP, KVK, SC>;
   constexpr bool F16 = KVK != KV_BF16;  // operand type of the MMA: f16 for f16 and fp8 caches
   constexpr int WR = T::WR, NB = T::NB, KSTEPS = D / 16;
   extern __shared__ char smem_raw[];
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
   const int rblk = warp % T::RBW, ts = warp / T::RBW;
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::NSTAGE; ++s) {
-      mbar_init(&full[s], TOKS ? 33 : 1);
+      mbar_init(&full[s], T::TOKS ? 33 : 1);
       mbar_init(&empty[s], T::NW);
     }
     mbar_init(&qfull[0], 32);
@@ -279,6 +282,7 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
     }
 
     float o[WR][NB][4];
+    float vref = kPow2Least;  // one V scale a page: o is in units of vref / kPLift
     float m_run[WR][2], l_run[WR][2];
 #pragma unroll
     for (int w = 0; w < WR; ++w) {
@@ -368,6 +372,23 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
             }
           }
         }
+        // one scale a page: the chunk's 16 tokens share theirs
+        float qk_chunk = qk_scale, v_chunk = 1.f;
+        if constexpr (T::BLKS) {
+          qk_chunk *= sks[c0];
+          const float vs = svs[c0];
+          if (fabsf(vs) > vref) {  // warp-uniform
+            const float up = pow2_above(fabsf(vs)), f = vref * pow2_inverse(up);
+            vref = up;
+#pragma unroll
+            for (int w = 0; w < WR; ++w)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[w][nb][j] *= f;
+          }
+          v_chunk = vs * pow2_inverse(vref) * kPLift;
+        }
         // ---- online softmax on the accumulators (rows quad, quad + 8; 4 tokens each)
         uint32_t pa[WR][4];
 #pragma unroll
@@ -378,8 +399,8 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int tt = (j >> 1) * 8 + 2 * qi + (j & 1);  // token within the chunk
-              float x = sacc[w][j >> 1][2 * h + (j & 1)] * qk_scale;
-              if constexpr (TOKS) x *= sks[c0 + tt];
+              float x = sacc[w][j >> 1][2 * h + (j & 1)] * qk_chunk;
+              if constexpr (T::TOKS && !T::BLKS) x *= sks[c0 + tt];
               const bool vis = c0 + tt < n_in && tok0 + c0 + tt < lim[w][h];
               sv[h][j] = vis ? x : -INFINITY;
             }
@@ -417,7 +438,10 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
               pr[h][j] = vis ? fast_exp2(sv[h][j] - m_run[w][h]) : 0.f;
               l_run[w][h] += pr[h][j];
               // a masked token's scale slot may be stale: only visible tokens are scaled
-              if constexpr (TOKS) pr[h][j] = vis ? pr[h][j] * svs[c0 + (j >> 1) * 8 + 2 * qi + (j & 1)] : 0.f;
+              if constexpr (T::BLKS)
+                pr[h][j] = vis ? pr[h][j] * v_chunk : 0.f;
+              else if constexpr (T::TOKS)
+                pr[h][j] = vis ? pr[h][j] * svs[c0 + (j >> 1) * 8 + 2 * qi + (j & 1)] : 0.f;
             }
           }
           pa[w][0] = pack2<F16>(pr[0][0], pr[0][1]);  // row quad,     tokens 2qi, 2qi+1
@@ -468,6 +492,14 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
       if (lane == 0 && k + 1 < ntiles) mbar_arrive(&empty[s]);  // the last stage holds the merge
     }
 
+    if constexpr (T::BLKS) {
+#pragma unroll
+      for (int w = 0; w < WR; ++w)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[w][nb][j] *= vref * (1.f / kPLift);
+    }
     // ---- merge the token streams of each row block (tree through the last stage)
     float* obuf = reinterpret_cast<float*>(smem + s_last * T::STAGE);
     if (threadIdx.x == 32) *cnt_seen_s = cnt_seen;
@@ -619,11 +651,11 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, TOKS>::NTHREADS, 2)
   zero_empty_units<D, MP, QK, T::NTHREADS>(p);
 }
 
-template <int D, int MP, int KVK, int QK, bool TOKS>
+template <int D, int MP, int KVK, int QK, int SC>
 cudaError_t launch_mma_instance(const KernelParams& prm, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  using T = MmaTraits<D, MP, KVK, TOKS>;
-  auto kern = decode_mma_kernel<D, MP, KVK, QK, TOKS>;
+  using T = MmaTraits<D, MP, KVK, SC>;
+  auto kern = decode_mma_kernel<D, MP, KVK, QK, SC>;
   static std::atomic<uint64_t> attr_done{0};  // devices whose limit is raised
   const cudaError_t e = set_smem_attr_once(attr_done, reinterpret_cast<const void*>(kern), T::SMEM);
   if (e != cudaSuccess) return e;
@@ -640,13 +672,15 @@ cudaError_t launch_mma_instance(const KernelParams& prm, const CUtensorMap& kmap
   return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, prm);
 }
 
-#define PA_MMA_ROWS(X, MP_)      \
-  X(MP_, KV_BF16, Q_BF16, false) \
-  X(MP_, KV_FP16, Q_FP16, false) \
-  X(MP_, KV_FP8, Q_BF16, false)  \
-  X(MP_, KV_FP8, Q_BF16, true)   \
-  X(MP_, KV_FP8, Q_FP16, false)  \
-  X(MP_, KV_FP8, Q_FP16, true)
+#define PA_MMA_ROWS(X, MP_)         \
+  X(MP_, KV_BF16, Q_BF16, SC_NONE)  \
+  X(MP_, KV_FP16, Q_FP16, SC_NONE)  \
+  X(MP_, KV_FP8, Q_BF16, SC_NONE)   \
+  X(MP_, KV_FP8, Q_BF16, SC_TOKEN)  \
+  X(MP_, KV_FP8, Q_BF16, SC_BLOCK)  \
+  X(MP_, KV_FP8, Q_FP16, SC_NONE)   \
+  X(MP_, KV_FP8, Q_FP16, SC_TOKEN)  \
+  X(MP_, KV_FP8, Q_FP16, SC_BLOCK)
 #define PA_MMA_ALL(X) PA_MMA_ROWS(X, 16) PA_MMA_ROWS(X, 32) PA_MMA_ROWS(X, 64)
 
 // A cache row must hold whole 128-byte slabs (a 64-dim fp8 cache stays on CUDA cores).
@@ -655,11 +689,11 @@ constexpr bool mma_fits(int D, int kvk) { return D * (kvk == KV_FP8 ? 1 : 2) >= 
 template <int D>
 cudaError_t launch_mma_for_dim(const KernelParams& prm, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int grid, int mp, int kvk, int qk,
-                               bool toks, cudaStream_t s) {
-#define PA_MMA_CASE(MP_, KVK_, QK_, TOKS_)                                          \
+                               int scales, cudaStream_t s) {
+#define PA_MMA_CASE(MP_, KVK_, QK_, SC_)                                          \
   if constexpr (mma_fits(D, KVK_)) {                                                \
-    if (mp == MP_ && kvk == KVK_ && qk == QK_ && toks == TOKS_)                     \
-      return launch_mma_instance<D, MP_, KVK_, QK_, TOKS_>(prm, kmap, vmap, grid, s); \
+    if (mp == MP_ && kvk == KVK_ && qk == QK_ && scales == SC_)                     \
+      return launch_mma_instance<D, MP_, KVK_, QK_, SC_>(prm, kmap, vmap, grid, s); \
   }
   PA_MMA_ALL(PA_MMA_CASE)
 #undef PA_MMA_CASE
@@ -667,10 +701,10 @@ cudaError_t launch_mma_for_dim(const KernelParams& prm, const CUtensorMap& kmap,
 }
 
 template <int D>
-int mma_ctas_per_sm_for_dim(int mp, int kvk, bool toks) {
-#define PA_MMA_OCC(MP_, KVK_, QK_, TOKS_)                                            \
+int mma_ctas_per_sm_for_dim(int mp, int kvk, int scales) {
+#define PA_MMA_OCC(MP_, KVK_, QK_, SC_)                                            \
   if constexpr (mma_fits(D, KVK_)) {                                                 \
-    if (mp == MP_ && kvk == KVK_ && toks == TOKS_) return MmaTraits<D, MP_, KVK_, TOKS_>::CTAS_PER_SM; \
+    if (mp == MP_ && kvk == KVK_ && scales == SC_) return MmaTraits<D, MP_, KVK_, SC_>::CTAS_PER_SM; \
   }
   PA_MMA_ALL(PA_MMA_OCC)
 #undef PA_MMA_OCC

@@ -1,6 +1,6 @@
 // Fifth-generation tensor-core decode (tcgen05, accumulators in tensor memory) for large
 // query tiles: 33 to 128 query rows per kv head, 16-bit caches of head dim 128 or 256 and
-// fp8 caches of head dim 128 with per-tensor, per-token or no scales.
+// fp8 caches of head dim 128 with per-tensor, per-token, per-page or no scales.
 //
 // A step is a tile of 64 tokens.  The CTA is split into roles that talk only through
 // mbarriers, so copies, MMAs and the softmax of different steps overlap:
@@ -43,12 +43,13 @@
 
 namespace pa {
 
-template <int D_, int MP_, int KVK_, bool TOKS_>
+template <int D_, int MP_, int KVK_, int SC_>
 struct TcTraits {
   static constexpr int D = D_;    // 128 or 256
   static constexpr int MP = MP_;  // query rows of a unit; the MMA always has M = 128
   static constexpr int KVK = KVK_;
-  static constexpr bool TOKS = TOKS_;  // per-token fp8 scales
+  static constexpr bool TOKS = SC_ != SC_NONE;   // fp8 scales staged for each token
+  static constexpr bool BLKS = SC_ == SC_BLOCK;  // (the same one for all of a page)
   static constexpr bool FP8 = KVK == KV_FP8;
   static constexpr int BPE = FP8 ? 1 : 2;
   static constexpr int W_PROD = 0, W_MMA = 1, W_SOFT = 2, W_CONV = 6;
@@ -416,6 +417,8 @@ struct TcProducer {
   const int4* items;
   const float* kscale;
   const float* vscale;
+  long long sc_block;  // strides of the staged scales (see KernelParams)
+  int sc_slot;
   int maxb, bs, bs_shift, nblocks, Hkv, RB;
   int lane, box_rows, nbox;
   uint32_t box_bytes, nk, nv, nsc;
@@ -438,10 +441,11 @@ struct TcProducer {
     flags = sflags; bt = prm->bt; items = prm->items; kscale = prm->k_scale;
     vscale = prm->v_scale; maxb = prm->maxb; bs = prm->bs; bs_shift = prm->bs_shift;
     nblocks = prm->nblocks; Hkv = prm->Hkv; RB = prm->RB;
+    sc_block = prm->sc_block; sc_slot = prm->sc_slot;
     box_rows = min(bs, T::TT);
     nbox = T::TT / box_rows;
     box_bytes = (uint32_t)box_rows * T::ROWB;
-    scale_bulk = T::TOKS && Hkv == 1 && box_rows == T::TT &&
+    scale_bulk = T::TOKS && sc_slot == 1 && box_rows == T::TT &&
                  ((reinterpret_cast<uintptr_t>(kscale) | reinterpret_cast<uintptr_t>(vscale)) & 15) == 0;
     nk = nv = nsc = 0;
     list.init(*prm, first);
@@ -575,7 +579,7 @@ struct TcProducer {
           const bool ok = __shfl_sync(kFull, bx.ok ? 1 : 0, src) != 0;
           const int tok = bx.tok0 + t;
           if (ok && tok < bx.t1) {
-            const size_t idx = ((size_t)blk * bs + (tok & (bs - 1))) * Hkv + bx.g;
+            const size_t idx = (size_t)(blk * sc_block) + (size_t)((tok & (bs - 1)) * sc_slot) + bx.g;
             cp_async_4(ks + t, kscale + idx);
             cp_async_4(vs + t, vscale + idx);
           }
@@ -642,11 +646,11 @@ struct TcProducer {
   }
 };
 
-template <int D_, int MP, int KVK, int QK, bool TOKS>
-__global__ void __launch_bounds__(TcTraits<D_, MP, KVK, TOKS>::NTHREADS, 1)
+template <int D_, int MP, int KVK, int QK, int SC>
+__global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const KernelParams p) {
-  using T = TcTraits<D_, MP, KVK, TOKS>;
+  using T = TcTraits<D_, MP, KVK, SC>;
   constexpr int SUB = T::SUB;
   constexpr int D = T::D;
   constexpr int NSP = T::NSP;
@@ -1014,6 +1018,21 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, TOKS>::NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
 
+      // one V scale a page: weights take the scale over a power of two above the item's largest
+      float vref = 1.f, vinv = 1.f;
+      if constexpr (T::BLKS) {
+        float big = 0.f;
+        for (int pg = (t0 >> p.bs_shift) + lane; pg <= (t1 - 1) >> p.bs_shift; pg += 32) {
+          const int blk = __ldg(p.bt + (size_t)b * p.maxb + pg);
+          if (blk >= 0 && blk < p.nblocks)
+            big = fmaxf(big, fabsf(__ldg(p.v_scale + (size_t)blk * p.Hkv + g_kv)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+        vref = pow2_above(big);
+        vinv = pow2_inverse(vref) * kPLift;
+        vref *= 1.f / kPLift;
+      }
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nsub; ++j, ++g) {
         const int tok0 = t0 + j * SUB, nv = min(SUB, t1 - tok0);  // tokens of the item here
@@ -1130,8 +1149,13 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, TOKS>::NTHREADS, 1)
                   const float2 v2 =
                       SC_REG ? make_float2(vsc[32 * h + 2 * i], vsc[32 * h + 2 * i + 1])
                              : *reinterpret_cast<const float2*>(svs + c0 + 32 * h + 2 * i);
-                  p0 = p0 == 0.f ? 0.f : p0 * v2.x;
-                  p1 = p1 == 0.f ? 0.f : p1 * v2.y;
+                  if constexpr (T::BLKS) {
+                    p0 = p0 == 0.f ? 0.f : p0 * (v2.x * vinv);
+                    p1 = p1 == 0.f ? 0.f : p1 * (v2.y * vinv);
+                  } else {
+                    p0 = p0 == 0.f ? 0.f : p0 * v2.x;
+                    p1 = p1 == 0.f ? 0.f : p1 * v2.y;
+                  }
                 }
                 pk[i] = pack16x2<BF>(p0, p1);
               }
@@ -1220,7 +1244,7 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, TOKS>::NTHREADS, 1)
         }
       }
       if (!DUAL || hs == 0) {
-        float inv = l_run > 0.f ? vts / l_run : 0.f;
+        float inv = l_run > 0.f ? (T::BLKS ? vref : vts) / l_run : 0.f;
         float lse2 = l_run > 0.f ? m_run + fast_log2(l_run) : -INFINITY;
         // piece 0 finishing the unit: merged with pieces 1 .. ns-1 in the arithmetic of
         // merge_unit
@@ -1407,11 +1431,11 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, TOKS>::NTHREADS, 1)
   }
 }
 
-template <int D, int MP, int KVK, int QK, bool TOKS>
+template <int D, int MP, int KVK, int QK, int SC>
 cudaError_t launch_tc_instance(const KernelParams& prm, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  using T = TcTraits<D, MP, KVK, TOKS>;
-  auto kern = decode_tc_kernel<D, MP, KVK, QK, TOKS>;
+  using T = TcTraits<D, MP, KVK, SC>;
+  auto kern = decode_tc_kernel<D, MP, KVK, QK, SC>;
   static std::atomic<uint64_t> attr_done{0};  // devices whose limit is raised
   const cudaError_t e = set_smem_attr_once(attr_done, reinterpret_cast<const void*>(kern), T::SMEM);
   if (e != cudaSuccess) return e;

@@ -68,9 +68,16 @@ inline int pow2_at_least(int x) {
   return p;
 }
 
+// Scales that differ between tokens are staged beside a tile: one for every token, or a page's
+// one scale where it is needed.
+enum StagedScales { SC_NONE = 0, SC_TOKEN = 1, SC_BLOCK = 2 };
+inline int staged_scales(int mode) {
+  return mode == PA_SCALE_PER_TOKEN ? SC_TOKEN : mode == PA_SCALE_PER_BLOCK ? SC_BLOCK : SC_NONE;
+}
+
 // CTAs of the decode instance for these parameters that fit on one SM.
 int simt_ctas_per_sm(int head_dim, int mp, int kvk, bool toks);
-int mma_ctas_per_sm(int head_dim, int mp, int kvk, bool toks);
+int mma_ctas_per_sm(int head_dim, int mp, int kvk, int scales);
 // Largest row tile of the tensor-core decode kernel.
 constexpr int kMmaMaxRows = 64;
 
@@ -121,10 +128,10 @@ inline Variant make_variant(const pa_config& c) {
                             : round_up(kItemCostTiles * (kTileBytes / (c.head_dim * v.bpe)), v.tt);
   v.units = c.batch * c.num_kv_heads * v.rb;
   const int kvk = c.kv_dtype == PA_FP8_E4M3 ? 2 : (c.kv_dtype == PA_FP16 ? 1 : 0);
-  const bool toks = c.kv_scale_mode == PA_SCALE_PER_TOKEN;
+  const int scales = staged_scales(c.kv_scale_mode);
   v.ctas_per_sm = v.path == 2   ? 1
-                  : v.path == 1 ? mma_ctas_per_sm(c.head_dim, v.mp, kvk, toks)
-                                : simt_ctas_per_sm(c.head_dim, v.mp, kvk, toks);
+                  : v.path == 1 ? mma_ctas_per_sm(c.head_dim, v.mp, kvk, scales)
+                                : simt_ctas_per_sm(c.head_dim, v.mp, kvk, scales != SC_NONE);
   v.ns_dec = decode_merge_limit(c.split_merge, v.path);
   v.ctas = 0;
   return v;
@@ -405,6 +412,22 @@ __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// V scales that differ between pages enter the f16 weights P, so they are taken relative to a
+// power of two above the largest so far (the accumulator is in units of it): a weight then keeps
+// its 11 bits however small the scales are.  A weight is at most 2^8 before its scale, so kPLift
+// = 2^7 more keeps it below f16's 65504 and moves f16's subnormals, where a weight loses bits,
+// down to 2^-21 of the largest.  pow2_above: the least power of two above x >= 0, within
+// [2^-125, 2^125]; pow2_inverse: its exact inverse.
+constexpr float kPLift = 128.f;
+constexpr float kPow2Least = 2.350988701644575e-38f;  // 2^-125
+__device__ __forceinline__ float pow2_above(float x) {
+  const int e = (int)((__float_as_uint(x) >> 23) & 255) + 1;
+  return __uint_as_float((uint32_t)min(max(e, 2), 252) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
 // Packed fp32x2 multiply-add (sm_100 family): d = a * b + c, lane-wise on float2.

@@ -26,28 +26,30 @@ cudaError_t launch_tc_d128(const KernelParams&, const CUtensorMap&, const CUtens
 cudaError_t launch_tc_d256(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int,
                            int, int, bool, cudaStream_t);
 cudaError_t launch_tc_fp8_d128(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int,
-                               int, int, bool, cudaStream_t);
+                               int, int, int, cudaStream_t);
+cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, const CUtensorMap&,
+                                     int, int, int, cudaStream_t);
 
-int mma_ctas_per_sm_d64(int, int, bool);
-int mma_ctas_per_sm_d128(int, int, bool);
-int mma_ctas_per_sm_d256(int, int, bool);
+int mma_ctas_per_sm_d64(int, int, int);
+int mma_ctas_per_sm_d128(int, int, int);
+int mma_ctas_per_sm_d256(int, int, int);
 cudaError_t launch_mma_d64(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int,
-                           int, int, bool, cudaStream_t);
+                           int, int, int, cudaStream_t);
 cudaError_t launch_mma_d128(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int,
-                            int, int, bool, cudaStream_t);
+                            int, int, int, cudaStream_t);
 cudaError_t launch_mma_d256(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int,
-                            int, int, bool, cudaStream_t);
+                            int, int, int, cudaStream_t);
 
 // The CUDA-core kernel serves 64-dim fp8 caches only (rows shorter than a 128-byte slab).
 int simt_ctas_per_sm(int head_dim, int mp, int kvk, bool toks) {
   return head_dim == 64 ? simt_ctas_per_sm_d64(mp, kvk, toks) : 1;
 }
 
-int mma_ctas_per_sm(int head_dim, int mp, int kvk, bool toks) {
+int mma_ctas_per_sm(int head_dim, int mp, int kvk, int scales) {
   switch (head_dim) {
-    case 64: return mma_ctas_per_sm_d64(mp, kvk, toks);
-    case 128: return mma_ctas_per_sm_d128(mp, kvk, toks);
-    default: return mma_ctas_per_sm_d256(mp, kvk, toks);
+    case 64: return mma_ctas_per_sm_d64(mp, kvk, scales);
+    case 128: return mma_ctas_per_sm_d128(mp, kvk, scales);
+    default: return mma_ctas_per_sm_d256(mp, kvk, scales);
   }
 }
 
@@ -72,6 +74,9 @@ KernelParams make_kernel_params(const DecodeArgs& a) {
   p.units = a.v.units;
   p.ns_dec = a.v.ns_dec;
   p.scale_mode = a.scale_mode;
+  const bool per_block = a.scale_mode == PA_SCALE_PER_BLOCK;
+  p.sc_slot = per_block ? 0 : a.p.num_kv_heads;
+  p.sc_block = (long long)a.p.num_kv_heads * (per_block ? 1 : a.p.block_size);
   p.Sq = a.p.max_q_len;
   p.Hq = a.p.num_q_heads;
   p.Hkv = a.p.num_kv_heads;
@@ -94,12 +99,14 @@ KernelParams make_kernel_params(const DecodeArgs& a) {
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           cudaStream_t s) {
   const KernelParams prm = make_kernel_params(a);
-  const bool toks = a.scale_mode == PA_SCALE_PER_TOKEN;
+  const int scales = staged_scales(a.scale_mode);
+  const bool toks = scales != SC_NONE;
   if (a.v.path == 2) {
     if (a.kv_kind == KV_FP8)
-      return a.p.head_dim == 128
-                 ? launch_tc_fp8_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, toks, s)
-                 : cudaErrorNotSupported;
+      return a.p.head_dim != 128 ? cudaErrorNotSupported
+             : scales == SC_BLOCK
+                 ? launch_tc_fp8_block_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s)
+                 : launch_tc_fp8_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, scales, s);
     switch (a.p.head_dim) {
       case 128: return launch_tc_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, toks, s);
       case 256: return launch_tc_d256(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, toks, s);
@@ -108,9 +115,9 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CU
   }
   if (a.v.path == 1) {
     switch (a.p.head_dim) {
-      case 64: return launch_mma_d64(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, toks, s);
-      case 128: return launch_mma_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, toks, s);
-      case 256: return launch_mma_d256(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, toks, s);
+      case 64: return launch_mma_d64(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, scales, s);
+      case 128: return launch_mma_d128(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, scales, s);
+      case 256: return launch_mma_d256(prm, kmap, vmap, a.v.ctas, a.v.mp, a.kv_kind, a.q_kind, scales, s);
       default: return cudaErrorNotSupported;
     }
   }
