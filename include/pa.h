@@ -47,7 +47,9 @@
  * (quantising them to fp8 where the cache is fp8), and pa_gather_kv copies a batch's
  * cached K and V rows out of the pages into contiguous buffers (the workspace copy of
  * the HSTU paged attention), with the same calling convention.  pa_build_tables grows and
- * shrinks block tables from the requests' lengths.
+ * shrinks block tables from the requests' lengths.  A step that attends over a part of its
+ * cached pages keeps channel bounds of every page's keys (pa_update_bounds), scores the pages
+ * with them (pa_score_blocks) and selects pages by score (pa_select_blocks).
  */
 #ifndef PA_H_
 #define PA_H_
@@ -336,6 +338,58 @@ PA_API pa_status pa_build_tables(const pa_config *cfg, const int32_t *context_le
                                  const int32_t *free_count, int32_t *new_held,
                                  int32_t *new_free_count, int64_t *slot_map, int32_t *flags,
                                  pa_stream stream);
+
+/* Channel bounds of a page's keys, kept as keys are appended.  (The pages cited above have no
+ * counterpart of this call and the two below.)
+ *
+ * k_bounds [num_blocks, num_kv_heads, 2, head_dim] in q_dtype holds, for each page and kv head,
+ * the least ([.., 0, :]) and the largest ([.., 1, :]) value of each channel over the page's keys
+ * as they were given (before any quantisation).  A page whose slot 0 is among the new rows
+ * starts afresh; any other page's bounds are widened by the new rows.  NaN stays NaN.
+ * Arguments and flags are those of pa_append_kv, which may run before or after it.  Reads cfg's
+ * batch, max_q_len, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks and
+ * q_dtype. */
+PA_API pa_status pa_update_bounds(const pa_config *cfg, const void *k_new,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *q_lens, void *k_bounds, int32_t *flags,
+                                  pa_stream stream);
+
+/* Scores of a sequence's pages for each new-token row and kv head.
+ *
+ * With L the keys that row i sees (as for the decode), page p < ceil(L / block_size) of row i
+ * and kv head g scores
+ *     max over the group's heads h of  sm_scale * sum_d (max(q_d, 0) hi_d + min(q_d, 0) lo_d)
+ * with lo and hi the page's bounds: for sm_scale >= 0 no key of the page has a larger logit.
+ * Other pages, and the rows i >= q_lens[b], score -inf.  Products and sums are in fp32; bounds
+ * or queries that are not finite give scores that are not (NaN included).
+ *   q        [B, Sq, Hq, D] q_dtype, 16-byte aligned
+ *   k_bounds [num_blocks, num_kv_heads, 2, head_dim] q_dtype, 16-byte aligned
+ *   scores   fp32 [B, Sq, Hkv, max_blocks_per_seq], written whole
+ *   flags    NULL, or a device int32: PA_FLAG_BAD_LENGTHS (that sequence scores -inf),
+ *            PA_FLAG_BAD_BLOCK_ID (that page scores -inf)
+ * Reads cfg's sizes, q_dtype, causal and sm_scale.  PA_ERR_UNSUPPORTED for more than 128 query
+ * heads a kv head, batch or num_kv_heads above 65535, and what the decode does not take. */
+PA_API pa_status pa_score_blocks(const pa_config *cfg, const void *q, const void *k_bounds,
+                                 const int32_t *block_tables, const int32_t *context_lens,
+                                 const int32_t *q_lens, float *scores, int32_t *flags,
+                                 pa_stream stream);
+
+/* The best pages of each row, in ascending order.
+ *
+ * Row (b, i, g) sees N = ceil(L / block_size) pages and gets min(top_k, N) of them: first the
+ * pages below num_first and the last num_last of the N (num_first + num_last <= top_k), then
+ * those with the highest scores; NaN ranks above every number, +0 and -0 are equal, and of
+ * equal scores the lower page wins.
+ *   scores        fp32 [B, Sq, Hkv, max_blocks_per_seq]; pages at and past N are not read
+ *   selected      int32 [B, Sq, Hkv, top_k], written whole: the pages, ascending, then -1
+ *   num_selected  int32 [B, Sq, Hkv]: min(top_k, N); 0 for rows i >= q_lens[b]
+ *   flags         NULL, or a device int32: PA_FLAG_BAD_LENGTHS (that sequence selects nothing)
+ * Reads cfg's batch, max_q_len, num_kv_heads, block_size, max_blocks_per_seq and causal. */
+PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
+                                  const int32_t *context_lens, const int32_t *q_lens,
+                                  int32_t top_k, int32_t num_first, int32_t num_last,
+                                  int32_t *selected, int32_t *num_selected, int32_t *flags,
+                                  pa_stream stream);
 
 /* A static, human-readable name of a status. */
 PA_API const char *pa_status_string(pa_status status);

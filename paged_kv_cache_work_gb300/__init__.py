@@ -16,7 +16,7 @@ from typing import Optional
 
 __all__ = ["PaConfig", "PaError", "load", "workspace_size", "plan", "decode", "reduce",
            "decode_step_static", "STATIC_SCRATCH_BYTES", "append_kv", "gather_kv",
-           "build_tables",
+           "build_tables", "update_bounds", "score_blocks", "select_blocks",
            "read_flags", "status_string", "config_for", "paged_attention", "LIB_PATH",
            "BF16", "FP16", "FP8_E4M3", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
            "SCALE_PER_BLOCK",
@@ -39,7 +39,7 @@ MERGE_AUTO, MERGE_IN_DECODE, MERGE_IN_REDUCE = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("pa_workspace_size", "pa_plan", "pa_decode", "pa_reduce", "pa_read_flags",
                     "pa_status_string", "pa_decode_step_static", "pa_gather_kv", "pa_append_kv",
-                    "pa_build_tables")
+                    "pa_build_tables", "pa_update_bounds", "pa_score_blocks", "pa_select_blocks")
 
 # Bytes of the device array behind pa_decode_step_static (PA_STATIC_SCRATCH_BYTES).
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -88,6 +88,13 @@ def load(path: str = LIB_PATH):
     L.pa_append_kv.restype = ctypes.c_int
     L.pa_build_tables.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.pa_build_tables.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    L.pa_update_bounds.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp]
+    L.pa_update_bounds.restype = ctypes.c_int
+    L.pa_score_blocks.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.pa_score_blocks.restype = ctypes.c_int
+    L.pa_select_blocks.argtypes = [cfgp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    L.pa_select_blocks.restype = ctypes.c_int
     L.pa_status_string.argtypes = [ctypes.c_int]
     L.pa_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -232,6 +239,53 @@ def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables,
         _dense(name, cfg.num_blocks, free_blocks, i32), _dense(name, 1, free_count, i32),
         _dense(name, B, new_held, i32), _dense(name, 1, new_free_count, i32),
         _dense(name, B * cfg.max_q_len, slot_map, i64, True), _dense(name, 1, flags, i32, True),
+        _stream(stream)))
+
+
+def update_bounds(cfg: PaConfig, k_new, block_tables, context_lens, q_lens, k_bounds, flags=None,
+                  stream=None):
+    """Widen the channel bounds k_bounds [num_blocks, Hkv, 2, D] of the pages that a step's new K
+    rows go to (see pa_update_bounds in pa.h); a page whose first slot is new starts afresh."""
+    i32, _, _, kinds = _types()
+    name, B, row = "pa_update_bounds", cfg.batch, cfg.num_kv_heads * cfg.head_dim
+    kind = kinds.get(cfg.q_dtype, ())
+    _check(name, load().pa_update_bounds(
+        ctypes.byref(cfg), _dense(name, B * cfg.max_q_len * row, k_new, kind),
+        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
+        _dense(name, cfg.num_blocks * row * 2, k_bounds, kind), _dense(name, 1, flags, i32, True),
+        _stream(stream)))
+
+
+def score_blocks(cfg: PaConfig, q, k_bounds, block_tables, context_lens, q_lens, scores,
+                 flags=None, stream=None):
+    """Upper bounds of the logits of every page for each new-token row and kv head, into scores
+    [B, Sq, Hkv, max_blocks_per_seq]; -inf for pages the row does not see (see pa_score_blocks in
+    pa.h)."""
+    i32, _, f32, kinds = _types()
+    name, B, rows = "pa_score_blocks", cfg.batch, cfg.batch * cfg.max_q_len
+    kind = kinds.get(cfg.q_dtype, ())
+    _check(name, load().pa_score_blocks(
+        ctypes.byref(cfg), _dense(name, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
+        _dense(name, cfg.num_blocks * cfg.num_kv_heads * 2 * cfg.head_dim, k_bounds, kind),
+        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
+        _dense(name, rows * cfg.num_kv_heads * cfg.max_blocks_per_seq, scores, f32),
+        _dense(name, 1, flags, i32, True), _stream(stream)))
+
+
+def select_blocks(cfg: PaConfig, scores, context_lens, q_lens, num_first: int, num_last: int,
+                  selected, num_selected, flags=None, stream=None):
+    """The best selected.shape[-1] pages of each row, ascending, the first num_first and the last
+    num_last always among them (see pa_select_blocks in pa.h)."""
+    i32, _, f32, _ = _types()
+    name, B = "pa_select_blocks", cfg.batch
+    rows, top_k = B * cfg.max_q_len * cfg.num_kv_heads, selected.shape[-1]
+    _check(name, load().pa_select_blocks(
+        ctypes.byref(cfg), _dense(name, rows * cfg.max_blocks_per_seq, scores, f32),
+        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32), top_k, int(num_first),
+        int(num_last), _dense(name, rows * top_k, selected, i32),
+        _dense(name, rows, num_selected, i32), _dense(name, 1, flags, i32, True),
         _stream(stream)))
 
 

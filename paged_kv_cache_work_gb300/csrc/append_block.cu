@@ -28,47 +28,14 @@ constexpr int kKeep = 4;  // 16-byte pieces of new rows a thread keeps in regist
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
 
 struct AppendBlockParams {
+  TouchParams t;
   const char* k_new;
   const char* v_new;
-  const int32_t* bt;
-  const int32_t* ctx;
-  const int32_t* qlens;
   char* k_cache;
   char* v_cache;
   float* k_scale;
   float* v_scale;
-  int32_t* flags;
-  int Sq, Hkv, bs, bs_shift, maxb, nblocks;
-  FastDiv head_div, page_div;  // by Hkv and by the pages a sequence can touch
 };
-
-// A touched page: the new rows [i0, i0 + rows) of sequence b go to slots [slot0, slot0 + rows)
-// of block blk.  False when there is none (or it is flagged).
-struct TouchedPage {
-  int i0, rows, slot0, blk;
-};
-__device__ __forceinline__ bool touched_page(const AppendBlockParams& p, int b, int j,
-                                             bool reports, TouchedPage* t) {
-  const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
-  const long long cap = (long long)p.maxb << p.bs_shift;
-  if (ql < 0 || ql > p.Sq || n < ql || (long long)n > cap) {
-    if (reports && j == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
-    return false;
-  }
-  const int first = n - ql, page = (first >> p.bs_shift) + j;
-  const long long start = (long long)page << p.bs_shift;
-  if (ql == 0 || start >= n) return false;
-  const int lo = max((int)start, first), hi = (int)min(start + p.bs, (long long)n);
-  t->i0 = lo - first;
-  t->rows = hi - lo;
-  t->slot0 = lo - (int)start;
-  t->blk = __ldg(p.bt + (size_t)b * p.maxb + page);
-  if (t->blk < 0 || t->blk >= p.nblocks) {
-    if (reports && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
-    return false;
-  }
-  return true;
-}
 
 template <int QK>
 __device__ __forceinline__ float2 pair_to_f2(uint32_t w) {
@@ -92,19 +59,19 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
   uint32_t u = blockIdx.x;
   const bool is_v = u & 1;
   u >>= 1;
-  const uint32_t bj = p.head_div.div(u);
-  const int g = (int)(u - bj * p.Hkv);
-  const int b = (int)p.page_div.div(bj), j = (int)p.page_div.mod(bj);
+  const uint32_t bj = p.t.head_div.div(u);
+  const int g = (int)(u - bj * p.t.Hkv);
+  const int b = (int)p.t.page_div.div(bj), j = (int)p.t.page_div.mod(bj);
   grid_dependency_wait();
   TouchedPage t;
-  if (!touched_page(p, b, j, tid == 0 && !is_v, &t)) return;
-  const size_t page_head = (size_t)t.blk * p.Hkv + g;
+  if (!touched_page(p.t, b, j, tid == 0 && !is_v, &t)) return;
+  const size_t page_head = (size_t)t.blk * p.t.Hkv + g;
   float* scale = (is_v ? p.v_scale : p.k_scale) + page_head;
   const bool fresh = t.slot0 == 0;
   const float s_old = fresh ? 0.f : *scale;
-  const size_t row_stride = (size_t)p.Hkv * D;  // elements between a head's rows (new and cached)
+  const size_t row_stride = (size_t)p.t.Hkv * D;  // elements between a head's rows (new and cached)
   const uint4* src = reinterpret_cast<const uint4*>(
-      (is_v ? p.v_new : p.k_new) + (((size_t)b * p.Sq + t.i0) * row_stride + (size_t)g * D) * 2);
+      (is_v ? p.v_new : p.k_new) + (((size_t)b * p.t.Sq + t.i0) * row_stride + (size_t)g * D) * 2);
   auto piece = [&](int e) {  // piece e of the page's new rows
     return __ldg(src + (size_t)(e / PPR) * (row_stride / 8) + e % PPR);
   };
@@ -143,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
 
   // ---- the older codes under the larger scale
   char* cache = (is_v ? p.v_cache : p.k_cache) +
-                ((size_t)t.blk * p.bs) * row_stride + (size_t)g * D;  // slot 0, this head
+                ((size_t)t.blk * p.t.bs) * row_stride + (size_t)g * D;  // slot 0, this head
   if (grown) {
     for (int e = tid; e < t.slot0 * PPR; e += kThreads) {
       uint2* at = reinterpret_cast<uint2*>(cache + (size_t)(e / PPR) * row_stride + (e % PPR) * 8);
@@ -187,30 +154,6 @@ cudaError_t launch(K kernel, const AppendBlockParams& p, uint32_t grid, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// The pages a sequence can touch with Sq new rows: they start anywhere in a page.
-long long pages_touched(const pa_config& c) {
-  return ((long long)c.max_q_len + c.block_size - 2) / c.block_size + 1;
-}
-
-AppendBlockParams block_params(const pa_config& c, const int32_t* block_tables,
-                               const int32_t* context_lens, const int32_t* q_lens,
-                               int32_t* flags) {
-  AppendBlockParams p{};
-  p.bt = block_tables;
-  p.ctx = context_lens;
-  p.qlens = q_lens;
-  p.flags = flags;
-  p.Sq = c.max_q_len;
-  p.Hkv = c.num_kv_heads;
-  p.bs = c.block_size;
-  p.bs_shift = ilog2((uint32_t)c.block_size);
-  p.maxb = c.max_blocks_per_seq;
-  p.nblocks = c.num_blocks;
-  p.head_div = FastDiv((uint32_t)c.num_kv_heads);
-  p.page_div = FastDiv((uint32_t)pages_touched(c));
-  return p;
-}
-
 }  // namespace
 
 pa_status append_block(const pa_config& c, const void* k_new, const void* v_new,
@@ -219,7 +162,8 @@ pa_status append_block(const pa_config& c, const void* k_new, const void* v_new,
                        float* v_scale, int32_t* flags, cudaStream_t s) {
   const double ctas = 2.0 * c.batch * (double)pages_touched(c) * c.num_kv_heads;
   if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  AppendBlockParams p = block_params(c, block_tables, context_lens, q_lens, flags);
+  AppendBlockParams p{};
+  p.t = touch_params(c, block_tables, context_lens, q_lens, flags);
   p.k_new = static_cast<const char*>(k_new);
   p.v_new = static_cast<const char*>(v_new);
   p.k_cache = static_cast<char*>(k_cache);
