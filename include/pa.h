@@ -49,7 +49,8 @@
  * the HSTU paged attention), with the same calling convention.  pa_build_tables grows and
  * shrinks block tables from the requests' lengths.  A step that attends over a part of its
  * cached pages keeps channel bounds of every page's keys (pa_update_bounds), scores the pages
- * with them (pa_score_blocks) and selects pages by score (pa_select_blocks).
+ * with them (pa_score_blocks), selects pages by score (pa_select_blocks) and attends over the
+ * selected ones (pa_decode_selected).
  */
 #ifndef PA_H_
 #define PA_H_
@@ -110,6 +111,8 @@ enum {
   PA_FLAG_WAIT_TIMEOUT = 4,  /* a kernel gave up a bounded wait on its own copies */
   PA_FLAG_STALE_PLAN = 8,    /* pa_decode read lengths other than those pa_plan planned for
                                 (they changed between the two calls); outputs unspecified */
+  PA_FLAG_BAD_SELECTION = 16, /* pa_decode_selected: a page count outside [0, top_k] or a listed
+                                page outside the sequence */
   PA_FLAG_NO_FREE_BLOCKS = 32, /* pa_build_tables: fewer free pages than the lengths need */
   PA_FLAG_BAD_FREE_LIST = 64 /* pa_build_tables: a held or free page count that cannot be */
 };
@@ -340,7 +343,7 @@ PA_API pa_status pa_build_tables(const pa_config *cfg, const int32_t *context_le
                                  pa_stream stream);
 
 /* Channel bounds of a page's keys, kept as keys are appended.  (The pages cited above have no
- * counterpart of this call and the two below.)
+ * counterpart of this call and the three below.)
  *
  * k_bounds [num_blocks, num_kv_heads, 2, head_dim] in q_dtype holds, for each page and kv head,
  * the least ([.., 0, :]) and the largest ([.., 1, :]) value of each channel over the page's keys
@@ -390,6 +393,30 @@ PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
                                   int32_t top_k, int32_t num_first, int32_t num_last,
                                   int32_t *selected, int32_t *num_selected, int32_t *flags,
                                   pa_stream stream);
+
+/* Attention of each row over its listed pages only.
+ *
+ * Row i of sequence b and the heads of kv head g attend over the keys of the logical pages
+ * selected[b][i][g][0 .. num_selected[b][i][g]) that lie below L (the keys the row sees, as for
+ * the decode): out and lse as for pa_decode with the softmax over those keys alone; a row with
+ * none gets out = 0, lse = -inf.  The list may be in any order; a page listed twice counts
+ * twice.  Any cache, scale mode and head grouping that pa_decode takes.
+ *   selected      int32 [B, Sq, Hkv, top_k] logical pages (columns of block_tables)
+ *   num_selected  int32 [B, Sq, Hkv]
+ *   lse           [B, Sq, Hq] fp32 or NULL
+ *   flags         NULL, or a device int32: PA_FLAG_BAD_LENGTHS (that sequence's rows get out = 0,
+ *                 lse = -inf), PA_FLAG_BAD_SELECTION (a count outside [0, top_k] is clamped, a
+ *                 page outside the sequence's is skipped), PA_FLAG_BAD_BLOCK_ID (a listed page
+ *                 whose block lies outside [0, num_blocks) is skipped)
+ * One launch, no workspace; the split of a row's pages depends on the sizes alone, so equal
+ * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used. */
+PA_API pa_status pa_decode_selected(const pa_config *cfg, const void *q, const void *k_cache,
+                                    const void *v_cache, const float *k_scale,
+                                    const float *v_scale, const int32_t *block_tables,
+                                    const int32_t *context_lens, const int32_t *q_lens,
+                                    const int32_t *selected, const int32_t *num_selected,
+                                    int32_t top_k, void *out, float *lse, int32_t *flags,
+                                    pa_stream stream);
 
 /* A static, human-readable name of a status. */
 PA_API const char *pa_status_string(pa_status status);

@@ -17,11 +17,12 @@ from typing import Optional
 __all__ = ["PaConfig", "PaError", "load", "workspace_size", "plan", "decode", "reduce",
            "decode_step_static", "STATIC_SCRATCH_BYTES", "append_kv", "gather_kv",
            "build_tables", "update_bounds", "score_blocks", "select_blocks",
+           "decode_selected",
            "read_flags", "status_string", "config_for", "paged_attention", "LIB_PATH",
            "BF16", "FP16", "FP8_E4M3", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
            "SCALE_PER_BLOCK",
            "FLAG_BAD_LENGTHS", "FLAG_BAD_BLOCK_ID", "FLAG_WAIT_TIMEOUT", "FLAG_STALE_PLAN",
-           "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST",
+           "FLAG_BAD_SELECTION", "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST",
            "EXPORTED_SYMBOLS",
            "MERGE_AUTO", "MERGE_IN_DECODE", "MERGE_IN_REDUCE"]
 
@@ -34,12 +35,13 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = rang
 BF16, FP16, FP8_E4M3 = 0, 1, 2
 SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN, SCALE_PER_BLOCK = 0, 1, 2, 3
 FLAG_BAD_LENGTHS, FLAG_BAD_BLOCK_ID, FLAG_WAIT_TIMEOUT, FLAG_STALE_PLAN = 1, 2, 4, 8
-FLAG_NO_FREE_BLOCKS, FLAG_BAD_FREE_LIST = 32, 64
+FLAG_BAD_SELECTION, FLAG_NO_FREE_BLOCKS, FLAG_BAD_FREE_LIST = 16, 32, 64
 MERGE_AUTO, MERGE_IN_DECODE, MERGE_IN_REDUCE = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("pa_workspace_size", "pa_plan", "pa_decode", "pa_reduce", "pa_read_flags",
                     "pa_status_string", "pa_decode_step_static", "pa_gather_kv", "pa_append_kv",
-                    "pa_build_tables", "pa_update_bounds", "pa_score_blocks", "pa_select_blocks")
+                    "pa_build_tables", "pa_update_bounds", "pa_score_blocks", "pa_select_blocks",
+                    "pa_decode_selected")
 
 # Bytes of the device array behind pa_decode_step_static (PA_STATIC_SCRATCH_BYTES).
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -95,6 +97,9 @@ def load(path: str = LIB_PATH):
     L.pa_score_blocks.restype = ctypes.c_int
     L.pa_select_blocks.argtypes = [cfgp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     L.pa_select_blocks.restype = ctypes.c_int
+    L.pa_decode_selected.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
+                                     vp, vp]
+    L.pa_decode_selected.restype = ctypes.c_int
     L.pa_status_string.argtypes = [ctypes.c_int]
     L.pa_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -286,6 +291,32 @@ def select_blocks(cfg: PaConfig, scores, context_lens, q_lens, num_first: int, n
         _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32), top_k, int(num_first),
         int(num_last), _dense(name, rows * top_k, selected, i32),
         _dense(name, rows, num_selected, i32), _dense(name, 1, flags, i32, True),
+        _stream(stream)))
+
+
+def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                    context_lens, q_lens, selected, num_selected, out, lse=None, flags=None,
+                    stream=None):
+    """Attention of each row over its listed pages selected [B, Sq, Hkv, top_k], of which the
+    first num_selected count (see pa_decode_selected in pa.h).  One launch, no workspace."""
+    i32, _, f32, kinds = _types()
+    name, B, Hkv, mode = "pa_decode_selected", cfg.batch, cfg.num_kv_heads, cfg.kv_scale_mode
+    rows, top_k = B * cfg.max_q_len, selected.shape[-1]
+    kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
+    heads = cfg.num_blocks * Hkv
+    cache = heads * cfg.block_size * cfg.head_dim
+    scales = (0, 1, heads * cfg.block_size, heads)[mode] if 0 <= mode <= 3 else 0
+    none = mode == SCALE_NONE
+    _check(name, load().pa_decode_selected(
+        ctypes.byref(cfg), _dense(name, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
+        _dense(name, cache, k_cache, cache_kind), _dense(name, cache, v_cache, cache_kind),
+        _dense(name, scales, k_scale, f32, none), _dense(name, scales, v_scale, f32, none),
+        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
+        _dense(name, rows * Hkv * top_k, selected, i32),
+        _dense(name, rows * Hkv, num_selected, i32), top_k,
+        _dense(name, rows * cfg.num_q_heads * cfg.head_dim, out, kind),
+        _dense(name, rows * cfg.num_q_heads, lse, f32, True), _dense(name, 1, flags, i32, True),
         _stream(stream)))
 
 

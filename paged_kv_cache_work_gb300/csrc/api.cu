@@ -7,7 +7,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "pa_internal.cuh"
+#include "decode_selected.cuh"
 
 using namespace pa;
 
@@ -243,6 +243,80 @@ pa_status pa_reduce(const pa_config* cfg, void* out, float* lse, void* ws, size_
   a.q_kind = cfg->q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
   return launch_reduce(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                 : PA_ERR_CUDA;
+}
+
+pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, const int32_t* context_lens,
+                             const int32_t* q_lens, const int32_t* selected,
+                             const int32_t* num_selected, int32_t top_k, void* out, float* lse,
+                             int32_t* flags, pa_stream stream) {
+  const pa_status st = validate(cfg);
+  if (st != PA_OK) return st;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !q_lens || !selected ||
+      !num_selected || !out || top_k < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(q_lens, 4) ||
+      !aligned(selected, 4) || !aligned(num_selected, 4) || !aligned(lse, 4) || !aligned(flags, 4))
+    return PA_ERR_INVALID_ARG;
+  const pa_config& c = *cfg;
+  const int mode = c.kv_scale_mode;
+  if (mode != PA_SCALE_NONE &&
+      (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
+    return PA_ERR_INVALID_ARG;
+  SelectedParams p;
+  p.q = static_cast<const char*>(q);
+  p.k_cache = static_cast<const char*>(k_cache);
+  p.v_cache = static_cast<const char*>(v_cache);
+  p.k_scale = mode == PA_SCALE_NONE ? nullptr : k_scale;
+  p.v_scale = mode == PA_SCALE_NONE ? nullptr : v_scale;
+  p.bt = block_tables;
+  p.ctx = context_lens;
+  p.qlens = q_lens;
+  p.selected = selected;
+  p.num = num_selected;
+  p.out = out;
+  p.lse = lse;
+  p.flags = flags;
+  const int scales = staged_scales(mode);
+  p.sc_head = scales != SC_NONE ? 1 : 0;
+  p.sc_slot = scales == SC_TOKEN ? c.num_kv_heads : 0;
+  p.sc_block = scales == SC_TOKEN   ? (long long)c.block_size * c.num_kv_heads
+               : scales == SC_BLOCK ? c.num_kv_heads
+                                    : 0;
+  p.Sq = c.max_q_len;
+  p.Hq = c.num_q_heads;
+  p.Hkv = c.num_kv_heads;
+  p.G = c.num_q_heads / c.num_kv_heads;
+  p.RB = ceil_div(p.G, 16);
+  p.bs_shift = ilog2((uint32_t)c.block_size);
+  p.maxb = c.max_blocks_per_seq;
+  p.nblocks = c.num_blocks;
+  p.causal = c.causal;
+  p.top_k = top_k;
+  p.qk_scale = c.sm_scale * kLog2e;
+  const double units_d = (double)c.batch * c.max_q_len * c.num_kv_heads * p.RB;
+  if (units_d * kSelMaxSplit > INT32_MAX ||
+      (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
+  const long long units = (long long)units_d;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const int pages = top_k < c.max_blocks_per_seq ? top_k : c.max_blocks_per_seq;
+  p.split = selected_split(units, (long long)pages * c.block_size, sms);
+  const int kvk = c.kv_dtype == PA_FP8_E4M3 ? KV_FP8 : c.kv_dtype == PA_FP16 ? KV_FP16 : KV_BF16;
+  const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (c.head_dim) {
+    case 64: e = launch_selected_d64(p, kvk, qk, units, s); break;
+    case 128: e = launch_selected_d128(p, kvk, qk, units, s); break;
+    default: e = launch_selected_d256(p, kvk, qk, units, s); break;
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_read_flags(const void* ws, size_t ws_bytes, int32_t* flags, pa_stream stream) {

@@ -419,12 +419,12 @@ __device__ __forceinline__ float fast_log2(float x) {
 // its 11 bits however small the scales are.  A weight is at most 2^8 before its scale, so kPLift
 // = 2^7 more keeps it below f16's 65504 and moves f16's subnormals, where a weight loses bits,
 // down to 2^-21 of the largest.  pow2_above: the least power of two above x >= 0, within
-// [2^-125, 2^125]; pow2_inverse: its exact inverse.
+// [2^-118, 2^125] (so that kPLift times the inverse is finite); pow2_inverse: its exact inverse.
 constexpr float kPLift = 128.f;
-constexpr float kPow2Least = 2.350988701644575e-38f;  // 2^-125
+constexpr float kPow2Least = 3.009265538105056e-36f;  // 2^-118
 __device__ __forceinline__ float pow2_above(float x) {
   const int e = (int)((__float_as_uint(x) >> 23) & 255) + 1;
-  return __uint_as_float((uint32_t)min(max(e, 2), 252) << 23);
+  return __uint_as_float((uint32_t)min(max(e, 9), 252) << 23);
 }
 __device__ __forceinline__ float pow2_inverse(float x) {
   return __uint_as_float((254u << 23) - __float_as_uint(x));
