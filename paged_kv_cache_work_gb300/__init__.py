@@ -118,10 +118,21 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device."""
+    global _current_stream
+    import torch
+    stream = torch.cuda.current_stream().cuda_stream  # (initialises CUDA)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:  # the same handle, without a Stream object: 0.2 us
+        _current_stream = lambda: raw(device())  # noqa: E731  instead of 3 us on the host
+    return stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -203,30 +214,40 @@ def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k
 
 
 _type_cache = None
-_current_device = None
 
 
 def _types():
-    """The torch types of int32, int64 and fp32 arrays and, by pa_dtype, of q and of a cache."""
-    global _type_cache, _current_device
+    """(current device, then the torch types of int32, int64 and fp32 arrays and, by pa_dtype,
+    those of q and of a cache)."""
+    global _type_cache
     if _type_cache is None:
         import torch
-        _current_device = torch.cuda.current_device
-        _type_cache = ((torch.int32,), (torch.int64,), (torch.float32,),
-                       {BF16: (torch.bfloat16,), FP16: (torch.float16,),
-                        FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)})
-    return _type_cache
+        cache = {BF16: (torch.bfloat16,), FP16: (torch.float16,),
+                 FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _type_cache = device, (torch.int32,), (torch.int64,), (torch.float32,), cache
+    device, i32, i64, f32, cache = _type_cache
+    try:
+        return device(), i32, i64, f32, cache
+    except RuntimeError:  # no GPU: no tensor is on the current one
+        return None, i32, i64, f32, cache
 
 
-def _dense(call: str, count: int, t, dtypes, optional: bool = False) -> Optional[int]:
+def _dense(call: str, device: int, count: int, t, dtypes) -> int:
     """Address of a contiguous tensor of at least `count` elements of one of `dtypes` on the
     current GPU (an int address passes as it is); PaError otherwise."""
-    if isinstance(t, int) or (t is None and optional):
-        return t
-    if t is None or t.dtype not in dtypes or t.numel() < count or not t.is_cuda \
-            or not t.is_contiguous() or t.get_device() != _current_device():
-        raise PaError(call, ERR_INVALID_ARG)
-    return t.data_ptr()
+    try:
+        if t.dtype in dtypes and t.numel() >= count and t.is_contiguous() \
+                and t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+    raise PaError(call, ERR_INVALID_ARG)
+
+
+def _maybe(call: str, device: int, count: int, t, dtypes) -> Optional[int]:
+    return None if t is None else _dense(call, device, count, t, dtypes)
 
 
 def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables, free_blocks,
@@ -235,31 +256,31 @@ def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables,
     back into the free stack free_blocks[:free_count], and write the new tokens' slots (see
     pa_build_tables in pa.h).  The held and free counts after the call go to new_held and
     new_free_count, which are the next call's held_blocks and free_count."""
-    i32, i64, _, _ = _types()
+    dev, i32, i64, _, _ = _types()
     name, B = "pa_build_tables", cfg.batch
     _check(name, load().pa_build_tables(
-        ctypes.byref(cfg), _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
-        _dense(name, B, held_blocks, i32),
-        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
-        _dense(name, cfg.num_blocks, free_blocks, i32), _dense(name, 1, free_count, i32),
-        _dense(name, B, new_held, i32), _dense(name, 1, new_free_count, i32),
-        _dense(name, B * cfg.max_q_len, slot_map, i64, True), _dense(name, 1, flags, i32, True),
-        _stream(stream)))
+        ctypes.byref(cfg), _dense(name, dev, B, context_lens, i32),
+        _dense(name, dev, B, q_lens, i32), _dense(name, dev, B, held_blocks, i32),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, cfg.num_blocks, free_blocks, i32), _dense(name, dev, 1, free_count, i32),
+        _dense(name, dev, B, new_held, i32), _dense(name, dev, 1, new_free_count, i32),
+        _maybe(name, dev, B * cfg.max_q_len, slot_map, i64),
+        _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
 def update_bounds(cfg: PaConfig, k_new, block_tables, context_lens, q_lens, k_bounds, flags=None,
                   stream=None):
     """Widen the channel bounds k_bounds [num_blocks, Hkv, 2, D] of the pages that a step's new K
     rows go to (see pa_update_bounds in pa.h); a page whose first slot is new starts afresh."""
-    i32, _, _, kinds = _types()
+    dev, i32, _, _, kinds = _types()
     name, B, row = "pa_update_bounds", cfg.batch, cfg.num_kv_heads * cfg.head_dim
     kind = kinds.get(cfg.q_dtype, ())
     _check(name, load().pa_update_bounds(
-        ctypes.byref(cfg), _dense(name, B * cfg.max_q_len * row, k_new, kind),
-        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
-        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
-        _dense(name, cfg.num_blocks * row * 2, k_bounds, kind), _dense(name, 1, flags, i32, True),
-        _stream(stream)))
+        ctypes.byref(cfg), _dense(name, dev, B * cfg.max_q_len * row, k_new, kind),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
+        _dense(name, dev, cfg.num_blocks * row * 2, k_bounds, kind),
+        _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
 def score_blocks(cfg: PaConfig, q, k_bounds, block_tables, context_lens, q_lens, scores,
@@ -267,30 +288,30 @@ def score_blocks(cfg: PaConfig, q, k_bounds, block_tables, context_lens, q_lens,
     """Upper bounds of the logits of every page for each new-token row and kv head, into scores
     [B, Sq, Hkv, max_blocks_per_seq]; -inf for pages the row does not see (see pa_score_blocks in
     pa.h)."""
-    i32, _, f32, kinds = _types()
+    dev, i32, _, f32, kinds = _types()
     name, B, rows = "pa_score_blocks", cfg.batch, cfg.batch * cfg.max_q_len
     kind = kinds.get(cfg.q_dtype, ())
     _check(name, load().pa_score_blocks(
-        ctypes.byref(cfg), _dense(name, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
-        _dense(name, cfg.num_blocks * cfg.num_kv_heads * 2 * cfg.head_dim, k_bounds, kind),
-        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
-        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
-        _dense(name, rows * cfg.num_kv_heads * cfg.max_blocks_per_seq, scores, f32),
-        _dense(name, 1, flags, i32, True), _stream(stream)))
+        ctypes.byref(cfg), _dense(name, dev, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
+        _dense(name, dev, cfg.num_blocks * cfg.num_kv_heads * 2 * cfg.head_dim, k_bounds, kind),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
+        _dense(name, dev, rows * cfg.num_kv_heads * cfg.max_blocks_per_seq, scores, f32),
+        _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
 def select_blocks(cfg: PaConfig, scores, context_lens, q_lens, num_first: int, num_last: int,
                   selected, num_selected, flags=None, stream=None):
     """The best selected.shape[-1] pages of each row, ascending, the first num_first and the last
     num_last always among them (see pa_select_blocks in pa.h)."""
-    i32, _, f32, _ = _types()
+    dev, i32, _, f32, _ = _types()
     name, B = "pa_select_blocks", cfg.batch
     rows, top_k = B * cfg.max_q_len * cfg.num_kv_heads, selected.shape[-1]
     _check(name, load().pa_select_blocks(
-        ctypes.byref(cfg), _dense(name, rows * cfg.max_blocks_per_seq, scores, f32),
-        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32), top_k, int(num_first),
-        int(num_last), _dense(name, rows * top_k, selected, i32),
-        _dense(name, rows, num_selected, i32), _dense(name, 1, flags, i32, True),
+        ctypes.byref(cfg), _dense(name, dev, rows * cfg.max_blocks_per_seq, scores, f32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32), top_k,
+        int(num_first), int(num_last), _dense(name, dev, rows * top_k, selected, i32),
+        _dense(name, dev, rows, num_selected, i32), _maybe(name, dev, 1, flags, i32),
         _stream(stream)))
 
 
@@ -299,7 +320,7 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
                     stream=None):
     """Attention of each row over its listed pages selected [B, Sq, Hkv, top_k], of which the
     first num_selected count (see pa_decode_selected in pa.h).  One launch, no workspace."""
-    i32, _, f32, kinds = _types()
+    dev, i32, _, f32, kinds = _types()
     name, B, Hkv, mode = "pa_decode_selected", cfg.batch, cfg.num_kv_heads, cfg.kv_scale_mode
     rows, top_k = B * cfg.max_q_len, selected.shape[-1]
     kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
@@ -308,16 +329,18 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
     scales = (0, 1, heads * cfg.block_size, heads)[mode] if 0 <= mode <= 3 else 0
     none = mode == SCALE_NONE
     _check(name, load().pa_decode_selected(
-        ctypes.byref(cfg), _dense(name, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
-        _dense(name, cache, k_cache, cache_kind), _dense(name, cache, v_cache, cache_kind),
-        _dense(name, scales, k_scale, f32, none), _dense(name, scales, v_scale, f32, none),
-        _dense(name, B * cfg.max_blocks_per_seq, block_tables, i32),
-        _dense(name, B, context_lens, i32), _dense(name, B, q_lens, i32),
-        _dense(name, rows * Hkv * top_k, selected, i32),
-        _dense(name, rows * Hkv, num_selected, i32), top_k,
-        _dense(name, rows * cfg.num_q_heads * cfg.head_dim, out, kind),
-        _dense(name, rows * cfg.num_q_heads, lse, f32, True), _dense(name, 1, flags, i32, True),
-        _stream(stream)))
+        ctypes.byref(cfg), _dense(name, dev, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
+        _dense(name, dev, cache, k_cache, cache_kind),
+        _dense(name, dev, cache, v_cache, cache_kind),
+        None if none else _dense(name, dev, scales, k_scale, f32),
+        None if none else _dense(name, dev, scales, v_scale, f32),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
+        _dense(name, dev, rows * Hkv * top_k, selected, i32),
+        _dense(name, dev, rows * Hkv, num_selected, i32), top_k,
+        _dense(name, dev, rows * cfg.num_q_heads * cfg.head_dim, out, kind),
+        _maybe(name, dev, rows * cfg.num_q_heads, lse, f32),
+        _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
 _DT = {"bf16": BF16, "fp16": FP16, "fp8": FP8_E4M3}
