@@ -123,8 +123,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Descriptor of a cache [num_blocks, block_size, Hkv, D] seen as a 4-D tensor (D innermost)
 // with a box of one head's rows of one page.  CUDA-core kernel: {D, 1, rows, 1}, no swizzle.
-// Tensor-core kernel: {128 bytes of D, 1, rows, 1} with the 128-byte swizzle, one box per
-// 128-byte column slab.
+// Tensor-core kernels: {128 bytes of D, 1, rows, 1} with the 128-byte swizzle, one box per
+// 128-byte column slab (64-byte rows: the whole row, with the 64-byte swizzle).
 bool kv_tensor_map(CUtensorMap* m, const void* base, const pa_config& c, int box_rows, bool slabs) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
@@ -137,13 +137,16 @@ bool kv_tensor_map(CUtensorMap* m, const void* base, const pa_config& c, int box
   cuuint64_t strides[3] = {(cuuint64_t)c.head_dim * bpe,
                            (cuuint64_t)c.num_kv_heads * c.head_dim * bpe,
                            (cuuint64_t)c.block_size * c.num_kv_heads * c.head_dim * bpe};
-  const cuuint32_t inner = slabs ? (cuuint32_t)(128 / bpe) : (cuuint32_t)c.head_dim;
+  const bool narrow = c.head_dim * bpe < 128;  // 64-byte rows: one slab of them
+  const cuuint32_t inner = slabs && !narrow ? (cuuint32_t)(128 / bpe) : (cuuint32_t)c.head_dim;
   cuuint32_t box[4] = {inner, 1, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   std::memset(m, 0, sizeof(*m));
   CUresult r = enc(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   slabs ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                   !slabs   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                   : narrow ? CU_TENSOR_MAP_SWIZZLE_64B
+                            : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -266,11 +269,19 @@ pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_
       (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
     return PA_ERR_INVALID_ARG;
   SelectedParams p;
+  const int scales = staged_scales(mode);
+  p.cache.k = static_cast<const char*>(k_cache);
+  p.cache.v = static_cast<const char*>(v_cache);
+  p.cache.k_scale = mode == PA_SCALE_NONE ? nullptr : k_scale;
+  p.cache.v_scale = mode == PA_SCALE_NONE ? nullptr : v_scale;
+  p.cache.sc_head = scales != SC_NONE ? 1 : 0;
+  p.cache.sc_slot = scales == SC_TOKEN ? c.num_kv_heads : 0;
+  p.cache.sc_block = scales == SC_TOKEN   ? (long long)c.block_size * c.num_kv_heads
+                     : scales == SC_BLOCK ? c.num_kv_heads
+                                          : 0;
+  p.cache.Hkv = c.num_kv_heads;
+  p.cache.bs_shift = ilog2((uint32_t)c.block_size);
   p.q = static_cast<const char*>(q);
-  p.k_cache = static_cast<const char*>(k_cache);
-  p.v_cache = static_cast<const char*>(v_cache);
-  p.k_scale = mode == PA_SCALE_NONE ? nullptr : k_scale;
-  p.v_scale = mode == PA_SCALE_NONE ? nullptr : v_scale;
   p.bt = block_tables;
   p.ctx = context_lens;
   p.qlens = q_lens;
@@ -279,18 +290,11 @@ pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_
   p.out = out;
   p.lse = lse;
   p.flags = flags;
-  const int scales = staged_scales(mode);
-  p.sc_head = scales != SC_NONE ? 1 : 0;
-  p.sc_slot = scales == SC_TOKEN ? c.num_kv_heads : 0;
-  p.sc_block = scales == SC_TOKEN   ? (long long)c.block_size * c.num_kv_heads
-               : scales == SC_BLOCK ? c.num_kv_heads
-                                    : 0;
   p.Sq = c.max_q_len;
   p.Hq = c.num_q_heads;
   p.Hkv = c.num_kv_heads;
   p.G = c.num_q_heads / c.num_kv_heads;
   p.RB = ceil_div(p.G, 16);
-  p.bs_shift = ilog2((uint32_t)c.block_size);
   p.maxb = c.max_blocks_per_seq;
   p.nblocks = c.num_blocks;
   p.causal = c.causal;
@@ -300,21 +304,27 @@ pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_
   if (units_d * kSelMaxSplit > INT32_MAX ||
       (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
-  const long long units = (long long)units_d;
-  int dev = 0, sms = 0;
+  SelectedKind k;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      cudaDeviceGetAttribute(&k.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ERR_CUDA;
   const int pages = top_k < c.max_blocks_per_seq ? top_k : c.max_blocks_per_seq;
-  p.split = selected_split(units, (long long)pages * c.block_size, sms);
-  const int kvk = c.kv_dtype == PA_FP8_E4M3 ? KV_FP8 : c.kv_dtype == PA_FP16 ? KV_FP16 : KV_BF16;
-  const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
+  k.units = (long long)units_d;
+  k.tokens = (long long)pages * c.block_size;
+  k.kvk = c.kv_dtype == PA_FP8_E4M3 ? KV_FP8 : c.kv_dtype == PA_FP16 ? KV_FP16 : KV_BF16;
+  k.qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
+  k.toks = scales == SC_TOKEN;
+  CUtensorMap kmap{}, vmap{};
+  if (k.kvk == KV_FP8 && (!kv_tensor_map(&kmap, k_cache, c, 16, true) ||
+                          !kv_tensor_map(&vmap, v_cache, c, 16, true)))
+    return PA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (c.head_dim) {
-    case 64: e = launch_selected_d64(p, kvk, qk, units, s); break;
-    case 128: e = launch_selected_d128(p, kvk, qk, units, s); break;
-    default: e = launch_selected_d256(p, kvk, qk, units, s); break;
+    case 64: e = launch_selected_d64(p, k, kmap, vmap, s); break;
+    case 128: e = launch_selected_d128(p, k, kmap, vmap, s); break;
+    default: e = launch_selected_d256(p, k, kmap, vmap, s); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

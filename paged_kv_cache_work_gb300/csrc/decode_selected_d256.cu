@@ -3,9 +3,9 @@
 
 namespace pa {
 
-cudaError_t launch_selected_d256(const SelectedParams& p, int kvk, int qk, long long units,
-                                cudaStream_t s) {
-  return launch_selected_for_dim<256>(p, kvk, qk, units, s);
+cudaError_t launch_selected_d256(SelectedParams& p, const SelectedKind& k, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, cudaStream_t s) {
+  return launch_selected_for_dim<256>(p, k, kmap, vmap, s);
 }
 
 }  // namespace pa

@@ -103,6 +103,10 @@ CASES = [
 
 # Weights are rounded to the MMA's operand type: bf16 for a bf16 cache (half a step: 2^-8), f16 for
 # fp16 and fp8 caches (2^-11).
+def rounding(kv, dtype):
+    return dict(weight_eps=2.0 ** -8 if kv == "16" and dtype == "bf16" else 2.0 ** -11)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,sq,hq,hkv,d,bs,longest,top_k,causal,dtype,kv,mode", CASES)
 def test_matches_64_bits(B, sq, hq, hkv, d, bs, longest, top_k, causal, dtype, kv, mode, cuda_device, pa):
@@ -110,8 +114,7 @@ def test_matches_64_bits(B, sq, hq, hkv, d, bs, longest, top_k, causal, dtype, k
     cfg = config(B, sq, hq, hkv, d, bs, p["maxb"], p["nblocks"], dtype, kv, mode, causal)
     out, lse = run(p, cfg, cuda_device)
     ref, ref_lse, size = reference(p, causal, d, mode)
-    eps = 2.0 ** -8 if kv == "16" and dtype == "bf16" else 2.0 ** -11
-    plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, eps)
+    plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, **rounding(kv, dtype))
     again, lse2 = run(p, cfg, cuda_device)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
     alone, _ = run(p, cfg, cuda_device, lse=False)
@@ -159,8 +162,8 @@ def test_odd_lists(kv, mode, cuda_device, pa):
 
     out, lse = run(p, cfg, cuda_device, pa.FLAG_BAD_SELECTION)
     ref, ref_lse, size = reference(p, 1, 128, mode, within)
-    eps = 2.0 ** -8 if kv == "16" else 2.0 ** -11
-    plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, eps)
+    tol = rounding(kv, "bf16")
+    plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, **tol)
 
     pages = plain64.pages(p["ctx"][0], 16)
     p["num"][0, 1, 0], p["num"][0, 1, 1] = 11, -3
@@ -178,7 +181,7 @@ def test_odd_lists(kv, mode, cuda_device, pa):
     assert listed or kv == "8"
     out, lse = run(bad, cfg, cuda_device, pa.FLAG_BAD_SELECTION | pa.FLAG_BAD_LENGTHS | (pa.FLAG_BAD_BLOCK_ID if listed else 0))
     ref, ref_lse, size = reference(p, 1, 128, mode, lists)
-    plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, eps)
+    plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, **tol)
 
 
 @pytest.mark.gpu
@@ -195,7 +198,7 @@ def test_ranges_that_leave_f16(d, cuda_device, pa):
         out, lse = run(p, cfg, cuda_device)
         ref, ref_lse, size = reference(p, 0, d, "block")
         plain64.check_attention(out.double().cpu() / factor, lse, ref / factor, ref_lse, size / factor, torch.bfloat16,
-                                2.0 ** -11)
+                                **rounding("8", "bf16"))
 
 
 @pytest.mark.gpu
@@ -220,7 +223,7 @@ def test_a_cache_past_32_bits_of_elements(cuda_device, pa):
         cfg = config(B, 1, hq, hkv, d, bs, 4, nblocks, kv=kv, mode=mode)
         out, lse = run(dict(small, kc=kc, vc=vc, ks=ks, vs=vs, bt=np.array([far])), cfg, cuda_device)
         ref, ref_lse, size = reference(small, 0, d, mode)
-        plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, 2.0 ** -8 if kv == "16" else 2.0 ** -11)
+        plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, **rounding(kv, "bf16"))
         del kc, vc
     torch.cuda.empty_cache()
 
@@ -306,7 +309,7 @@ def test_a_whole_sparse_step(kv, cuda_device, pa):
             if mode == "block":
                 p["ks"], p["vs"] = z["ks"].cpu(), z["vs"].cpu()
             ref, ref_lse, size = reference(p, 1, d, mode)
-            plain64.check_attention(z["out"], z["lse"], ref, ref_lse, size, torch.bfloat16, 2.0 ** -8 if kv == "16" else 2.0 ** -11)
+            plain64.check_attention(z["out"], z["lse"], ref, ref_lse, size, torch.bfloat16, **rounding(kv, "bf16"))
     torch.cuda.current_stream().wait_stream(stream)
 
 
