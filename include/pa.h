@@ -162,12 +162,14 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  *   lse      [B, Sq, Hq] fp32 natural-log LSE, or NULL
  * The tables and lengths must be the ones given to pa_plan, with the same contents.  A CTA
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
- * fp8 cache) derives its first work item from the lengths (the planner's rules) and starts
- * on it while the planner may still be running; it waits for the planner before the rest of
- * its list and before writing anything, and raises PA_FLAG_STALE_PLAN if the planner's first
- * item differs.  The other decode kernels wait for the planner first.
+ * fp8 cache) and of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
+ * query rows per kv head at head dim 128, up to 16 at 256) derives its first work item from the
+ * lengths (the planner's rules) and starts on it while the planner may still be running; it
+ * waits for the planner before the rest of its list and before writing anything, and raises
+ * PA_FLAG_STALE_PLAN if the planner's first item differs.  The other decode kernels wait for the
+ * planner first.
  * The kernels launch with programmatic dependent launch, so pa_decode reads q, the caches,
- * the tables and the lengths once the launch before it in the stream has let its dependents
+ * the scales, the tables and the lengths once the launch before it in the stream has let its dependents
  * start (a pa_plan call does so after its own wait on the launch before it): a kernel between
  * pa_plan and pa_decode that writes any of them must not let its dependents start early.
  * A decode that completed leaves the merge counters as pa_plan set them, so pa_decode may

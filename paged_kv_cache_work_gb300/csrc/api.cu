@@ -199,7 +199,7 @@ pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, co
   }
   if ((st = check_ws(ws, ws_bytes, L)) != PA_OK) return st;
 
-  const int box_rows = cfg->block_size < v.tt ? cfg->block_size : v.tt;
+  const int box_rows = v.path == 3 ? 16 : cfg->block_size < v.tt ? cfg->block_size : v.tt;
   CUtensorMap kmap, vmap;
   if (!kv_tensor_map(&kmap, k_cache, *cfg, box_rows, v.path >= 1) ||
       !kv_tensor_map(&vmap, v_cache, *cfg, box_rows, v.path >= 1))

@@ -9,6 +9,12 @@
 // 448 s), so it cannot wipe out its neighbours.  All of a page's new rows of one call are taken
 // together: the order of rows does not enter.
 //
+// The quotient.  x / s is the correctly rounded one, by Markstein's correction (P. Markstein, IBM
+// J. Res. Dev. 34, 1990): with r = RN(1 / s) and q = RN(x r), q + r (x - q s), the remainder and
+// the sum each one fused multiply-add, is RN(x / s) while the remainder is exact, which it is for
+// every q that E4M3 does not round to zero when s >= 2^-90 (other scales divide).  An infinite q
+// (an infinite x) is left as it is.
+//
 // One CTA per (sequence, touched page, kv head, K or V): nobody else writes that page's codes of
 // that head or its scale, so there is nothing to join.  A thread keeps up to kKeep 16-byte pieces
 // of the new rows in registers between the pass for a and the pass for the codes; only pages
@@ -64,21 +70,28 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
   const int b = (int)p.t.page_div.div(bj), j = (int)p.t.page_div.mod(bj);
   grid_dependency_wait();
   TouchedPage t;
-  if (!touched_page(p.t, b, j, tid == 0 && !is_v, &t)) return;
-  const size_t page_head = (size_t)t.blk * p.t.Hkv + g;
-  float* scale = (is_v ? p.v_scale : p.k_scale) + page_head;
-  const bool fresh = t.slot0 == 0;
-  const float s_old = fresh ? 0.f : *scale;
+  if (!touched_page(p.t, b, j, tid == 0 && !is_v && g == 0, &t)) return;
+  // the new rows are on their way while the block table and the old scale are looked up
   const size_t row_stride = (size_t)p.t.Hkv * D;  // elements between a head's rows (new and cached)
   const uint4* src = reinterpret_cast<const uint4*>(
       (is_v ? p.v_new : p.k_new) + (((size_t)b * p.t.Sq + t.i0) * row_stride + (size_t)g * D) * 2);
   auto piece = [&](int e) {  // piece e of the page's new rows
     return __ldg(src + (size_t)(e / PPR) * (row_stride / 8) + e % PPR);
   };
-
-  // ---- largest finite magnitude of the page's new rows
   const int pieces = t.rows * PPR;
   uint4 keep[kKeep];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int e = tid + k * kThreads;
+    keep[k] = e < pieces ? piece(e) : make_uint4(0, 0, 0, 0);
+  }
+  const int blk = touched_block(p.t, b, t, tid == 0 && !is_v);
+  if (blk < 0) return;
+  float* scale = (is_v ? p.v_scale : p.k_scale) + (size_t)blk * p.t.Hkv + g;
+  const bool fresh = t.slot0 == 0;
+  const float s_old = fresh ? 0.f : *scale;
+
+  // ---- largest finite magnitude of the page's new rows
   float a = 0.f;
   auto amax_of = [&](const uint4& w) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
@@ -88,11 +101,6 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
       a = finite_amax(finite_amax(a, f.x), f.y);
     }
   };
-#pragma unroll
-  for (int k = 0; k < kKeep; ++k) {
-    const int e = tid + k * kThreads;
-    keep[k] = e < pieces ? piece(e) : make_uint4(0, 0, 0, 0);
-  }
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) amax_of(keep[k]);
   for (int e = tid + kKeep * kThreads; e < pieces; e += kThreads) amax_of(piece(e));
@@ -110,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
 
   // ---- the older codes under the larger scale
   char* cache = (is_v ? p.v_cache : p.k_cache) +
-                ((size_t)t.blk * p.t.bs) * row_stride + (size_t)g * D;  // slot 0, this head
+                ((size_t)blk * p.t.bs) * row_stride + (size_t)g * D;  // slot 0, this head
   if (grown) {
     for (int e = tid; e < t.slot0 * PPR; e += kThreads) {
       uint2* at = reinterpret_cast<uint2*>(cache + (size_t)(e / PPR) * row_stride + (e % PPR) * 8);
@@ -121,13 +129,20 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
     }
   }
   // ---- the new codes
+  const float r = __frcp_rn(s);
+  const bool exact = s >= 0x1p-90f;
+  auto over = [&](float x) {
+    const float q = x * r;
+    const float c = __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    return !exact ? __fdiv_rn(x, s) : fabsf(q) > 1024.f ? q : c;
+  };
   auto put = [&](int e, const uint4& v) {
     const uint32_t h[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = pair_to_f2<QK>(h[k]);
-      c[k] = e4m3x2_rn_sat(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+      c[k] = e4m3x2_rn_sat(over(f.x), over(f.y));
     }
     *reinterpret_cast<uint2*>(cache + (size_t)(t.slot0 + e / PPR) * row_stride + (e % PPR) * 8) =
         make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));

@@ -51,32 +51,36 @@ inline TouchParams touch_params(const pa_config& c, const int32_t* block_tables,
 
 #if defined(__CUDACC__)
 
-// A touched page: the new rows [i0, i0 + rows) of sequence b go to slots [slot0, slot0 + rows)
-// of block blk.  False when there is none (or it is flagged).
+// A touched page: the new rows [i0, i0 + rows) of sequence b go to slots [slot0, slot0 + rows) of
+// its logical page `page`.  False when there is none (or the lengths are flagged).
 struct TouchedPage {
-  int i0, rows, slot0, blk;
+  int i0, rows, slot0, page;
 };
-__device__ __forceinline__ bool touched_page(const TouchParams& p, int b, int j,
-                                             bool reports, TouchedPage* t) {
+__device__ __forceinline__ bool touched_page(const TouchParams& p, int b, int j, bool reports,
+                                             TouchedPage* t) {
   const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
   const long long cap = (long long)p.maxb << p.bs_shift;
   if (ql < 0 || ql > p.Sq || n < ql || (long long)n > cap) {
     if (reports && j == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
     return false;
   }
-  const int first = n - ql, page = (first >> p.bs_shift) + j;
-  const long long start = (long long)page << p.bs_shift;
+  const int first = n - ql;
+  t->page = (first >> p.bs_shift) + j;
+  const long long start = (long long)t->page << p.bs_shift;
   if (ql == 0 || start >= n) return false;
   const int lo = max((int)start, first), hi = (int)min(start + p.bs, (long long)n);
   t->i0 = lo - first;
   t->rows = hi - lo;
   t->slot0 = lo - (int)start;
-  t->blk = __ldg(p.bt + (size_t)b * p.maxb + page);
-  if (t->blk < 0 || t->blk >= p.nblocks) {
-    if (reports && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
-    return false;
-  }
   return true;
+}
+// Its block, -1 (and flagged) for one outside the pool.
+__device__ __forceinline__ int touched_block(const TouchParams& p, int b, const TouchedPage& t,
+                                             bool reports) {
+  const int blk = __ldg(p.bt + (size_t)b * p.maxb + t.page);
+  if (blk >= 0 && blk < p.nblocks) return blk;
+  if (reports && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
+  return -1;
 }
 
 // Two fp32 values to two E4M3 codes (lo -> low byte): round to nearest even, saturating.

@@ -107,11 +107,10 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
   const int b = (int)p.t.page_div.div(bj), j = (int)p.t.page_div.mod(bj);
   grid_dependency_wait();
   TouchedPage t;
-  if (!touched_page(p.t, b, j, tid == 0, &t)) return;
+  if (!touched_page(p.t, b, j, tid == 0 && g == 0, &t)) return;
   const size_t row_stride = (size_t)p.t.Hkv * D;
   const uint4* src = reinterpret_cast<const uint4*>(
                          p.k_new + (((size_t)b * p.t.Sq + t.i0) * row_stride + (size_t)g * D) * 2) + c;
-  uint4* out = reinterpret_cast<uint4*>(p.bounds + ((size_t)t.blk * p.t.Hkv + g) * 2 * D * 2) + c;
   uint4 lo, hi;
   if (rg < t.rows) {
     lo = hi = __ldg(src + (size_t)rg * (row_stride / 8));
@@ -124,8 +123,10 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
     s_lo[tid] = lo;
     s_hi[tid] = hi;
   }
+  const int blk = rg == 0 ? touched_block(p.t, b, t, tid == 0) : -1;
   __syncthreads();
-  if (rg != 0) return;
+  if (blk < 0) return;
+  uint4* out = reinterpret_cast<uint4*>(p.bounds + ((size_t)blk * p.t.Hkv + g) * 2 * D * 2) + c;
   for (int k = 1; k < min(RG, t.rows); ++k) {
     lo = extreme8<QK, false>(lo, s_lo[k * PPR + c]);
     hi = extreme8<QK, true>(hi, s_hi[k * PPR + c]);

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(T::NTHREADS, SelectedSmem<T>::CTAS_PER_SM)
   uint32_t phase = 0;
   for (int j = 0; j < my; ++j) {
     if constexpr (T::FP8) {
-      if (!mbar_wait_drain(&bar[st], phase)) {  // copies that never came: give up on the rest
+      if (!stream_wait(&bar[st], phase)) {  // copies that never came: give up on the rest
         if (p.flags) atomicOr(p.flags, PA_FLAG_WAIT_TIMEOUT);
         if (j + 1 < my) mbar_wait_drain(&bar[st == 2 ? 0 : st + 1], st == 2 ? phase ^ 1 : phase);
         break;
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(T::NTHREADS, SelectedSmem<T>::CTAS_PER_SM)
     const uint32_t stage = ring_addr + st * T::STAGE;
     if constexpr (T::FP8) {
       const Chunk* cs = reinterpret_cast<const Chunk*>(meta + st * T::META);
-      const Chunk c0 = cs[0], c1 = cs[1];
-      const bool all = c0.rows + c1.rows == 32;
+      const Chunk c0 = cs[0], c1 = cs[SUB - 1];
+      const bool all = c0.rows == 16 && c1.rows == 16;
       if (!all) zero_rows<T>(ring + st * T::STAGE + T::TILE, c0.rows, c1.rows, lane);
       att.tile_fp8(stage, {c0.ks, c1.ks}, {c0.vs, c1.vs},
                    reinterpret_cast<const float*>(meta + st * T::META + 32), all,

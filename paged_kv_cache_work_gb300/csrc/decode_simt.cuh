@@ -40,7 +40,7 @@ struct SimtTraits {
   static constexpr int D = D_;
   static constexpr int MP = MP_;
   static constexpr bool TOKS = TOKS_;
-  static constexpr bool BLKS = false;  // a page's one scale is staged for each token
+  static constexpr bool BLKS = false;
   static constexpr int BPE = KVK == KV_FP8 ? 1 : 2;
   static constexpr int LPT0 = cmax(D / 16, 2 * MP);
   static constexpr int LPT = (MP * (D / LPT0) > 64) ? 2 * LPT0 : LPT0;  // lanes per token group

@@ -29,7 +29,7 @@ __host__ __device__ constexpr size_t round_up_sz(size_t a, size_t b) { return (a
 // tiles of `mp` (a power of two); a unit of work is one (sequence, kv head, row
 // tile), and `tt` is the number of tokens staged per pipeline stage.
 struct Variant {
-  int path;         // 0: CUDA-core kernel, 1: mma.sync kernel, 2: tcgen05 kernel
+  int path;         // 0: CUDA-core kernel, 1: mma.sync kernel, 2: tcgen05 kernel, 3: streaming kernel
   int rows;         // M = G * Sq
   int mp;           // rows per unit (padded to a power of two)
   int rb;           // row tiles per kv head
@@ -78,6 +78,7 @@ inline int staged_scales(int mode) {
 // CTAs of the decode instance for these parameters that fit on one SM.
 int simt_ctas_per_sm(int head_dim, int mp, int kvk, bool toks);
 int mma_ctas_per_sm(int head_dim, int mp, int kvk, int scales);
+int stream_ctas_per_sm(int head_dim);
 // Largest row tile of the tensor-core decode kernel.
 constexpr int kMmaMaxRows = 64;
 
@@ -95,6 +96,21 @@ inline int decode_merge_limit(int split_merge, int path) {
   return 1;
 }
 
+// The streaming kernel (an fp8 cache with one scale for each page and kv head): query rows of a
+// tile, the tokens that its warps take in a round, the cost of an item in such rounds (the batched
+// shapes: 3 rounds 45.2 and 41.0 us a step, 6 rounds 43.2 and 40.1, 9 rounds 43.3 and 43.0), and
+// the most rows per kv head it takes.  At head
+// dim 128 two tiles beat one of the mma.sync kernel (24 rows, batched GQA: 62 against 107 us; 32
+// rows, long pages: 65 against 100 us); at 256, where the tiles leave room for one CTA an SM, they
+// do not (32 rows: 95 against 81 us; one tile of 16: 73 against 86 us).  64-dim rows: always (4
+// rows: 50 against 93 us on CUDA cores).
+constexpr int kStreamRows = 16;
+constexpr int stream_round_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
+constexpr int kStreamItemCostRounds = 5;
+constexpr int stream_max_rows(int head_dim) {
+  return head_dim == 64 ? 0x7fffffff : head_dim == 128 ? 32 : 16;
+}
+
 // Query rows per kv head above which a 128-dim head runs on the tcgen05 kernel.
 constexpr int kTcMinRows = 33;
 
@@ -105,7 +121,8 @@ constexpr int kTcMinRows = 33;
 // 128 rows), otherwise on mma.sync with the rows padded to 16, 32 or 64 (larger groups cut
 // into 64-row tiles): even a tile of one real row in sixteen costs less there than
 // CUDA-core arithmetic.  A 64-dim fp8 cache (64-byte rows) runs on the CUDA-core kernel, in
-// tiles of up to 8 rows.
+// tiles of up to 8 rows.  An fp8 cache with one scale for each page runs on the streaming kernel
+// up to stream_max_rows.
 inline Variant make_variant(const pa_config& c) {
   Variant v{};
   v.rows = (c.num_q_heads / c.num_kv_heads) * c.max_q_len;
@@ -114,22 +131,30 @@ inline Variant make_variant(const pa_config& c) {
   if (v.path == 1 && c.head_dim >= 128 && v.rows >= kTcMinRows &&
       (c.kv_dtype != PA_FP8_E4M3 || c.head_dim == 128))
     v.path = 2;
-  if (v.path == 2)
+  if (staged_scales(c.kv_scale_mode) == SC_BLOCK && v.rows <= stream_max_rows(c.head_dim))
+    v.path = 3;
+  if (v.path == 3)
+    v.mp = kStreamRows;
+  else if (v.path == 2)
     v.mp = v.rows <= 64 ? 64 : 128;
   else if (v.path == 1)
     v.mp = v.rows >= kMmaMaxRows ? kMmaMaxRows : (v.rows <= 16 ? 16 : pow2_at_least(v.rows));
   else
     v.mp = v.rows <= kSimtMaxRows ? pow2_at_least(v.rows) : kSimtMaxRows;
   v.rb = ceil_div(v.rows, v.mp);
-  v.tt = v.path == 2 ? kTcStepTokens : kTileBytes / (c.head_dim * v.bpe);
+  v.tt = v.path == 3   ? stream_round_tokens(c.head_dim)
+         : v.path == 2 ? kTcStepTokens
+                       : kTileBytes / (c.head_dim * v.bpe);
   // the item cost is measured in 16 KB tiles of streaming (tcgen05: in steps), rounded up
   // to whole tiles
-  v.item_cost = v.path == 2 ? kTcItemCostSteps * kTcStepTokens
+  v.item_cost = v.path == 3   ? kStreamItemCostRounds * v.tt
+                : v.path == 2 ? kTcItemCostSteps * kTcStepTokens
                             : round_up(kItemCostTiles * (kTileBytes / (c.head_dim * v.bpe)), v.tt);
   v.units = c.batch * c.num_kv_heads * v.rb;
   const int kvk = c.kv_dtype == PA_FP8_E4M3 ? 2 : (c.kv_dtype == PA_FP16 ? 1 : 0);
   const int scales = staged_scales(c.kv_scale_mode);
-  v.ctas_per_sm = v.path == 2   ? 1
+  v.ctas_per_sm = v.path == 3   ? stream_ctas_per_sm(c.head_dim)
+                  : v.path == 2 ? 1
                   : v.path == 1 ? mma_ctas_per_sm(c.head_dim, v.mp, kvk, scales)
                                 : simt_ctas_per_sm(c.head_dim, v.mp, kvk, scales != SC_NONE);
   v.ns_dec = decode_merge_limit(c.split_merge, v.path);

@@ -44,7 +44,7 @@ struct StreamTraits {
   static constexpr int NW = 4;
   static constexpr int NTHREADS = NW * 32;
   static constexpr int ROW = D * BPE;                     // bytes of a row
-  static constexpr int TK = FP8 || ROW <= 128 ? 32 : 16;  // tokens of a warp's tile
+  static constexpr int TK = ROW <= 128 ? 32 : 16;         // tokens of a warp's tile
   static constexpr int SUB = TK / 16;                     // 16-token chunks of a tile
   static constexpr int NST = 3;
   // fp8: a tile is SLABS column slabs of SLABW bytes a row, as the TMA boxes bring them
@@ -53,7 +53,7 @@ struct StreamTraits {
   static constexpr int TILE = TK * ROW;  // bytes of a K (or V) tile
   static constexpr int STAGE = 2 * TILE;
   static constexpr int RING = NW * NST * STAGE;
-  // fp8: what a stage's chunks are (Chunk, two of 16 bytes), or its tokens' scales (K, then V)
+  // fp8: what a stage's chunks are (up to two Chunks), and its tokens' scales (K, then V)
   static constexpr int META = !FP8 ? 0 : 32 + (TOKS ? 2 * TK * 4 : 0);
   static constexpr int KSTEPS = D / 16;
   static constexpr int NB = D / 8;                // 8-channel blocks of the output
@@ -61,6 +61,21 @@ struct StreamTraits {
   static constexpr int O_SLOT = ROWS * OSTR * 4;  // one staged state's accumulators
   static_assert(FP8 || !TOKS, "scales belong to fp8 caches");
 };
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -78,9 +93,14 @@ __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two 16x16 byte matrices transposed: register r of matrix j holds rows 4 qi .. + 3 of channel
-// quad + 8 r (lanes 16 j + i give the address of its row i).
-__device__ __forceinline__ void ldsm_b8_x2_t(uint32_t addr, uint32_t (&r)[4]) {
+// One or two 16x16 byte matrices transposed: register 2 j + r holds rows 4 qi .. + 3 of channel
+// quad + 8 r of matrix j (lane 16 j + i gives the address of its row i).
+__device__ __forceinline__ void ldsm_b8_t(uint32_t addr, uint32_t (&r)[2]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0, %1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_b8_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
@@ -140,16 +160,16 @@ __device__ __forceinline__ void stream_copy(const CacheView& cv, int g, uint32_t
   }
 }
 
-// fp8: the two chunks of a tile into stage `st` of the warp's ring, completing on its barrier.
-// Lane lane0 + s holds chunk s (its block and Chunk); called by the whole warp.
+// fp8: the chunks of a tile into a stage of the warp's ring, completing on its barrier.  Lane
+// lane0 + s holds chunk s (its block and Chunk); called by the whole warp.
 template <class T>
 __device__ __forceinline__ void stream_tma(const CacheView& cv, const CUtensorMap* kmap,
                                            const CUtensorMap* vmap, int g, char* stage, char* meta,
                                            uint64_t* bar, int blk, const Chunk& ch, int lane0,
                                            int lane) {
-  const bool mine = (lane >> 1) == (lane0 >> 1);
+  const bool mine = lane / T::SUB == lane0 / T::SUB;
   const bool copies = mine && ch.rows > 0;
-  const int s = lane & 1;
+  const int s = lane % T::SUB;
   const uint32_t nv = __popc(__ballot_sync(kFull, copies));
   if (lane == 0) mbar_arrive_expect_tx(bar, nv * 2u * 16u * T::ROW);
   __syncwarp();
@@ -164,15 +184,17 @@ __device__ __forceinline__ void stream_tma(const CacheView& cv, const CUtensorMa
   }
   if (mine) *reinterpret_cast<Chunk*>(meta + 16 * s) = ch;  // (its scales may still be on their way)
   if constexpr (T::TOKS) {  // a lane a token
-    const int src = lane0 + (lane >> 4), r = lane & 15;
+    const int src = lane0 + (lane >> 4) % T::SUB, r = lane & 15;
     const int bk = __shfl_sync(kFull, blk, src), sl = __shfl_sync(kFull, slot, src);
     const bool ok = r < __shfl_sync(kFull, ch.rows, src);
     const size_t at = ok ? (size_t)(bk * cv.sc_block) + (size_t)((sl + r) * cv.sc_slot) +
                                (size_t)g * cv.sc_head
                          : 0;
-    const uint32_t to = smem_addr(meta + 32) + lane * 4;
-    cp_async_4_zfill(to, cv.k_scale + at, ok);
-    cp_async_4_zfill(to + T::TK * 4, cv.v_scale + at, ok);
+    const uint32_t to = smem_addr(meta + 32) + lane % T::TK * 4;
+    if (lane < T::TK) {
+      cp_async_4_zfill(to, cv.k_scale + at, ok);
+      cp_async_4_zfill(to + T::TK * 4, cv.v_scale + at, ok);
+    }
     cp_async_arrive_noinc(bar);
   }
 }
@@ -188,6 +210,10 @@ __device__ __forceinline__ void zero_rows(char* vt, int rows0, int rows1, int la
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
+}
+// Bounded wait for a stage's copies (the clock is read only when the first try fails).
+__device__ __forceinline__ bool stream_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || mbar_wait_drain(bar, parity);
 }
 // Arrivals a stage's barrier expects.
 template <class T>
@@ -343,18 +369,19 @@ struct WarpAttention {
   template <class F>
   __device__ __forceinline__ void tile_fp8(uint32_t stage, const float (&ks)[2], const float (&vs)[2],
                                            const float* sc, bool all, F seen, int lane) {
+    constexpr int SUB = T::SUB, TK = T::TK, NT8 = 2 * SUB;
     const uint32_t kt = stage, vt = stage + T::TILE;
     const int mat = lane >> 3, qi = lane & 3, n = lane & 7;
     const int pair[2] = {2 * qi + 4 * (qi & 2), 2 * qi + 4};  // first of a block's two tokens
     // ---- logits: s[2 c + j] block j of chunk c
-    float s[4][4];
+    float s[NT8][4];
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+    for (int nb = 0; nb < NT8; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
     const int krow = mat < 2 ? n + 2 * (n & 4) : n + 4;
 #pragma unroll
     for (int kk = 0; kk < KSTEPS; kk += 2)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < SUB; ++c) {
         uint32_t r[4];  // block 0: k-steps kk, kk + 1; block 1
         ldsm_x4(tile_piece<T>(kt, 16 * c + krow, kk + (mat & 1)), r[0], r[1], r[2], r[3]);
 #pragma unroll
@@ -367,7 +394,7 @@ struct WarpAttention {
       }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < NT8; ++b) {
       const int c = b >> 1, j = b & 1;
       float2 k2;
       if constexpr (T::TOKS)
@@ -376,15 +403,15 @@ struct WarpAttention {
         k2 = make_float2(ks[c], ks[c]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x0 = s[b][2 * h] * (qk[h] * k2.x), x1 = s[b][2 * h + 1] * (qk[h] * k2.y);
+        float2 x = fmul2(make_float2(s[b][2 * h], s[b][2 * h + 1]), make_float2(qk[h] * k2.x, qk[h] * k2.y));
         if (!all) {
           const int lim = seen(c, h);
-          x0 = pair[j] < lim ? x0 : -INFINITY;
-          x1 = pair[j] + 1 < lim ? x1 : -INFINITY;
+          x.x = pair[j] < lim ? x.x : -INFINITY;
+          x.y = pair[j] + 1 < lim ? x.y : -INFINITY;
         }
-        s[b][2 * h] = x0;
-        s[b][2 * h + 1] = x1;
-        mx[h] = fmaxf(mx[h], fmaxf(x0, x1));
+        s[b][2 * h] = x.x;
+        s[b][2 * h + 1] = x.y;
+        mx[h] = fmaxf(mx[h], fmaxf(x.x, x.y));
       }
     }
 #pragma unroll
@@ -395,9 +422,9 @@ struct WarpAttention {
     follow(mx);
     float big;
     if constexpr (T::TOKS)  // (magnitudes order as their bits do)
-      big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(sc[32 + lane]))));
+      big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(sc[TK + lane % TK]))));
     else
-      big = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+      big = fmaxf(fabsf(vs[0]), fabsf(vs[SUB - 1]));
     if (big > vref) {  // warp-uniform
       const float up = pow2_above(big), f = vref * pow2_inverse(up);
       vref = up;
@@ -408,32 +435,39 @@ struct WarpAttention {
     }
     const float vinv = pow2_inverse(vref) * kPLift;
     // ---- weights: a masked logit (-inf) gives 0, also while the row has seen no key
-    const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-    uint32_t pa[2][4];
+    const float base[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t pa[SUB][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < NT8; ++b) {
       const int c = b >> 1, j = b & 1;
       float2 v2;
       if constexpr (T::TOKS)
-        v2 = *reinterpret_cast<const float2*>(sc + 32 + 16 * c + pair[j]);
+        v2 = *reinterpret_cast<const float2*>(sc + TK + 16 * c + pair[j]);
       else
         v2 = make_float2(vs[c], vs[c]);
+      v2 = make_float2(v2.x * vinv, v2.y * vinv);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float p0 = fast_exp2(s[b][2 * h] - base[h]), p1 = fast_exp2(s[b][2 * h + 1] - base[h]);
-        l[h] += p0 + p1;
-        pa[c][2 * j + h] = pack2<true>(p0 * (v2.x * vinv), p1 * (v2.y * vinv));
+        float2 e = fadd2(make_float2(s[b][2 * h], s[b][2 * h + 1]), make_float2(base[h], base[h]));
+        e.x = fast_exp2(e.x);
+        e.y = fast_exp2(e.y);
+        sum[h] = fadd2(sum[h], e);
+        e = fmul2(e, v2);
+        pa[c][2 * j + h] = pack2<true>(e.x, e.y);
       }
     }
+    l[0] += sum[0].x + sum[0].y;
+    l[1] += sum[1].x + sum[1].y;
     // ---- o += P V: row i = 4 qi' + 2 j + e of a chunk's matrix is token e of block j of thread qi'
     const int i = lane & 15, iq = i >> 2;
-    const int vrow = (lane & 16) + ((i & 2) ? 2 * iq + 4 : 2 * iq + 4 * (iq & 2)) + (i & 1);
+    const int vrow = (SUB == 2 ? lane & 16 : 0) + ((i & 2) ? 2 * iq + 4 : 2 * iq + 4 * (iq & 2)) + (i & 1);
 #pragma unroll
     for (int nd = 0; nd < NB / 2; ++nd) {
-      uint32_t r[4];  // chunk 0: channels quad, quad + 8 of the 16; chunk 1
-      ldsm_b8_x2_t(tile_piece<T>(vt, vrow, nd), r);
+      uint32_t r[2 * SUB];  // chunk 0: channels quad, quad + 8 of the 16; chunk 1
+      ldsm_b8_t(tile_piece<T>(vt, vrow, nd), r);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < SUB; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t w = r[2 * c + j];

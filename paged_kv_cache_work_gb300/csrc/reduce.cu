@@ -30,6 +30,8 @@ cudaError_t launch_tc_fp8_d128(const KernelParams&, const CUtensorMap&, const CU
 cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, const CUtensorMap&,
                                      int, int, int, cudaStream_t);
 
+cudaError_t launch_stream(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int, int,
+                          cudaStream_t);
 int mma_ctas_per_sm_d64(int, int, int);
 int mma_ctas_per_sm_d128(int, int, int);
 int mma_ctas_per_sm_d256(int, int, int);
@@ -101,6 +103,8 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CU
   const KernelParams prm = make_kernel_params(a);
   const int scales = staged_scales(a.scale_mode);
   const bool toks = scales != SC_NONE;
+  if (a.v.path == 3)
+    return launch_stream(prm, kmap, vmap, a.v.ctas, a.p.head_dim, a.q_kind, s);
   if (a.v.path == 2) {
     if (a.kv_kind == KV_FP8)
       return a.p.head_dim != 128 ? cudaErrorNotSupported
