@@ -99,6 +99,33 @@ def test_append_matches_the_plain_steps(B, sq, hkv, d, bs, prior, dtype, kind, c
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_quotient_is_the_rounded_one(dtype, cuda_device, pa):
+    """Every finite value of the type over scales of every kind of significand, small ones among
+    them: the codes are those of a division."""
+    dev, rng, bs, d = cuda_device, np.random.default_rng(5), 64, 256
+    kind = KINDS[dtype][0]
+    every = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(kind)
+    every = every[torch.isfinite(every)].float()
+    pages = []
+    for big in (1.0, 3.0, 1e-3, 448.0, 6e4, 1.7e-5, *rng.uniform(0.5, 900.0, 26), *(2.0 ** -np.arange(90.0, 126.0, 4) if dtype == "bf16" else ())):
+        big = float(torch.tensor(big).to(kind))
+        x = every[every.abs() <= big]
+        x = x[torch.from_numpy(rng.permutation(len(x))[:bs * d - 1])]
+        pages.append(torch.nn.functional.pad(torch.cat((x, torch.tensor([big]))), (0, bs * d - 1 - len(x))))
+    n = len(pages)
+    new = torch.stack(pages).reshape(n, bs, 1, d).to(kind)
+    bt = np.arange(n)[:, None]
+    codes, scale = torch.zeros(n, bs, 1, d, dtype=torch.uint8), torch.ones(n, 1)
+    want = plain64.append_block(new, codes, scale, [bs] * n, [bs] * n, bt, bs)
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    got = [codes.to(dev).clone(), codes.to(dev).clone(), scale.to(dev).clone(), scale.to(dev).clone()]
+    pa.append_kv(config(n, bs, 1, 1, d, bs, 1, n, dtype), new.to(dev), new.to(dev), t(bt), t([bs] * n), t([bs] * n), *got)
+    assert torch.equal(got[2].cpu(), want[1]) and torch.equal(got[3].cpu(), want[1])
+    assert same_codes(got[0], want[0]) and same_codes(got[1], want[0])
+
+
+@pytest.mark.gpu
 def test_append_flags_and_skips(cuda_device, pa):
     dev, rng = cuda_device, np.random.default_rng(3)
     B, sq, hkv, d, bs = 4, 20, 2, 128, 16
