@@ -8,15 +8,22 @@
 // k_d <= hi_d) has <q, k> above sum_d max(q_d lo_d, q_d hi_d), and that is one dot product of
 // length 2 D: sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d.  So the scores are a matrix product of
 // the query rows with the pages' bounds, on mma.sync m16n8k16 with fp32 accumulation (products of
-// 16-bit values are exact): 16 query rows by 8 pages.  A quad's four lanes read their page's
-// bounds straight from global memory in 16-byte pieces; with the contraction's order permuted
-// alike on both sides (a lane's 8 channels of a piece are 4 of one k-step and 4 of the next) the
-// pieces are the B fragments as they land, so nothing is staged.  The query rows wait in shared
-// memory in fragment order; a step's max(q, 0) and min(q, 0) are one instruction each.
-// What bounds it is the 4 D bytes of a (page, head).
+// 16-bit values are exact): 16 query rows by 8 pages.  What bounds it is the 4 D bytes of a (page,
+// head), one contiguous piece; what it takes is enough of them in flight (about 100 KB an SM), which
+// registers do not hold.  So each warp streams its pages on its own through a ring of shared-memory
+// stages of 8 pages by 16-byte cp.async, a page a warp instruction at head dim 128, with the blocks
+// of 32 pages looked up at a time (a lane each).  max(q, 0) and min(q, 0) stay in registers as A
+// fragments.  With the contraction's order permuted alike on both sides (a lane's 8 channels of a
+// 16-byte piece are 4 of one k-step and 4 of the next) a page's pieces are the B fragments as a lane
+// reads them.
+//   Measured on 32 contexts of 32,768 to 131,072 tokens in pages of 64 (168 MB, 25.1 us at the copy
+// rate): 31.9 us with 12 warps an SM (8: 32.0, 16: 30.6, 48: 34.4), and 7.5 us on contexts of at
+// most 8,192 in pages of 16, where 16 warps take 8.0 and 48 take 12.0.  Pages read straight into
+// registers by 33, 12 and 8 warps an SM took 38, 41 and 56 us, a 512-byte bulk copy a page 50 us (the
+// copy engine takes about 40 cycles for each, however short).
 //
-// Row tiles hold whole query tokens: 16 / G tokens of G heads for G <= 16 (the rows of a token
-// are then reduced to their maximum through shared memory), or ceil(G / 16) tiles for one token.
+// A row tile holds whole query tokens where a group has 1, 2, 4 or 8 heads (16 / G tokens; a
+// token's maximum is up to three shuffles away); other groups take ceil(G / 16) tiles a token.
 //
 // Select.  One CTA per row: scores become order-preserving 32-bit keys in shared memory, four
 // passes over 8 bits each find the k-th largest key, and one ordered pass writes the pages above
@@ -66,7 +73,7 @@ cudaError_t launch_pdl(void (*kernel)(P), const P& p, dim3 grid, int threads, si
 }
 
 // ---- bounds ------------------------------------------------------------------------------
-constexpr int kBoundsThreads = 256;
+constexpr int kBoundsThreads = 128;
 
 template <int QK, bool MAX>
 __device__ __forceinline__ uint32_t extreme2(uint32_t x, uint32_t y) {  // NaN wins
@@ -111,14 +118,20 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
   const size_t row_stride = (size_t)p.t.Hkv * D;
   const uint4* src = reinterpret_cast<const uint4*>(
                          p.k_new + (((size_t)b * p.t.Sq + t.i0) * row_stride + (size_t)g * D) * 2) + c;
+  // four rows of each thread at a time, all on their way at once
   uint4 lo, hi;
   if (rg < t.rows) {
     lo = hi = __ldg(src + (size_t)rg * (row_stride / 8));
-#pragma unroll 4
-    for (int r = rg + RG; r < t.rows; r += RG) {
-      const uint4 x = __ldg(src + (size_t)r * (row_stride / 8));
-      lo = extreme8<QK, false>(lo, x);
-      hi = extreme8<QK, true>(hi, x);
+    for (int r0 = rg; r0 < t.rows; r0 += 4 * RG) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = __ldg(src + (size_t)min(r0 + k * RG, t.rows - 1) * (row_stride / 8));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        lo = extreme8<QK, false>(lo, x[k]);
+        hi = extreme8<QK, true>(hi, x[k]);
+      }
     }
     s_lo[tid] = lo;
     s_hi[tid] = hi;
@@ -141,7 +154,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
 
 // ---- score -------------------------------------------------------------------------------
 constexpr int kScoreWarps = 4;
-constexpr int kScoreMaxTiles = 8;  // row tiles whose query rows fit one CTA
+constexpr int kScoreWarpsPerSm = 12;
+constexpr int kScoreMaxGroups = 32;
 
 struct ScoreParams {
   const char* q;
@@ -152,11 +166,13 @@ struct ScoreParams {
   float* scores;
   int32_t* flags;
   int Sq, Hq, Hkv, G, bs_shift, maxb, nblocks, causal;
-  int tpt;         // tokens per row tile (G <= 16), else 0
-  int tiles_tok;   // row tiles per token (G > 16), else 1
-  int toks_cta;    // tokens of one CTA
-  int tok_groups;  // CTAs along the tokens
-  int groups_cta;  // groups of 8 pages each warp takes
+  int tpt;         // tokens of a warp's row tile (G 1, 2, 4 or 8), else 1
+  int g_shift;     // log2(G) then, else -1
+  int parts;       // row tiles per token
+  int tok_groups;  // warps along the tokens
+  int runs;        // warps along the pages
+  int batch;
+  int groups;      // groups of 8 pages of a warp
   float sm_scale;
 };
 
@@ -184,158 +200,193 @@ __device__ __forceinline__ void score_mma(float (&d)[4], const uint32_t (&a)[4],
   }
 }
 
+template <int D>
+struct ScoreSmem {
+  static constexpr int PAGE = 4 * D;       // bytes of a (page, head)
+  static constexpr int STRIDE = PAGE + 64;  // so that two quads read distinct banks
+  static constexpr int STAGE = 8 * STRIDE;
+  static constexpr int NST = D == 64 ? 6 : 3;
+  static constexpr int WARP = NST * STAGE;
+  static constexpr int BYTES = kScoreWarps * WARP;
+  static constexpr int CTAS_PER_SM = D == 256 ? 2 : 3;
+  static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "shared memory");
+};
+
 template <int D, int QK>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const ScoreParams p) {
-  constexpr int NP = D / 32;  // 16-byte pieces a lane holds of each bound: two k-steps each
-  constexpr int KSTEPS = D / 16;
-  // query rows in A fragment order: [tile][k-step][lane] (a0..a3)
-  extern __shared__ uint4 s_q[];
-  __shared__ float s_c[kScoreWarps][16][9];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, qi = lane & 3;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int tg = blockIdx.x % p.tok_groups, pg = blockIdx.x / p.tok_groups;
-  const int tok0 = tg * p.toks_cta, toks = min(p.toks_cta, p.Sq - tok0);
-  const int tiles = p.tpt ? ceil_div(toks, p.tpt) : toks * p.tiles_tok;
+__global__ void __launch_bounds__(kScoreWarps * 32, ScoreSmem<D>::CTAS_PER_SM) score_kernel(const ScoreParams p) {
+  using M = ScoreSmem<D>;
+  constexpr int NP = D / 32;  // 16-byte pieces a lane takes of each bound: two k-steps each
+  extern __shared__ __align__(128) char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qi = lane & 3;
+  char* const ring = smem + warp * M::WARP;
+  // the heads of a page are neighbours in memory and here
+  const uint32_t w = blockIdx.x * (uint32_t)kScoreWarps + warp;
+  const int tg = (int)(w % p.tok_groups), g = (int)(w / p.tok_groups % p.Hkv);
+  const int run = (int)(w / p.tok_groups / p.Hkv);
+  const int pg = run % p.runs, b = run / p.runs;
+  const int tok0 = tg * p.tpt, toks = min(p.tpt, p.Sq - tok0);
+  const int page0 = pg * 8 * p.groups, page_end = min(p.maxb, page0 + 8 * p.groups);
   grid_dependency_wait();
   grid_dependents_launch();
+  if (b >= p.batch) return;
 
-  const int page0 = pg * kScoreWarps * p.groups_cta * 8;  // this CTA's first page
-  const int page_end = min(p.maxb, page0 + kScoreWarps * p.groups_cta * 8);
-  // keys that any row of this CTA sees
-  const int ql = __ldg(p.qlens + b);
-  int most = keys_seen(p.ctx, p.qlens, b, 0, p.Sq, p.maxb, p.bs_shift, 0);
-  const bool bad = most < 0;
-  if (bad || tok0 >= ql) {
-    if (bad && tid == 0 && blockIdx.x == 0 && g == 0 && p.flags)
-      atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
-    most = 0;
-  } else if (p.causal) {
-    most = most - ql + min(tok0 + toks, ql);
-  }
-  const int npages = pages_of(most, p.bs_shift);
-  float* const out = p.scores + (((size_t)b * p.Sq + tok0) * p.Hkv + g) * p.maxb;
-  const size_t tok_stride = (size_t)p.Hkv * p.maxb;
+  const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
+  const bool bad = ql < 0 || ql > p.Sq || n < ql || (long long)n > ((long long)p.maxb << p.bs_shift);
+  if (bad && lane == 0 && tg == 0 && g == 0 && pg == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
+  // pages that token t of this warp sees; last: the end of those that any of its tokens sees
+  auto pages_seen = [&](int t) {
+    const int i = tok0 + t;
+    return pages_of(bad || i >= ql ? 0 : p.causal ? n - ql + i + 1 : n, p.bs_shift);
+  };
+  const int last = min(page_end, bad || tok0 >= ql ? 0 : pages_seen(min(tok0 + toks, ql) - 1 - tok0));
+  const int mine = last > page0 ? (last - page0 + 7) >> 3 : 0;  // groups of pages to score
 
-  if (page0 < npages) {
-    // fragment (tile, k-step, lane): rows quad and quad + 8 of the tile, channels
-    // 32 (k-step / 2) + 8 qi + 4 (k-step & 1) + {0, 1} and {2, 3}
-    for (int e = tid; e < tiles * KSTEPS * 32; e += kScoreWarps * 32) {
-      const int l = e & 31, ks = (e >> 5) % KSTEPS, tile = (e >> 5) / KSTEPS;
-      uint32_t a[2][2] = {{0, 0}, {0, 0}};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (l >> 2) + 8 * h;
-        int t, head;
-        bool real;
-        if (p.tpt) {
-          t = tile * p.tpt + r / p.G;
-          head = r % p.G;
-          real = r / p.G < p.tpt && t < toks;
-        } else {
-          t = tile / p.tiles_tok;
-          head = (tile % p.tiles_tok) * 16 + r;
-          real = head < p.G;
-        }
-        if (real) {
-          const char* row = p.q + ((((size_t)b * p.Sq + tok0 + t) * p.Hq + (size_t)g * p.G + head) * D) * 2;
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(
-              row + (32 * (ks >> 1) + 8 * (l & 3) + 4 * (ks & 1)) * 2));
-          a[h][0] = v.x;
-          a[h][1] = v.y;
-        }
-      }
-      s_q[e] = make_uint4(a[0][0], a[1][0], a[0][1], a[1][1]);
-    }
-  }
-  __syncthreads();
-
-  for (int gi = 0; gi < p.groups_cta; ++gi) {
-    const int pbase = page0 + (gi * kScoreWarps + warp) * 8;
-    if (pbase >= page_end) break;
-    const int page = pbase + quad;  // this lane's B column
-    uint4 lo[NP], hi[NP];
-    bool ok = false;
-    if (page < npages) {
-      const int blk = __ldg(p.bt + (size_t)b * p.maxb + page);
-      ok = blk >= 0 && blk < p.nblocks;
-      if (ok) {
-        const uint4* box = reinterpret_cast<const uint4*>(p.bounds + ((size_t)blk * p.Hkv + g) * 2 * D * 2);
-#pragma unroll
-        for (int t = 0; t < NP; ++t) {
-          lo[t] = __ldg(box + 4 * t + qi);
-          hi[t] = __ldg(box + D / 8 + 4 * t + qi);
-        }
-      } else if (qi == 0 && p.flags) {
-        atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
-      }
-    }
-    if (!ok) {
-#pragma unroll
-      for (int t = 0; t < NP; ++t) lo[t] = hi[t] = make_uint4(0, 0, 0, 0);
-    }
-    const unsigned ok_mask = __ballot_sync(kFull, ok);  // bit 4 c: page c of the group
-    float best[2] = {-INFINITY, -INFINITY};             // G > 16: over the token's tiles so far
-    // whether row t of this CTA sees page pbase + col, and the score that goes out
-    auto put = [&](int t, int col, float v) {
-      const int seen = bad ? 0 : keys_seen(p.ctx, p.qlens, b, tok0 + t, p.Sq, p.maxb, p.bs_shift, p.causal);
-      const bool in = pbase + col < pages_of(seen, p.bs_shift) && ((ok_mask >> (4 * col)) & 1);
-      out[t * tok_stride + pbase + col] = in ? v : -INFINITY;
-    };
-    for (int tile = 0; tile < tiles; ++tile) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      if (pbase < npages) {
-#pragma unroll
-        for (int t = 0; t < NP; ++t) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 a = s_q[(tile * KSTEPS + 2 * t + h) * 32 + lane];
-            const uint32_t up[4] = {extreme2<QK, true>(a.x, 0u), extreme2<QK, true>(a.y, 0u),
-                                    extreme2<QK, true>(a.z, 0u), extreme2<QK, true>(a.w, 0u)};
-            const uint32_t dn[4] = {extreme2<QK, false>(a.x, 0u), extreme2<QK, false>(a.y, 0u),
-                                    extreme2<QK, false>(a.z, 0u), extreme2<QK, false>(a.w, 0u)};
-            score_mma<QK>(c, up, h ? hi[t].z : hi[t].x, h ? hi[t].w : hi[t].y);
-            score_mma<QK>(c, dn, h ? lo[t].z : lo[t].x, h ? lo[t].w : lo[t].y);
+  // group k's pages into stage st; lane l holds the block of page 32 (k / 4) + l.  A page outside the
+  // pool or past the last is copied from block 0 and not used.
+  int blk = 0;
+  uint32_t ok = 0;  // pages of the 32 that count
+  const char* const bounds = p.bounds + (size_t)g * M::PAGE;
+  const size_t block_stride = (size_t)p.Hkv * M::PAGE;
+  const uint32_t ring_addr = smem_addr(ring);
+  auto issue = [&](int k, int st) -> uint32_t {  // returns the group's pages that count
+    uint32_t in = 0;
+    if (k < mine) {
+      if ((k & 3) == 0) {
+        const int page = page0 + 8 * k + lane;
+        bool good = false;
+        blk = 0;
+        if (page < last) {
+          blk = __ldg(p.bt + (size_t)b * p.maxb + page);
+          good = blk >= 0 && blk < p.nblocks;
+          if (!good) {
+            blk = 0;
+            if (p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
           }
         }
+        ok = __ballot_sync(kFull, good);
       }
-      // c: rows quad, quad + 8 of pages pbase + 2 qi, + 1
-      if (p.tpt) {
-        __syncwarp();
-        s_c[warp][quad][2 * qi] = c[0] * p.sm_scale;
-        s_c[warp][quad][2 * qi + 1] = c[1] * p.sm_scale;
-        s_c[warp][quad + 8][2 * qi] = c[2] * p.sm_scale;
-        s_c[warp][quad + 8][2 * qi + 1] = c[3] * p.sm_scale;
-        __syncwarp();
-        for (int e = lane; e < p.tpt * 8; e += 32) {
-          const int tt = e >> 3, col = e & 7, t = tile * p.tpt + tt;
-          if (t >= toks || pbase + col >= page_end) continue;
-          float v = s_c[warp][tt * p.G][col];
-          for (int h = 1; h < p.G; ++h) v = max_nan(v, s_c[warp][tt * p.G + h][col]);
-          put(t, col, v);
+      in = (ok >> (8 * (k & 3))) & 255;
+      constexpr int LPP = M::PAGE / 16;  // 16-byte pieces of a page
+#pragma unroll
+      for (int e0 = 0; e0 < 8 * LPP; e0 += 32) {
+        const int page = (e0 + lane) / LPP, piece = (e0 + lane) % LPP;
+        const int bk = __shfl_sync(kFull, blk, 8 * (k & 3) + page);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         ring_addr + st * M::STAGE + page * M::STRIDE + piece * 16),
+                     "l"(bounds + bk * block_stride + piece * 16)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return in;
+  };
+  uint32_t in_ring[M::NST - 1];  // of the groups on their way, the next one first
+#pragma unroll
+  for (int k = 0; k < M::NST - 1; ++k) in_ring[k] = issue(k, k);
+
+  // A fragments of row tile `part` (rows quad, quad + 8): max(q, 0) and min(q, 0) of k-step 2 t + h;
+  // rows past the group or the tokens are some real row, and their products are not used
+  uint32_t up[NP][2][4], dn[NP][2][4];
+  auto load_q = [&](int part) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = quad + 8 * h;
+      const int t = p.g_shift >= 0 ? min(r >> p.g_shift, toks - 1) : 0;
+      const int head = p.g_shift >= 0 ? r & (p.G - 1) : min(16 * part + r, p.G - 1);
+      const uint4* row = reinterpret_cast<const uint4*>(
+          p.q + ((((size_t)b * p.Sq + tok0 + t) * p.Hq + (size_t)g * p.G + head) * D) * 2) + qi;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int s = 0; s < NP; ++s) {
+        const uint4 x = __ldg(row + 4 * s);
+        const uint4 u = extreme8<QK, true>(x, zero), d = extreme8<QK, false>(x, zero);
+        up[s][0][h] = u.x;
+        up[s][0][2 + h] = u.y;
+        up[s][1][h] = u.z;
+        up[s][1][2 + h] = u.w;
+        dn[s][0][h] = d.x;
+        dn[s][0][2 + h] = d.y;
+        dn[s][1][h] = d.z;
+        dn[s][1][2 + h] = d.w;
+      }
+    }
+  };
+  if (mine > 0) load_q(0);
+
+  float* const out = p.scores + (((size_t)b * p.Sq + tok0) * p.Hkv + g) * p.maxb;
+  const size_t tok_stride = (size_t)p.Hkv * p.maxb;
+  int st = 0;
+  for (int k = 0; k < mine; ++k) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(M::NST - 2) : "memory");
+    __syncwarp();
+    const uint32_t in = in_ring[0];
+#pragma unroll
+    for (int j = 0; j + 1 < M::NST - 1; ++j) in_ring[j] = in_ring[j + 1];
+    in_ring[M::NST - 2] = issue(k + M::NST - 1, st == 0 ? M::NST - 1 : st - 1);
+    const uint4* box = reinterpret_cast<const uint4*>(ring + st * M::STAGE + quad * M::STRIDE) + qi;
+    const int pbase = page0 + 8 * k;
+    // pages pbase + 2 qi, + 1 of token t score v0, v1
+    auto put = [&](int t, float v0, float v1) {
+      const int page = pbase + 2 * qi, seen = pages_seen(t);
+      if (page < page_end) out[t * tok_stride + page] = page < seen && ((in >> (2 * qi)) & 1) ? v0 : -INFINITY;
+      if (page + 1 < page_end)
+        out[t * tok_stride + page + 1] = page + 1 < seen && ((in >> (2 * qi + 1)) & 1) ? v1 : -INFINITY;
+    };
+    float best[2] = {-INFINITY, -INFINITY};  // a token of several row tiles: over those so far
+    for (int part = 0; part < p.parts; ++part) {
+      if (p.parts > 1) load_q(part);
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < NP; ++t) {
+        const uint4 lo = box[4 * t], hi = box[D / 8 + 4 * t];
+        score_mma<QK>(c, up[t][0], hi.x, hi.y);
+        score_mma<QK>(c2, dn[t][0], lo.x, lo.y);
+        score_mma<QK>(c, up[t][1], hi.z, hi.w);
+        score_mma<QK>(c2, dn[t][1], lo.z, lo.w);
+      }
+      // c: rows quad (c[0], c[1]) and quad + 8 of pages pbase + 2 qi, + 1
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = (c[e] + c2[e]) * p.sm_scale;
+      if (p.g_shift >= 0) {
+        const bool two = (8 >> p.g_shift) < toks;  // rows 8 and up hold tokens too
+        for (int o = 4; o < 4 << p.g_shift; o <<= 1) {
+          c[0] = max_nan(c[0], __shfl_xor_sync(kFull, c[0], o));
+          c[1] = max_nan(c[1], __shfl_xor_sync(kFull, c[1], o));
+          if (two) {
+            c[2] = max_nan(c[2], __shfl_xor_sync(kFull, c[2], o));
+            c[3] = max_nan(c[3], __shfl_xor_sync(kFull, c[3], o));
+          }
+        }
+        const int t = quad >> p.g_shift, t8 = (quad + 8) >> p.g_shift;
+        if ((quad & (p.G - 1)) == 0) {
+          if (t < toks) put(t, c[0], c[1]);
+          if (t8 < toks) put(t8, c[2], c[3]);
         }
       } else {
-        const int part = tile % p.tiles_tok;
-        if (part == 0) best[0] = best[1] = -INFINITY;
-        if (part * 16 + quad < p.G) {
-          best[0] = max_nan(best[0], c[0] * p.sm_scale);
-          best[1] = max_nan(best[1], c[1] * p.sm_scale);
+        if (16 * part + quad < p.G) {
+          best[0] = max_nan(best[0], c[0]);
+          best[1] = max_nan(best[1], c[1]);
         }
-        if (part * 16 + quad + 8 < p.G) {
-          best[0] = max_nan(best[0], c[2] * p.sm_scale);
-          best[1] = max_nan(best[1], c[3] * p.sm_scale);
+        if (16 * part + quad + 8 < p.G) {
+          best[0] = max_nan(best[0], c[2]);
+          best[1] = max_nan(best[1], c[3]);
         }
-        if (part + 1 == p.tiles_tok) {
+        if (part + 1 == p.parts) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             best[0] = max_nan(best[0], __shfl_xor_sync(kFull, best[0], o));
             best[1] = max_nan(best[1], __shfl_xor_sync(kFull, best[1], o));
           }
-          const int col = 2 * qi + quad;
-          if (quad < 2 && pbase + col < page_end) put(tile / p.tiles_tok, col, quad ? best[1] : best[0]);
+          if (quad == 0) put(0, best[0], best[1]);
         }
       }
     }
+    if (++st == M::NST) st = 0;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // pages that none of the tokens sees
+  for (int t = 0; t < toks; ++t)
+    for (int page = page0 + 8 * mine + lane; page < page_end; page += 32) out[t * tok_stride + page] = -INFINITY;
 }
 
 // ---- select ------------------------------------------------------------------------------
@@ -524,7 +575,7 @@ extern "C" pa_status pa_score_blocks(const pa_config* cfg, const void* q, const 
   if (!page_size_ok(c.block_size) || c.num_q_heads % c.num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
   if (c.q_dtype != PA_BF16 && c.q_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
   const int G = c.num_q_heads / c.num_kv_heads;
-  if (c.batch > 65535 || c.num_kv_heads > 65535 || G > 16 * kScoreMaxTiles ||
+  if (c.batch > 65535 || c.num_kv_heads > 65535 || G > 128 ||
       (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
 
@@ -545,30 +596,38 @@ extern "C" pa_status pa_score_blocks(const pa_config* cfg, const void* q, const 
   p.nblocks = c.num_blocks;
   p.causal = c.causal;
   p.sm_scale = c.sm_scale;
-  p.tpt = G <= 16 ? 16 / G : 0;
-  p.tiles_tok = G <= 16 ? 1 : ceil_div(G, 16);
-  p.toks_cta = p.tpt ? kScoreMaxTiles * p.tpt : kScoreMaxTiles / p.tiles_tok;
-  p.toks_cta = p.toks_cta < c.max_q_len ? p.toks_cta : c.max_q_len;
-  p.tok_groups = ceil_div(c.max_q_len, p.toks_cta);
-  p.groups_cta = 4;
-  const long long gx = (long long)ceil_div(c.max_blocks_per_seq, kScoreWarps * 8 * p.groups_cta) * p.tok_groups;
-  if (gx > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  const int tiles = p.tpt ? ceil_div(p.toks_cta, p.tpt) : p.toks_cta * p.tiles_tok;
-  const dim3 grid((unsigned)gx, c.num_kv_heads, c.batch);
-  const int tile_bytes = (c.head_dim / 16) * 32 * (int)sizeof(uint4);
+  const bool packed = G == 1 || G == 2 || G == 4 || G == 8;
+  p.tpt = packed ? 16 / G : 1;
+  p.g_shift = packed ? ilog2((uint32_t)G) : -1;
+  p.parts = ceil_div(G, 16);
+  if (p.tpt > c.max_q_len) p.tpt = c.max_q_len;
+  p.tok_groups = ceil_div(c.max_q_len, p.tpt);
+  // pages of a warp: as many as leave the GPU kScoreWarpsPerSm warps an SM, 256 at most
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const int all = ceil_div(c.max_blocks_per_seq, 8);
+  const double per = (double)c.batch * c.num_kv_heads * p.tok_groups * all / (kScoreWarpsPerSm * sms);
+  p.groups = per < 1. ? 1 : per > kScoreMaxGroups ? kScoreMaxGroups : (int)per;
+  p.runs = ceil_div(all, p.groups);
+  p.batch = c.batch;
+  const double warps = (double)c.batch * c.num_kv_heads * p.tok_groups * p.runs;
+  if (warps > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(((long long)warps + kScoreWarps - 1) / kScoreWarps));
   static std::atomic<uint64_t> done[6];  // devices whose shared-memory limit is raised
-  auto go = [&](void (*kernel)(ScoreParams), std::atomic<uint64_t>& d) {
-    const cudaError_t e = set_smem_attr_once(d, reinterpret_cast<const void*>(kernel), kScoreMaxTiles * tile_bytes);
+  auto go = [&](void (*kernel)(ScoreParams), std::atomic<uint64_t>& d, int smem) {
+    const cudaError_t e = set_smem_attr_once(d, reinterpret_cast<const void*>(kernel), smem);
     return e != cudaSuccess ? e
-                            : launch_pdl(kernel, p, grid, kScoreWarps * 32, (size_t)tiles * tile_bytes,
+                            : launch_pdl(kernel, p, grid, kScoreWarps * 32, (size_t)smem,
                                          reinterpret_cast<cudaStream_t>(stream));
   };
   const bool half = c.q_dtype == PA_FP16;
   cudaError_t e;
   switch (c.head_dim) {
-    case 64: e = half ? go(score_kernel<64, Q_FP16>, done[0]) : go(score_kernel<64, Q_BF16>, done[1]); break;
-    case 128: e = half ? go(score_kernel<128, Q_FP16>, done[2]) : go(score_kernel<128, Q_BF16>, done[3]); break;
-    default: e = half ? go(score_kernel<256, Q_FP16>, done[4]) : go(score_kernel<256, Q_BF16>, done[5]); break;
+    case 64: e = half ? go(score_kernel<64, Q_FP16>, done[0], ScoreSmem<64>::BYTES) : go(score_kernel<64, Q_BF16>, done[1], ScoreSmem<64>::BYTES); break;
+    case 128: e = half ? go(score_kernel<128, Q_FP16>, done[2], ScoreSmem<128>::BYTES) : go(score_kernel<128, Q_BF16>, done[3], ScoreSmem<128>::BYTES); break;
+    default: e = half ? go(score_kernel<256, Q_FP16>, done[4], ScoreSmem<256>::BYTES) : go(score_kernel<256, Q_BF16>, done[5], ScoreSmem<256>::BYTES); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
