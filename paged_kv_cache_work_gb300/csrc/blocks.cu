@@ -25,9 +25,16 @@
 // A row tile holds whole query tokens where a group has 1, 2, 4 or 8 heads (16 / G tokens; a
 // token's maximum is up to three shuffles away); other groups take ceil(G / 16) tiles a token.
 //
-// Select.  One CTA per row: scores become order-preserving 32-bit keys in shared memory, four
-// passes over 8 bits each find the k-th largest key, and one ordered pass writes the pages above
-// it and the first of those equal to it.
+// Select.  One CTA per row: scores become order-preserving 32-bit keys, the k-th largest is found, and one ordered pass writes the pages above it and the first of those equal
+// to it.  What bounds it is the chain of block-wide steps of a row.  So the k-th key comes from one
+// histogram: 256 bins of equal width between the row's least and greatest finite score spread the
+// shared-memory atomics (a float's own upper bits fall into a few exponents: four passes of 8 bits
+// took 14.3 us for 1,024 rows of at most 2,048 pages, this takes 12.0), and the keys of the bin with
+// the k-th are few enough to rank each against all of them.  Rows that leave more than 128 in the bin
+// (ties, outliers) take the passes of 8 bits (1,024 rows of 2,048 equal scores: 18.8 us).  A warp
+// keeps a run of a row's pages in registers where the row has at most 2,048.  Of the 12.0 us the
+// reading of scores and lengths takes 5.4 (two waves of CTAs), the histogram 2.1, the bin's ranks
+// 2.2, the ordered pass 2.5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, ScoreSmem<D>::CTAS_PER_SM) s
 }
 
 // ---- select ------------------------------------------------------------------------------
-constexpr int kSelectThreads = 256;
+constexpr int kSelectRank = 128;      // keys of a bin that are ranked each against all
 constexpr int kSelectKeys = 49152;  // keys that fit in shared memory
 
 struct SelectParams {
@@ -411,16 +418,29 @@ __device__ __forceinline__ uint32_t key_of(float x, bool forced) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-template <bool CACHED>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
-  constexpr int NW = kSelectThreads / 32;
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+constexpr uint32_t kLeastFinite = 0x00800000u, kMostFinite = 0xff7fffffu;  // keys of -+FLT_MAX
+
+// R > 0: keys in registers, R groups of 32 pages a warp; kKeysShared: in shared memory; kKeysAgain:
+// made from the scores in each pass.
+constexpr int kKeysShared = 0, kKeysAgain = -1;
+
+template <int R, int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
+  constexpr int NW = THREADS / 32;
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_hist[256];
-  __shared__ uint32_t s_prefix, s_left;
+  __shared__ __align__(16) uint32_t s_hist[256];
+  __shared__ __align__(16) uint32_t s_cand[kSelectRank];
+  __shared__ uint32_t s_prefix, s_left, s_num;
+  __shared__ uint2 s_range[NW];
   __shared__ int2 s_cnt[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const size_t row = blockIdx.x;
-  const int i = (int)((row / p.Hkv) % p.Sq), b = (int)(row / ((size_t)p.Hkv * p.Sq));
+  const uint32_t row = blockIdx.x, tok = row / p.Hkv;
+  const int i = (int)(tok % p.Sq), b = (int)(tok / p.Sq);
+  for (int e = tid; e < 256; e += THREADS) s_hist[e] = 0;
+  if (tid == 0) s_num = 0;
   grid_dependency_wait();
   grid_dependents_launch();
   int seen = keys_seen(p.ctx, p.qlens, b, i, p.Sq, p.maxb, p.bs_shift, p.causal);
@@ -429,70 +449,148 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     seen = 0;
   }
   const int N = pages_of(seen, p.bs_shift), k = min(p.top_k, N);
-  int32_t* out = p.selected + row * p.top_k;
+  int32_t* out = p.selected + (size_t)row * p.top_k;
   if (tid == 0) p.num[row] = k;
-  for (int e = k + tid; e < p.top_k; e += kSelectThreads) out[e] = -1;
+  for (int e = k + tid; e < p.top_k; e += THREADS) out[e] = -1;
   if (N <= p.top_k) {
-    for (int e = tid; e < N; e += kSelectThreads) out[e] = e;
+    for (int e = tid; e < N; e += THREADS) out[e] = e;
     return;
   }
-  const float* x = p.scores + row * p.maxb;
+  const float* x = p.scores + (size_t)row * p.maxb;
   const int hi_first = N - p.last;
-  auto key = [&](int e) -> uint32_t {
-    if constexpr (CACHED) return s_key[e];
-    return key_of(__ldg(x + e), e < p.first || e >= hi_first);
-  };
-  if constexpr (CACHED)
-    for (int e = tid; e < N; e += kSelectThreads)
-      s_key[e] = key_of(__ldg(x + e), e < p.first || e >= hi_first);
-
-  // ---- the k-th largest key: its bytes from the top, among the keys that share those above
-  uint32_t prefix = 0, left = (uint32_t)k;  // left: how many of the keys with `prefix` are in
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int e = tid; e < 256; e += kSelectThreads) s_hist[e] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int e = tid; e < N; e += kSelectThreads) {
-      const uint32_t v = key(e);
-      if ((v & mask) == prefix) atomicAdd(&s_hist[(v >> shift) & 255], 1u);
-    }
-    __syncthreads();
-    if (warp == 0) {  // bins from the top, eight a lane
-      uint32_t c[8], sum = 0;
+  auto make_key = [&](int e) { return key_of(__ldg(x + e), e < p.first || e >= hi_first); };
+  const int per = round_up(ceil_div(N, NW), 32);  // a warp's run of pages
+  const int e0 = min(warp * per, N), e1 = min(e0 + per, N);
+  uint32_t keys[R > 0 ? R : 1];
+  // f(page, its key) on the run's pages, 32 at a time: whole warps, key 0 (no score's) past its end
+  auto each = [&](auto&& f) {
+    if constexpr (R > 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - (8 * lane + j)];
-      uint32_t inc = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
+      for (int j = 0; j < R; ++j)
+        if (e0 + 32 * j < e1) f(e0 + 32 * j + lane, keys[j]);
+    } else {
+#pragma unroll 4
+      for (int base = e0; base < e1; base += 32) {
+        const int e = base + lane;
+        uint32_t v = 0;
+        if (e < e1) v = R == kKeysShared ? s_key[e] : make_key(e);
+        f(e, v);
       }
-      uint32_t above = inc - sum;
-      if (above < left && left <= inc) {  // one lane
+    }
+  };
+  if constexpr (R > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < left && left <= above + c[j]) {
-            s_prefix = prefix | (uint32_t)(255 - (8 * lane + j)) << shift;
-            s_left = left - above;
-          }
-          above += c[j];
-        }
+    for (int j = 0; j < R; ++j) keys[j] = e0 + 32 * j + lane < e1 ? make_key(e0 + 32 * j + lane) : 0;
+  } else if constexpr (R == kKeysShared) {
+#pragma unroll 4
+    for (int e = e0 + lane; e < e1; e += 32) s_key[e] = make_key(e);
+    __syncwarp();
+  }
+  uint32_t least = ~0u, most = 0u;  // finite keys
+  each([&](int, uint32_t v) {
+    if (v >= kLeastFinite && v <= kMostFinite) {
+      least = min(least, v);
+      most = max(most, v);
+    }
+  });
+  least = __reduce_min_sync(kFull, least);
+  most = __reduce_max_sync(kFull, most);
+  if (lane == 0) s_range[warp] = make_uint2(least, most);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    least = min(least, s_range[w].x);
+    most = max(most, s_range[w].y);
+  }
+
+  // ---- the k-th largest key (prefix), and how many of those equal to it are in (left)
+  uint32_t prefix = 0, left = (uint32_t)k;
+  // the bin of 256 with the left-th key from the top: the same in every warp
+  auto find_bin = [&]() -> uint32_t {
+    uint32_t c[8], sum = 0;  // bins from the top, eight a lane
+    const uint4 h1 = *reinterpret_cast<const uint4*>(s_hist + 252 - 8 * lane);
+    const uint4 h0 = *reinterpret_cast<const uint4*>(s_hist + 248 - 8 * lane);
+    c[0] = h1.w, c[1] = h1.z, c[2] = h1.y, c[3] = h1.x;
+    c[4] = h0.w, c[5] = h0.z, c[6] = h0.y, c[7] = h0.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += c[j];
+    uint32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += y;
+    }
+    uint32_t above = inc - sum, bin = 0, rest = 0;
+    const int src = __ffs(__ballot_sync(kFull, above < left && left <= inc)) - 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (above < left && left <= above + c[j]) {
+        bin = 255 - (8 * lane + j);
+        rest = left - above;
+      }
+      above += c[j];
+    }
+    left = __shfl_sync(kFull, rest, src);
+    return __shfl_sync(kFull, bin, src);
+  };
+  // A monotone map: x - low, the product and the truncation are monotone each.  Where the range
+  // overflows or vanishes, NaN and infinity still convert to bins that keep the order.
+  const float low = least <= most ? score_of(least) : 0.f;
+  const float width = least <= most ? score_of(most) - low : INFINITY;
+  const float scale = 255.f / width;
+  auto bin_of = [&](uint32_t v) -> uint32_t {
+    if (v >= 0xfffffffeu) return 255u;
+    return (uint32_t)min(max(__float2int_rz((score_of(v) - low) * scale), 0), 255);
+  };
+  each([&](int, uint32_t v) {
+    if (v) atomicAdd(&s_hist[bin_of(v)], 1u);
+  });
+  __syncthreads();
+  const uint32_t bin = find_bin();
+  const int cand = (int)s_hist[bin];
+  if (cand <= kSelectRank) {
+    each([&](int, uint32_t v) {
+      if (v && bin_of(v) == bin) s_cand[atomicAdd(&s_num, 1u)] = v;
+    });
+    __syncthreads();
+    for (int c = tid; c < cand; c += THREADS) {  // rank each against all
+      const uint32_t v = s_cand[c];
+      uint32_t above = 0, equal = 0;
+#pragma unroll 8
+      for (int j = 0; j < cand; ++j) {
+        const uint32_t y = s_cand[j];
+        above += y > v;
+        equal += y == v;
+      }
+      if (above < left && left <= above + equal) {  // equal keys write the same
+        s_prefix = v;
+        s_left = left - above;
       }
     }
     __syncthreads();
     prefix = s_prefix;
     left = s_left;
+  } else {  // its bytes from the top, among the keys that share those above
+    left = (uint32_t)k;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      __syncthreads();
+      for (int e = tid; e < 256; e += THREADS) s_hist[e] = 0;
+      __syncthreads();
+      const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+      each([&](int, uint32_t v) {
+        if (v && (v & mask) == prefix) atomicAdd(&s_hist[(v >> shift) & 255], 1u);
+      });
+      __syncthreads();
+      prefix |= find_bin() << shift;
+    }
   }
 
   // ---- ascending pages: those above the key, and the first `left` equal to it
-  const int per = round_up(ceil_div(N, NW), 32);  // a warp's run of pages
-  const int e0 = min(warp * per, N), e1 = min(e0 + per, N);
   int above = 0, equal = 0;
-  for (int e = e0 + lane; e < e1; e += 32) {
-    const uint32_t v = key(e);
+  each([&](int, uint32_t v) {
     above += v > prefix;
     equal += v == prefix;
-  }
+  });
   above = __reduce_add_sync(kFull, above);
   equal = __reduce_add_sync(kFull, equal);
   if (lane == 0) s_cnt[warp] = make_int2(above, equal);
@@ -502,18 +600,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     at += s_cnt[w].x;
     eq += s_cnt[w].y;
   }
-  for (int base = e0; base < e1; base += 32) {
-    const int e = base + lane;
-    const uint32_t v = e < e1 ? key(e) : 0u;
-    const unsigned gt = __ballot_sync(kFull, e < e1 && v > prefix);
-    const unsigned same = __ballot_sync(kFull, e < e1 && v == prefix);
-    const unsigned below = (1u << lane) - 1;
+  const unsigned below = (1u << lane) - 1;
+  each([&](int e, uint32_t v) {
+    const unsigned gt = __ballot_sync(kFull, v > prefix);
+    const unsigned same = __ballot_sync(kFull, v == prefix);
     const int rank = eq + __popc(same & below);
-    const bool take = ((gt >> lane) & 1) || (((same >> lane) & 1) && rank < (int)left);
+    const bool take = v > prefix || (v == prefix && rank < (int)left);
     if (take) out[at + __popc(gt & below) + min(rank, (int)left)] = e;
     at += __popc(gt);
     eq += __popc(same);
-  }
+  });
 }
 
 }  // namespace
@@ -668,13 +764,28 @@ extern "C" pa_status pa_select_blocks(const pa_config* cfg, const float* scores,
   p.first = num_first;
   p.last = num_last;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)rows);
-  if (c.max_blocks_per_seq > kSelectKeys)
-    return launch_pdl(select_kernel<false>, p, grid, kSelectThreads, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  static std::atomic<uint64_t> done{0};  // devices whose shared-memory limit is raised
-  if (set_smem_attr_once(done, reinterpret_cast<const void*>(select_kernel<true>), kSelectKeys * 4) != cudaSuccess)
+  auto go = [&](void (*kernel)(SelectParams), int threads, size_t smem) {
+    return launch_pdl(kernel, p, dim3((unsigned)rows), threads, smem, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  };
+  // Rows of 256 and 2,048 columns, 1,024 of them: 6.1 and 13.7 us with 2 and 8 groups of registers a
+  // warp, 8.2 us for the first with 8, 15.3 us for the second from shared memory.  Longer rows
+  // take 1,024 threads, 32 rows of 2,049 and 8,192 columns 6.5 and 9.9 us and 7.3 and 18.0 us with 256,
+  // unless there are more rows than SMs: 1,024 rows 41 and 64 us, 16.4 and 42 us with 256 threads;
+  // at 32,768 columns 251 us and 662 us.  Keys made again in each pass, 32 rows of 32,768: 33.9 us
+  // for 25.6 us.
+  if (c.max_blocks_per_seq <= 2 * 256) return go(select_kernel<2, 256>, 256, 0);
+  if (c.max_blocks_per_seq <= 8 * 256) return go(select_kernel<8, 256>, 256, 0);
+  if (c.max_blocks_per_seq > kSelectKeys) return go(select_kernel<kKeysAgain, 1024>, 1024, 0);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ERR_CUDA;
-  return launch_pdl(select_kernel<true>, p, grid, kSelectThreads, (size_t)c.max_blocks_per_seq * 4, s) == cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
+  const size_t smem = (size_t)c.max_blocks_per_seq * 4;
+  if (c.max_blocks_per_seq <= 32 * 256 && rows > sms)  // (32 KB of keys at most: no raised limit)
+    return go(select_kernel<kKeysShared, 256>, 256, smem);
+  static std::atomic<uint64_t> done{0};  // devices whose shared-memory limit is raised
+  void (*const kernel)(SelectParams) = select_kernel<kKeysShared, 1024>;
+  if (set_smem_attr_once(done, reinterpret_cast<const void*>(kernel), kSelectKeys * 4) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return go(kernel, 1024, smem);
 }

@@ -155,7 +155,8 @@ SELECT = [
     (1, 1, 1, 16, 40000, 128, 1, 4, 0, "ties"), (2, 1, 1, 16, 20000, 1000, 0, 0, 0, "odd"), (2, 3, 2, 16, 300, 1, 0, 1, 1, "odd"),
     (2, 1, 2, 16, 5000, 5, 2, 3, 0, "equal"), (1, 1, 1, 1024, 1, 4, 1, 1, 0, "plain"), (2, 1, 1, 16, 600, 37, 0, 0, 0, "equal"),
     (1, 1, 2, 16, 70000, 300, 3, 3, 0, "plain"), (1, 1, 1, 16, 900000, 64, 1, 1, 0, "ties"), (1, 1, 1, 16, 900000, 55000, 1, 1, 0, "odd"),
-    (2, 1, 1, 16, 528, 32, 0, 0, 0, "plain"), (2, 1, 1, 16, 512, 32, 0, 0, 0, "plain"),
+    (40, 1, 4, 16, 33000, 128, 1, 4, 0, "plain"), (20, 4, 2, 16, 100000, 300, 2, 4, 1, "odd"),  # more rows than SMs, long ones
+    (40, 1, 5, 16, 150000, 64, 0, 1, 0, "ties"), (2, 1, 1, 16, 528, 32, 0, 0, 0, "plain"), (2, 1, 1, 16, 512, 32, 0, 0, 0, "plain"),
 ]
 
 
@@ -185,6 +186,43 @@ def test_selection_is_that_of_a_sort(B, sq, hkv, bs, longest, top_k, first, last
     assert int(flags.item()) == 0
     assert np.array_equal(num.cpu().numpy(), count)
     assert np.array_equal(sel.cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [255, 256, 257, 300, 2000])
+@pytest.mark.parametrize("values", ["whole range", "neighbours", "subnormal", "one finite", "no finite", "outlier", "halves"])
+def test_selection_from_odd_ranges(n, values, cuda_device, pa):
+    """Ranges whose width overflows, vanishes or is that of one far value: every rank's page is a sort's."""
+    rng = np.random.default_rng(n)
+    top = np.finfo(np.float32).max
+    x = rng.standard_normal((1, 1, 6, n)).astype(np.float32)
+    if values == "whole range":
+        x = (x / np.abs(x).max() * top).astype(np.float32)
+        x[0, 0, 1, 3:5] = top, -top
+        x[0, 0, 2, 3:6] = np.inf, -np.inf, np.nan
+    elif values == "neighbours":
+        x = (np.float32(1).view(np.int32) + rng.integers(0, 3, x.shape)).astype(np.int32).view(np.float32)
+    elif values == "subnormal":
+        x = (rng.integers(0, 1000, x.shape).astype(np.int32) | rng.choice([0, -2**31], x.shape).astype(np.int32)).view(np.float32)
+    elif values == "one finite":
+        x = rng.choice(np.float32([np.inf, -np.inf, np.nan]), x.shape)
+        x[..., n // 2] = -3.0
+    elif values == "no finite":
+        x = rng.choice(np.float32([np.inf, -np.inf, np.nan]), x.shape)
+    elif values == "outlier":
+        x[0, 0, :, n - 9] = 1e30
+        x[0, 0, 3:, 7] = -1e38
+    else:
+        x = np.where(rng.random(x.shape) < 0.5, x, np.float32(-0.0))
+    for k in (1, 2, n // 3, n - 1):
+        cfg = config(1, 1, 6, 6, 128, 16, n, 1)
+        sel = torch.full((1, 1, 6, k), -9, dtype=torch.int32, device=cuda_device)
+        num = torch.full((1, 1, 6), -9, dtype=torch.int32, device=cuda_device)
+        pa.select_blocks(cfg, torch.from_numpy(x).to(cuda_device), gpu([n * 16], cuda_device), gpu([1], cuda_device), 0, 1,
+                         sel, num)
+        want, count = plain64.select(x, [n * 16], [1], 16, 0, k, 0, 1)
+        assert np.array_equal(num.cpu().numpy(), count)
+        assert np.array_equal(sel.cpu().numpy(), want)
 
 
 @pytest.mark.gpu
