@@ -230,7 +230,7 @@ PA_API pa_status pa_decode_step_static(const pa_config *cfg, const void *q, cons
  * row_off[b] .. row_off[b] + context_lens[b] - 1 of k_out and of v_out, where
  * row_off[b] = context_lens[0] + ... + context_lens[b - 1]; a row is one token's
  * [num_kv_heads, head_dim] values exactly as the cache stores them (bf16, fp16 or E4M3
- * codes; per-token fp8 scales are not copied).  Reads cfg's batch, num_kv_heads, head_dim,
+ * codes; the scales of tokens or pages are not copied).  Reads cfg's batch, num_kv_heads, head_dim,
  * block_size, max_blocks_per_seq, num_blocks and kv_dtype; the other fields are ignored.
  *
  *   k_cache, v_cache  device, [num_blocks, block_size, num_kv_heads, head_dim], 16-byte aligned
@@ -372,8 +372,8 @@ PA_API pa_status pa_update_bounds(const pa_config *cfg, const void *k_new,
  *   scores   fp32 [B, Sq, Hkv, max_blocks_per_seq], written whole
  *   flags    NULL, or a device int32: PA_FLAG_BAD_LENGTHS (that sequence scores -inf),
  *            PA_FLAG_BAD_BLOCK_ID (that page scores -inf)
- * Reads cfg's sizes, q_dtype, causal and sm_scale.  PA_ERR_UNSUPPORTED for more than 128 query
- * heads a kv head, batch or num_kv_heads above 65535, and what the decode does not take. */
+ * Reads cfg's sizes, q_dtype, causal and sm_scale.  PA_ERR_UNSUPPORTED for what the decode does
+ * not take. */
 PA_API pa_status pa_score_blocks(const pa_config *cfg, const void *q, const void *k_bounds,
                                  const int32_t *block_tables, const int32_t *context_lens,
                                  const int32_t *q_lens, float *scores, int32_t *flags,
@@ -411,7 +411,9 @@ PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
  *                 page outside the sequence's is skipped), PA_FLAG_BAD_BLOCK_ID (a listed page
  *                 whose block lies outside [0, num_blocks) is skipped)
  * One launch, no workspace; the split of a row's pages depends on the sizes alone, so equal
- * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used. */
+ * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used.
+ * PA_ERR_UNSUPPORTED for what the decode does not take, and for lists of 2^31 tokens or more
+ * (top_k * block_size). */
 PA_API pa_status pa_decode_selected(const pa_config *cfg, const void *q, const void *k_cache,
                                     const void *v_cache, const float *k_scale,
                                     const float *v_scale, const int32_t *block_tables,

@@ -246,6 +246,14 @@ def _dense(call: str, device: int, count: int, t, dtypes) -> int:
     raise PaError(call, ERR_INVALID_ARG)
 
 
+def _columns(call: str, t) -> int:
+    """The last dimension of a tensor that has one; PaError otherwise."""
+    shape = getattr(t, "shape", None)
+    if not shape:
+        raise PaError(call, ERR_INVALID_ARG)
+    return shape[-1]
+
+
 def _maybe(call: str, device: int, count: int, t, dtypes) -> Optional[int]:
     return None if t is None else _dense(call, device, count, t, dtypes)
 
@@ -306,7 +314,7 @@ def select_blocks(cfg: PaConfig, scores, context_lens, q_lens, num_first: int, n
     num_last always among them (see pa_select_blocks in pa.h)."""
     dev, i32, _, f32, _ = _types()
     name, B = "pa_select_blocks", cfg.batch
-    rows, top_k = B * cfg.max_q_len * cfg.num_kv_heads, selected.shape[-1]
+    rows, top_k = B * cfg.max_q_len * cfg.num_kv_heads, _columns(name, selected)
     _check(name, load().pa_select_blocks(
         ctypes.byref(cfg), _dense(name, dev, rows * cfg.max_blocks_per_seq, scores, f32),
         _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32), top_k,
@@ -322,7 +330,7 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
     first num_selected count (see pa_decode_selected in pa.h).  One launch, no workspace."""
     dev, i32, _, f32, kinds = _types()
     name, B, Hkv, mode = "pa_decode_selected", cfg.batch, cfg.num_kv_heads, cfg.kv_scale_mode
-    rows, top_k = B * cfg.max_q_len, selected.shape[-1]
+    rows, top_k = B * cfg.max_q_len, _columns(name, selected)
     kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
     heads = cfg.num_blocks * Hkv
     cache = heads * cfg.block_size * cfg.head_dim

@@ -302,7 +302,8 @@ pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_
   p.qk_scale = c.sm_scale * kLog2e;
   const double units_d = (double)c.batch * c.max_q_len * c.num_kv_heads * p.RB;
   if (units_d * kSelMaxSplit > INT32_MAX ||
-      (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX)
+      (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX ||
+      (long long)top_k * c.block_size > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   SelectedKind k;
   int dev = 0;

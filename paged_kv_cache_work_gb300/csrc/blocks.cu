@@ -671,9 +671,7 @@ extern "C" pa_status pa_score_blocks(const pa_config* cfg, const void* q, const 
   if (!page_size_ok(c.block_size) || c.num_q_heads % c.num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
   if (c.q_dtype != PA_BF16 && c.q_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
   const int G = c.num_q_heads / c.num_kv_heads;
-  if (c.batch > 65535 || c.num_kv_heads > 65535 || G > 128 ||
-      (long long)c.max_blocks_per_seq * c.block_size > INT32_MAX)
-    return PA_ERR_UNSUPPORTED;
+  if ((long long)c.max_blocks_per_seq * c.block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
 
   ScoreParams p;
   p.q = static_cast<const char*>(q);
@@ -698,6 +696,7 @@ extern "C" pa_status pa_score_blocks(const pa_config* cfg, const void* q, const 
   p.parts = ceil_div(G, 16);
   if (p.tpt > c.max_q_len) p.tpt = c.max_q_len;
   p.tok_groups = ceil_div(c.max_q_len, p.tpt);
+  if ((double)c.batch * c.num_kv_heads * p.tok_groups > INT32_MAX) return PA_ERR_UNSUPPORTED;
   // pages of a warp: as many as leave the GPU kScoreWarpsPerSm warps an SM, 256 at most
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

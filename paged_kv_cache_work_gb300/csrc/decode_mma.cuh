@@ -687,14 +687,16 @@ cudaError_t launch_mma_instance(const KernelParams& prm, const CUtensorMap& kmap
   PA_MMA_ROWS(X, 16) PA_MMA_ROWS(X, 32) PA_MMA_ROWS(X, 64) PA_MMA_PAGES(X, 32) PA_MMA_PAGES(X, 64)
 
 // A cache row must hold whole 128-byte slabs (a 64-dim fp8 cache stays on CUDA cores).
-constexpr bool mma_fits(int D, int kvk) { return D * (kvk == KV_FP8 ? 1 : 2) >= 128; }
+constexpr bool mma_fits(int D, int kvk, int scales) {
+  return D * (kvk == KV_FP8 ? 1 : 2) >= 128 && (scales != SC_BLOCK || D == 256);
+}
 
 template <int D>
 cudaError_t launch_mma_for_dim(const KernelParams& prm, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int grid, int mp, int kvk, int qk,
                                int scales, cudaStream_t s) {
 #define PA_MMA_CASE(MP_, KVK_, QK_, SC_)                                          \
-  if constexpr (mma_fits(D, KVK_)) {                                                \
+  if constexpr (mma_fits(D, KVK_, SC_)) {                                                \
     if (mp == MP_ && kvk == KVK_ && qk == QK_ && scales == SC_)                     \
       return launch_mma_instance<D, MP_, KVK_, QK_, SC_>(prm, kmap, vmap, grid, s); \
   }
@@ -706,7 +708,7 @@ cudaError_t launch_mma_for_dim(const KernelParams& prm, const CUtensorMap& kmap,
 template <int D>
 int mma_ctas_per_sm_for_dim(int mp, int kvk, int scales) {
 #define PA_MMA_OCC(MP_, KVK_, QK_, SC_)                                            \
-  if constexpr (mma_fits(D, KVK_)) {                                                 \
+  if constexpr (mma_fits(D, KVK_, SC_)) {                                                 \
     if (mp == MP_ && kvk == KVK_ && scales == SC_) return MmaTraits<D, MP_, KVK_, SC_>::CTAS_PER_SM; \
   }
   PA_MMA_ALL(PA_MMA_OCC)

@@ -251,6 +251,62 @@ def test_equal_scales_are_the_per_token_cache(cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sq,hq,hkv,d,bs", [(1, 16, 1, 128, 16), (2, 4, 1, 64, 64), (1, 8, 2, 256, 32), (3, 6, 1, 256, 16),
+                                            (4, 16, 1, 128, 32)])
+def test_decode_reads_nothing_else(sq, hq, hkv, d, bs, cuda_device, pa):
+    """NaN codes and scales wherever no key lies change no bit; the static scratch gives the same; a
+    bad page is flagged and the other sequences keep their bits; so is a plan for other lengths."""
+    p = decode_problem(7, 4, sq, hq, hkv, d, bs, 700, "bf16", 2)
+    p["ctx"][1] = p["ql"][1] = 1
+    p["ql"][:] = np.minimum(p["ctx"], sq)
+    p["bt"][1, 0] = p["nblocks"] - 1
+    cfg = config(4, sq, hq, hkv, d, bs, p["maxb"], p["nblocks"], causal=1)
+    out, lse = run_decode(pa, p, cfg, cuda_device)
+    free = np.ones((p["nblocks"], bs), bool)
+    for b in range(4):
+        for t in range(p["ctx"][b]):
+            free[p["bt"][b, t // bs], t % bs] = False
+    for k in ("kc", "vc"):
+        p[k][torch.from_numpy(free)] = 0x7f
+    for k in ("ks", "vs"):
+        p[k][torch.from_numpy(free.all(1))] = float("nan")
+    again, lse_again = run_decode(pa, p, cfg, cuda_device)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+    dev = cuda_device
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    args = [p[k].to(dev) for k in ("q", "kc", "vc", "ks", "vs")]
+    bt, ctx, ql = t(p["bt"]), t(p["ctx"]), t(p["ql"])
+    o2, l2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+    if pa.workspace_size(cfg) <= pa.STATIC_SCRATCH_BYTES:
+        pa.decode_step_static(cfg, *args, bt, ctx, ql, o2, l2)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+    ws = torch.empty(pa.workspace_size(cfg), dtype=torch.uint8, device=dev)
+
+    def step(tables, now):
+        pa.plan(cfg, bt, ctx, ql, ws)
+        pa.decode(cfg, *args, tables, now, ql, o2, l2, ws)
+        pa.reduce(cfg, o2, l2, ws)
+        torch.cuda.synchronize()
+
+    for bad in (-1, p["nblocks"]):
+        bt_bad = bt.clone()
+        bt_bad[2, 0] = bad
+        step(bt_bad, ctx)
+        assert pa.read_flags(ws) == pa.FLAG_BAD_BLOCK_ID
+        for b in (0, 1, 3):
+            assert torch.equal(o2[b], out[b]) and torch.equal(l2[b], lse[b])
+    if d < 256 or sq * hq // hkv <= 16:  # (the mma.sync kernel waits for the planner)
+        half = ctx.clone()
+        half[0] //= 2
+        step(bt, half)
+        assert pa.read_flags(ws) & pa.FLAG_STALE_PLAN
+    step(bt, ctx)
+    assert pa.read_flags(ws) == 0 and torch.equal(o2, out)
+
+
+@pytest.mark.gpu
 def test_generation_appends_then_decodes(cuda_device, pa):
     """Steps of append and decode (captured, on a stream of their own, replayed) over pages that
     grow: each step's output is that of the cache the plain append left."""

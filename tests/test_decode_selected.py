@@ -341,6 +341,7 @@ def test_refused_on_the_host(lib):
                      (dict(B=0), pa.ERR_INVALID_ARG), (dict(kv="16", mode="block"), pa.ERR_UNSUPPORTED),
                      (dict(maxb=1 << 28), pa.ERR_UNSUPPORTED), (dict(B=1 << 20, sq=1 << 10), pa.ERR_UNSUPPORTED)):
         assert call(config(**{**good, **kw})) == want, kw
+    assert call(top_k=1 << 27) == pa.ERR_UNSUPPORTED  # a list of 2^31 tokens
     for mode in ("tensor", "token", "block"):
         c = config(**good, kv="8", mode=mode)
         assert call(c) == pa.ERR_INVALID_ARG
@@ -359,7 +360,7 @@ def test_binding_refuses_tensors_that_do_not_fit(cuda_device, pa):
                 ql=t(p["ql"]), sel=t(p["sel"]), num=t(p["num"]), out=p["q"].to(dev))
     bad = [("q", p["q"]), ("q", good["q"].float()), ("q", good["q"].repeat(1, 1, 1, 2)[..., ::2]), ("kc", good["kc"][1:]),
            ("kc", good["kc"].half()), ("bt", good["bt"].long()), ("ctx", good["ctx"][:1]), ("sel", good["sel"][:1]),
-           ("num", good["num"].flatten()[:3]), ("out", good["out"][:1]), ("vc", None)]
+           ("num", good["num"].flatten()[:3]), ("out", good["out"][:1]), ("vc", None), ("sel", None), ("sel", 1 << 20)]
     for k, x in bad:
         with pytest.raises(pa.PaError) as e:
             pa.decode_selected(cfg, *{**good, k: x}.values())

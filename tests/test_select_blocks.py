@@ -89,6 +89,7 @@ SCORE = [
     (3, 1, 4, 1, 128, 16, 700, 0, "bf16"), (2, 3, 10, 2, 64, 16, 3000, 1, "fp16"), (2, 1, 16, 1, 256, 64, 900, 0, "bf16"),
     (2, 2, 24, 1, 128, 16, 500, 1, "bf16"), (1, 5, 256, 2, 64, 32, 400, 1, "bf16"), (2, 70, 3, 3, 128, 16, 200, 1, "fp16"),
     (4, 40, 7, 1, 64, 128, 1000, 0, "bf16"), (1, 1, 1, 1, 128, 16, 1, 0, "bf16"), (1, 4, 9, 1, 256, 1024, 5000, 1, "fp16"),
+    (1, 2, 150, 1, 64, 16, 100, 1, "bf16"), (70000, 1, 1, 1, 64, 16, 16, 0, "bf16"),
 ]
 
 
@@ -302,7 +303,7 @@ def test_bounds_and_scores_refused_on_the_host(lib):
         c = config(**good)
         c.q_dtype = pa.FP8_E4M3
         assert call(c) == pa.ERR_UNSUPPORTED
-    for kw in (dict(hq=9), dict(hq=2 * 129), dict(B=65536), dict(maxb=1 << 28)):
+    for kw in (dict(hq=9), dict(B=1 << 21, sq=1 << 11), dict(maxb=1 << 28)):
         assert score(config(**{**good, **kw})) == pa.ERR_UNSUPPORTED, kw
     assert score(config(**good, sm=float("nan"))) == pa.ERR_INVALID_ARG
     assert lib.pa_update_bounds(None, *([fake] * 5), None, None) == pa.ERR_INVALID_ARG
