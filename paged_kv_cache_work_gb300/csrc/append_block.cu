@@ -18,10 +18,14 @@
 // One CTA per (sequence, touched page, kv head, K or V): nobody else writes that page's codes of
 // that head or its scale, so there is nothing to join.  A thread keeps up to kKeep 16-byte pieces
 // of the new rows in registers between the pass for a and the pass for the codes; only pages
-// with more new rows than that are read twice (the second time from L2).  Most of the grid may be
-// pages that nobody touches (the host does not know the lengths), so CTAs are small: prompts of
-// 1 to 4,096 rows, append and bounds, 27.6 us with 128 threads, 33.6 with 256, 52.7 with 512, 32.7
-// with 64; a persistent grid that walks over the pages, 36.9.
+// with more new rows than that are read twice (the second time from L2).  A thread keeps its column,
+// so its rows are one stride apart.  Most of the grid may be pages that nobody touches (the host
+// does not know the lengths), so CTAs are small.  Eight prompts of 1 to 4,096 rows, 8 heads of 128:
+// 20.7 us (100 MB, 14.7 us at the copy rate), 27.2 with the bounds' update behind it.  The two
+// calls took 32.3 us with 256 threads (4 pieces kept), 29.2 with 4 pieces kept, 30.4 with registers cut
+// to 64 for eight CTAs an SM; earlier forms 27.6 us with 128 threads, 52.7 with 512, 32.7 with 64,
+// and 36.9 as a persistent grid that walks over the pages.  What bounds it: instructions, about
+// ten for two values, at 0.6 a cycle and scheduler, while a CTA's loads come in once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -59,14 +63,14 @@ __device__ __forceinline__ float finite_amax(float a, float x) {
   return m <= 3.402823466e38f ? fmaxf(a, m) : a;  // false for inf and NaN
 }
 
-// The larger magnitude of each half (NaN wins).
+// The larger magnitude of each half under some sign (NaN wins).
 template <int QK>
 __device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t w) {
   uint32_t r;
   if constexpr (QK == Q_BF16)
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w & 0x7fff7fffu));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w));
   else
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w & 0x7fff7fffu));
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w));
   return r;
 }
 
@@ -82,6 +86,7 @@ template <int D, int QK>
 __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBlockParams p) {
   constexpr int PPR = D / 8;  // 16-byte pieces (8 elements) of a new row
   constexpr int NW = kThreads / 32;
+  constexpr int RG = kThreads / PPR;  // rows taken at a time: a thread keeps its column
   __shared__ uint32_t s_max[NW];
   const int tid = threadIdx.x;
   const bool is_v = blockIdx.x & 1;
@@ -95,16 +100,14 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
   const size_t row_stride = (size_t)p.t.Hkv * D;  // elements between a head's rows (new and cached)
   const uint4* src = reinterpret_cast<const uint4*>(
       (is_v ? p.v_new : p.k_new) + (((size_t)b * p.t.Sq + t.i0) * row_stride + (size_t)g * D) * 2);
-  auto piece = [&](int e) {  // piece e of the page's new rows
-    return __ldg(src + (size_t)(e / PPR) * (row_stride / 8) + e % PPR);
-  };
-  const int pieces = t.rows * PPR;
+  const int c = tid % PPR, r0 = tid / PPR;
+  const size_t step = RG * (row_stride / 8);
+  src += (size_t)r0 * (row_stride / 8) + c;
+  auto piece = [&](int k) { return __ldg(src + (size_t)k * step); };  // of row r0 + k RG
+  const int count = (t.rows - r0 + RG - 1) / RG;                       // this thread's pieces
   uint4 keep[kKeep];
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) {
-    const int e = tid + k * kThreads;
-    keep[k] = e < pieces ? piece(e) : make_uint4(0, 0, 0, 0);
-  }
+  for (int k = 0; k < kKeep; ++k) keep[k] = k < count ? piece(k) : make_uint4(0, 0, 0, 0);
   const int blk = touched_block(p.t, b, t, tid == 0 && !is_v);
   if (blk < 0) return;
   float* scale = (is_v ? p.v_scale : p.k_scale) + (size_t)blk * p.t.Hkv + g;
@@ -118,20 +121,20 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
   };
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) amax_of(keep[k]);
-  for (int e = tid + kKeep * kThreads; e < pieces; e += kThreads) amax_of(piece(e));
+  for (int k = kKeep; k < count; ++k) amax_of(piece(k));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) big = amax2<QK>(big, __shfl_xor_sync(kFull, big, o));
   if ((tid & 31) == 0) s_max[tid >> 5] = big;
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < NW; ++x) big = amax2<QK>(big, s_max[x]);
-  const float2 big2 = pair_to_f2<QK>(big);
+  const float2 big2 = pair_to_f2<QK>(big & 0x7fff7fffu);
   float a = fmaxf(big2.x, big2.y);
   const bool finite = fabsf(big2.x) <= 3.402823466e38f && fabsf(big2.y) <= 3.402823466e38f;
   if (!finite) {  // the same for the whole CTA: look again, past infinities and NaN
     a = 0.f;
-    for (int e = tid; e < pieces; e += kThreads) {
-      const uint4 v = piece(e);
+    for (int k = 0; k < count; ++k) {
+      const uint4 v = piece(k);
       const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -157,45 +160,44 @@ __global__ void __launch_bounds__(kThreads) append_block_kernel(const AppendBloc
   char* cache = (is_v ? p.v_cache : p.k_cache) +
                 ((size_t)blk * p.t.bs) * row_stride + (size_t)g * D;  // slot 0, this head
   if (grown) {
-    for (int e = tid; e < t.slot0 * PPR; e += kThreads) {
-      uint2* at = reinterpret_cast<uint2*>(cache + (size_t)(e / PPR) * row_stride + (e % PPR) * 8);
-      uint2 c = *at;
-      c.x = rescale4(c.x, s_old, s);
-      c.y = rescale4(c.y, s_old, s);
-      *at = c;
+    char* at = cache + (size_t)r0 * row_stride + c * 8;
+    for (int row = r0; row < t.slot0; row += RG, at += RG * row_stride) {
+      uint2 x = *reinterpret_cast<uint2*>(at);
+      x.x = rescale4(x.x, s_old, s);
+      x.y = rescale4(x.y, s_old, s);
+      *reinterpret_cast<uint2*>(at) = x;
     }
   }
   // ---- the new codes
   const float r = __frcp_rn(s);
   const float2 r2 = make_float2(r, r), neg_s2 = make_float2(-s, -s);
   const bool fast = finite && s >= 0x1p-90f;  // the same for the whole CTA
-  auto put = [&](int e, const uint4& v) {
+  char* const dst = cache + (size_t)(t.slot0 + r0) * row_stride + c * 8;
+  auto put = [&](int k, const uint4& v) {
     const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4];
+    uint32_t e[4];
     if (fast) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = pair_to_f2<QK>(h[k]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = pair_to_f2<QK>(h[j]);
         float2 q = mul2(x, r2);
         q = ffma2(ffma2(q, neg_s2, x), r2, q);
-        c[k] = e4m3x2_rn_sat(q.x, q.y);
+        e[j] = e4m3x2_rn_sat(q.x, q.y);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = pair_to_f2<QK>(h[k]);
-        c[k] = e4m3x2_rn_sat(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s));
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = pair_to_f2<QK>(h[j]);
+        e[j] = e4m3x2_rn_sat(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s));
       }
     }
-    *reinterpret_cast<uint2*>(cache + (size_t)(t.slot0 + e / PPR) * row_stride + (e % PPR) * 8) =
-        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    *reinterpret_cast<uint2*>(dst + (size_t)k * RG * row_stride) =
+        make_uint2(__byte_perm(e[0], e[1], 0x5410), __byte_perm(e[2], e[3], 0x5410));
   };
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) {
-    const int e = tid + k * kThreads;
-    if (e < pieces) put(e, keep[k]);
-  }
-  for (int e = tid + kKeep * kThreads; e < pieces; e += kThreads) put(e, piece(e));
+  for (int k = 0; k < kKeep; ++k)
+    if (k < count) put(k, keep[k]);
+  for (int k = kKeep; k < count; ++k) put(k, piece(k));
 }
 
 template <class K>

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
   const int g = (int)(blockIdx.x - bj * p.t.Hkv);
   const int b = (int)p.t.page_div.div(bj), j = (int)p.t.page_div.mod(bj);
   grid_dependency_wait();
+  grid_dependents_launch();
   TouchedPage t;
   if (!touched_page(p.t, b, j, tid == 0 && g == 0, &t)) return;
   const size_t row_stride = (size_t)p.t.Hkv * D;
