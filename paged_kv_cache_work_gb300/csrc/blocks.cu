@@ -18,7 +18,7 @@
 // reads them.
 //   Measured on 32 contexts of 32,768 to 131,072 tokens in pages of 64 (168 MB, 25.1 us at the copy
 // rate): 31.9 us with 12 warps an SM (8: 32.0, 16: 30.6, 48: 34.4), and 7.5 us on contexts of at
-// most 8,192 in pages of 16, where 16 warps take 8.0 and 48 take 12.0.  Pages read straight into
+// most 4,096 in pages of 16, where 16 warps take 8.0 and 48 take 12.0.  Pages read straight into
 // registers by 33, 12 and 8 warps an SM took 38, 41 and 56 us, a 512-byte bulk copy a page 50 us (the
 // copy engine takes about 40 cycles for each, however short).
 //
