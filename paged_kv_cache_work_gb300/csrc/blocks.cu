@@ -2,7 +2,9 @@
 // the best pages.
 //
 // Bounds.  One CTA per (sequence, touched page, kv head): the least and largest value of each
-// channel over the new rows, joined with the page's older bounds unless it is fresh.
+// channel over the new rows, joined with the page's older bounds unless it is fresh.  Reading the
+// rows bounds it: four rows of a thread are in flight at once (8 prompts, 33.6 MB that the append
+// has just left in L2: 8.6 us; a step of 32 tokens 2.2 us, the launch).
 //
 // Score.  For a page with channel bounds lo, hi and a query row q no key k of the page (lo_d <=
 // k_d <= hi_d) has <q, k> above sum_d max(q_d lo_d, q_d hi_d), and that is one dot product of

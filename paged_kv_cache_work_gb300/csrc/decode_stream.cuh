@@ -11,6 +11,12 @@
 // The first item is derived from the lengths with the planner's own arithmetic, so that its copies
 // and products start while the planner may still be running; nothing is written (flags included)
 // and no other item is read before the planner has finished.
+//   Measured, plan, decode and reduce: 64 sequences of 8,192 to 16,384 tokens (16 heads on one kv head
+// of 128, 202 MB) 43.1 us, 32 of 512 to 4,096 with four new tokens each (32 heads on 8, 153 MB) 36.9
+// us.  Pages stream at 6.2 TB/s once under way, bound by what two warps a scheduler issue (0.35 of a
+// slot a cycle); about 10 us are the planner, the first copies, the last items' merge and the
+// reducer.  The mma.sync kernel, whose CTAs pass tiles through one ring with barriers, took 54.4 and
+// 58.3 us.
 #pragma once
 
 #include "page_stream.cuh"

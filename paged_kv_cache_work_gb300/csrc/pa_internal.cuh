@@ -97,9 +97,9 @@ inline int decode_merge_limit(int split_merge, int path) {
 }
 
 // The streaming kernel (an fp8 cache with one scale for each page and kv head): query rows of a
-// tile, the tokens that its warps take in a round, the cost of an item in such rounds (the batched
-// shapes: 3 rounds 45.2 and 41.0 us a step, 6 rounds 43.2 and 40.1, 9 rounds 43.3 and 43.0), and
-// the most rows per kv head it takes.  At head
+// tile, the tokens that its warps take in a round, the cost of an item in such rounds (64 long
+// sequences and 32 of four new tokens: 3 rounds 44.9 and 39.3 us a step, 5 rounds 43.5 and 38.1, 7
+// rounds 42.8 and 38.9, 9 rounds 43.3 and 40.9), and the most rows per kv head it takes.  At head
 // dim 128 two tiles beat one of the mma.sync kernel (24 rows, batched GQA: 62 against 107 us; 32
 // rows, long pages: 65 against 100 us); at 256, where the tiles leave room for one CTA an SM, they
 // do not (32 rows: 95 against 81 us; one tile of 16: 73 against 86 us).  64-dim rows: always (4
