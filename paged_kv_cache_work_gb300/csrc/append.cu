@@ -10,9 +10,9 @@
 // paged-attention metadata decode" (FlyDSL PR #910, Breaking Changes: per_token_kv):
 // per-token, the row's scale is amax / 448 (1 for an all-zero row) and is written beside the
 // codes; per-tensor, the caller's one scale is read; with no scale the values are encoded as
-// they are.  (One scale for each page and kv head: append_block.cu.)  The scale and every quotient are IEEE fp32 operations (correctly rounded
-// division), and the code is the E4M3 value nearest to the quotient, ties to even, magnitudes
-// past 448 saturating to 448.
+// they are.  (One scale for each page and kv head: append_block.cu.)  The scale and every quotient
+// are IEEE fp32 operations (correctly rounded division), and the code is the E4M3 value nearest to
+// the quotient, ties to even, magnitudes past 448 saturating to 448.
 //
 // One warp per (sequence, new row, kv head): each lane holds D / 32 consecutive elements
 // (8 to 16 bytes of input), the row's amax is a shuffle reduction, and the codes go out as

@@ -27,16 +27,16 @@
 // A row tile holds whole query tokens where a group has 1, 2, 4 or 8 heads (16 / G tokens; a
 // token's maximum is up to three shuffles away); other groups take ceil(G / 16) tiles a token.
 //
-// Select.  One CTA per row: scores become order-preserving 32-bit keys, the k-th largest is found, and one ordered pass writes the pages above it and the first of those equal
-// to it.  What bounds it is the chain of block-wide steps of a row.  So the k-th key comes from one
-// histogram: 256 bins of equal width between the row's least and greatest finite score spread the
-// shared-memory atomics (a float's own upper bits fall into a few exponents: four passes of 8 bits
-// took 14.3 us for 1,024 rows of at most 2,048 pages, this takes 12.0), and the keys of the bin with
-// the k-th are few enough to rank each against all of them.  Rows that leave more than 128 in the bin
-// (ties, outliers) take the passes of 8 bits (1,024 rows of 2,048 equal scores: 18.8 us).  A warp
-// keeps a run of a row's pages in registers where the row has at most 2,048.  Of the 12.0 us the
-// reading of scores and lengths takes 5.4 (two waves of CTAs), the histogram 2.1, the bin's ranks
-// 2.2, the ordered pass 2.5.
+// Select.  One CTA per row: scores become order-preserving 32-bit keys, the k-th largest is found,
+// and one ordered pass writes the pages above it and the first of those equal to it.  What bounds
+// it is the chain of block-wide steps of a row.  So the k-th key comes from one histogram: 256 bins
+// of equal width between the row's least and greatest finite score spread the shared-memory atomics
+// (a float's own upper bits fall into a few exponents: four passes of 8 bits took 14.3 us for 1,024
+// rows of at most 2,048 pages, this takes 12.1), and the keys of the bin with the k-th are few enough
+// to rank each against all of them.  Rows that leave more than 128 in the bin (ties, outliers) take
+// the passes of 8 bits (1,024 rows of 2,048 equal scores: 18.8 us).  A warp keeps a run of a row's
+// pages in registers where the row has at most 2,048.  Of the 12.1 us the reading of lengths and
+// scores takes 5.4 (two waves of CTAs), the histogram 2.1, the bin's ranks 2.2, the ordered pass 2.5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -223,7 +223,8 @@ struct ScoreSmem {
 };
 
 template <int D, int QK>
-__global__ void __launch_bounds__(kScoreWarps * 32, ScoreSmem<D>::CTAS_PER_SM) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, ScoreSmem<D>::CTAS_PER_SM)
+    score_kernel(const ScoreParams p) {
   using M = ScoreSmem<D>;
   constexpr int NP = D / 32;  // 16-byte pieces a lane takes of each bound: two k-steps each
   extern __shared__ __align__(128) char smem[];
@@ -723,9 +724,18 @@ extern "C" pa_status pa_score_blocks(const pa_config* cfg, const void* q, const 
   const bool half = c.q_dtype == PA_FP16;
   cudaError_t e;
   switch (c.head_dim) {
-    case 64: e = half ? go(score_kernel<64, Q_FP16>, done[0], ScoreSmem<64>::BYTES) : go(score_kernel<64, Q_BF16>, done[1], ScoreSmem<64>::BYTES); break;
-    case 128: e = half ? go(score_kernel<128, Q_FP16>, done[2], ScoreSmem<128>::BYTES) : go(score_kernel<128, Q_BF16>, done[3], ScoreSmem<128>::BYTES); break;
-    default: e = half ? go(score_kernel<256, Q_FP16>, done[4], ScoreSmem<256>::BYTES) : go(score_kernel<256, Q_BF16>, done[5], ScoreSmem<256>::BYTES); break;
+    case 64:
+      e = half ? go(score_kernel<64, Q_FP16>, done[0], ScoreSmem<64>::BYTES)
+               : go(score_kernel<64, Q_BF16>, done[1], ScoreSmem<64>::BYTES);
+      break;
+    case 128:
+      e = half ? go(score_kernel<128, Q_FP16>, done[2], ScoreSmem<128>::BYTES)
+               : go(score_kernel<128, Q_BF16>, done[3], ScoreSmem<128>::BYTES);
+      break;
+    default:
+      e = half ? go(score_kernel<256, Q_FP16>, done[4], ScoreSmem<256>::BYTES)
+               : go(score_kernel<256, Q_BF16>, done[5], ScoreSmem<256>::BYTES);
+      break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
