@@ -440,11 +440,12 @@ __device__ __forceinline__ float fast_log2(float x) {
 }
 
 // V scales that differ between pages enter the f16 weights P, so they are taken relative to a
-// power of two above the largest so far (the accumulator is in units of it): a weight then keeps
-// its 11 bits however small the scales are.  A weight is at most 2^8 before its scale, so kPLift
-// = 2^7 more keeps it below f16's 65504 and moves f16's subnormals, where a weight loses bits,
-// down to 2^-21 of the largest.  pow2_above: the least power of two above x >= 0, within
-// [2^-118, 2^125] (so that kPLift times the inverse is finite); pow2_inverse: its exact inverse.
+// power of two, vref, that the accumulator is in units of.  A weight is at most 2^8 before its
+// scale, so kPLift = 2^7 more keeps it below f16's 65504; a scale is at least kVRange = 2^-8 of
+// vref, so a weight has its 11 bits from 2^-13 of the row's largest on.  vref moves up and down
+// with the scales (move_v_unit), whatever weight their pages have: a page of zeros may have any
+// scale.  pow2_above: the least power of two above x >= 0, within [2^-118, 2^125] (so that kPLift
+// times the inverse is finite); pow2_inverse: its exact inverse.
 constexpr float kPLift = 128.f;
 constexpr float kPow2Least = 3.009265538105056e-36f;  // 2^-118
 __device__ __forceinline__ float pow2_above(float x) {
@@ -453,6 +454,18 @@ __device__ __forceinline__ float pow2_above(float x) {
 }
 __device__ __forceinline__ float pow2_inverse(float x) {
   return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+
+// The accumulators' unit vref to the power of two above the scale x, and the factor (exact, a power
+// of two) that brings the accumulators along.  Not below 2^-60 of the largest unit so far, vtop:
+// an accumulator is a sum of fewer than 2^31 terms below 2^8 * 448 * kPLift * 2^60, so it stays
+// below 2^115; weights of pages with a scale below 2^-68 of the largest lose bits.
+constexpr float kVRange = 1.f / 256.f;
+__device__ __forceinline__ float move_v_unit(float x, float& vref, float& vtop) {
+  const float to = fmaxf(pow2_above(x), vtop * 0x1p-60f), f = vref * pow2_inverse(to);
+  vref = to;
+  vtop = fmaxf(vtop, to);
+  return f;
 }
 
 // Packed fp32x2 multiply-add (sm_100 family): d = a * b + c, lane-wise on float2.

@@ -235,6 +235,48 @@ def test_tiny_and_huge_scales_lose_nothing(sq, hq, hkv, d, cuda_device, pa):
                                 2.0 ** -11, 1.1e-4)
 
 
+# ---- scales that lie far apart ----------------------------------------------------------------
+def far_scales(rng, p, kind, ratio):
+    """Half of the pages, first ones among them, get a V scale 1 / ratio times the others' and no
+    part in the output: they hold zeros ("zeros": what an append of zeros leaves, with its scale of
+    1) or keys whose logits lie far below every other ("low")."""
+    nblocks = p["vs"].shape[0]
+    far = torch.from_numpy(rng.random(nblocks) < 0.5)
+    for b in range(len(p["ctx"])):
+        if p["ctx"][b]:
+            far[p["bt"][b, 0]] = True
+            far[p["bt"][b, plain64.pages(p["ctx"][b], p["kc"].shape[1]) - 1]] = False
+    p["vs"] = torch.where(far[:, None], p["vs"] / ratio, p["vs"])
+    if kind == "zeros":
+        p["vc"][far] = 0
+    else:  # keys of -448 * 0.03 in every channel against queries above zero: logits below -80
+        p["q"] = p["q"].abs()
+        p["kc"][far] = 0xfe
+        p["ks"][far] = 0.03
+
+
+FAR = [
+    # Sq, Hq, Hkv, D, bs, dtype, longest
+    (1, 8, 2, 128, 16, "bf16", 300), (2, 8, 2, 128, 32, "fp16", 300), (2, 8, 2, 64, 16, "bf16", 300),
+    (1, 4, 1, 256, 16, "fp16", 200),
+]
+
+
+# Weights keep f16's half step (2^-11) whatever the other pages' scales are.
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["zeros", "low"])
+@pytest.mark.parametrize("sq,hq,hkv,d,bs,dtype,longest", FAR)
+def test_a_page_of_far_larger_scale_costs_the_others_nothing(sq, hq, hkv, d, bs, dtype, longest, kind, cuda_device, pa):
+    for ratio in (1e-5, 1e-7, 1e-9, 1e-14):
+        rng = np.random.default_rng(21)
+        p = decode_problem(13, 2, sq, hq, hkv, d, bs, longest, dtype, 1)
+        far_scales(rng, p, kind, ratio)
+        cfg = config(2, sq, hq, hkv, d, bs, p["maxb"], p["nblocks"], dtype, 1)
+        out, lse = run_decode(pa, p, cfg, cuda_device)
+        ref, ref_lse, size = reference(p, 1, float(np.float32(d ** -0.5)))
+        plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, 2.0 ** -11)
+
+
 @pytest.mark.gpu
 def test_equal_scales_are_the_per_token_cache(cuda_device, pa):
     """The same scale on every page, given per page and per token: the same attention."""

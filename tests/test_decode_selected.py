@@ -202,6 +202,33 @@ def test_ranges_that_leave_f16(d, cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["zeros", "low"])
+@pytest.mark.parametrize("d,bs,mode,dtype", [(128, 16, "block", "bf16"), (64, 64, "block", "fp16"), (64, 16, "block", "bf16"),
+                                             (256, 16, "block", "bf16"), (128, 32, "token", "fp16"), (256, 16, "token", "bf16")])
+def test_far_larger_scales_cost_the_others_nothing(d, bs, mode, dtype, kind, cuda_device, pa):
+    """Half of the pages (or tokens) get a V scale 1 / ratio times the others' and no part in the
+    output, as they hold zeros or keys whose logits lie far below every other: the others keep
+    their weights' bits."""
+    for ratio in (1e-5, 1e-7, 1e-9, 1e-14):
+        p = problem(15, 2, 2, 8, 2, d, bs, 400, 20, 0, dtype, "8", mode, 1)
+        rng = np.random.default_rng(16)
+        far = torch.from_numpy(rng.random(p["vs"].shape[:1] if mode == "block" else p["vs"].shape[:2]) < 0.5)
+        p["vs"][far] /= ratio
+        if kind == "zeros":
+            p["vc"][far] = 0
+        else:  # keys of -448 * 0.04 in every channel against queries above zero: logits below -80
+            p["q"] = p["q"].abs()
+            p["kc"][far] = 0xfe
+            p["ks"][far] = 0.04
+            for b in range(2):  # (a row that sees far keys alone would be theirs: list some of the others)
+                p["sel"][b, :, :, 0] = next(x for x in range(p["maxb"]) if not far[p["bt"][b, x]].all())
+        cfg = config(2, 2, 8, 2, d, bs, p["maxb"], p["nblocks"], dtype, "8", mode)
+        out, lse = run(p, cfg, cuda_device)
+        ref, ref_lse, size = reference(p, 0, d, mode)
+        plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, **rounding("8", dtype))
+
+
+@pytest.mark.gpu
 def test_a_cache_past_32_bits_of_elements(cuda_device, pa):
     """Pages beyond element 2^31 of the cache (and of the fp8 one's bytes)."""
     B, hq, hkv, d, bs = 1, 4, 2, 128, 1024
