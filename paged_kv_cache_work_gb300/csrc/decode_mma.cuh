@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
     }
 
     float o[WR][NB][4];
-    float vref = kPow2Least;  // one V scale a page: o is in units of vref / kPLift
+    float vref = kPow2Least, vtop = kPow2Least;  // one V scale a page: o is in units of vref / kPLift
     float m_run[WR][2], l_run[WR][2];
 #pragma unroll
     for (int w = 0; w < WR; ++w) {
@@ -377,9 +377,8 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
         if constexpr (T::BLKS) {
           qk_chunk *= sks[c0];
           const float vs = svs[c0];
-          if (fabsf(vs) > vref) {  // warp-uniform
-            const float up = pow2_above(fabsf(vs)), f = vref * pow2_inverse(up);
-            vref = up;
+          if (fabsf(vs) > vref || (fabsf(vs) > 0.f && fabsf(vs) < vref * kVRange)) {  // warp-uniform
+            const float f = move_v_unit(fabsf(vs), vref, vtop);
 #pragma unroll
             for (int w = 0; w < WR; ++w)
 #pragma unroll

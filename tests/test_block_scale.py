@@ -258,7 +258,7 @@ def far_scales(rng, p, kind, ratio):
 FAR = [
     # Sq, Hq, Hkv, D, bs, dtype, longest
     (1, 8, 2, 128, 16, "bf16", 300), (2, 8, 2, 128, 32, "fp16", 300), (2, 8, 2, 64, 16, "bf16", 300),
-    (1, 4, 1, 256, 16, "fp16", 200),
+    (1, 4, 1, 256, 16, "fp16", 200), (10, 4, 2, 256, 16, "bf16", 200), (20, 16, 8, 256, 32, "fp16", 200),
 ]
 
 
