@@ -308,11 +308,63 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float a, float b) {
       : "f"(b), "f"(a));
   return r;
 }
+// Eight f16 values times f.
+__device__ __forceinline__ void scale_h2(uint4& x, __half2 f) {
+  __half2* h = reinterpret_cast<__half2*>(&x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = __hmul2(h[j], f);
+}
 // Two E4M3 codes (low byte first) to an f16 pair (exact).
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
   __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
+
+// One V scale v for each page, with 2^top above the largest of an item's pages.  Weights are f16, at
+// most 2^8 before their scale.  Where an item's scales lie within 2^8 of one another the weights take
+// v 2^(7 - top), at least 2^-2, and the codes are widened as they are.  Where they do not (a page
+// of zeros, or one that no row looks at, may have any scale) v is split over both operands of the
+// PV MMA by exact powers of two: the widened codes take 2^shift, at most 2^7 (448 * 2^7 is below
+// f16's 65504) and at least 2^-15 (the least code, 2^-9, is then f16's least subnormal, so every
+// code stays exact), and the weights the rest, v 2^(14 - top - shift), which is in [2^6, 2^7) while
+// shift has room.  A weight then has its 11 bits from 2^-20 of the row's largest on for a scale of
+// 2^-22 of the item's largest, from 2^-12 on for one of 2^-30.
+struct VScales {
+  int top;
+  bool wide;
+  // top >= -98 where v is split, so that a weight takes at most 2^(14 + 98 + 15) v
+  __device__ __forceinline__ void of_item(const KernelParams& p, int b, int g, int t0, int t1, int lane) {
+    float big = 0.f, small = INFINITY;
+    for (int pg = (t0 >> p.bs_shift) + lane; pg <= (t1 - 1) >> p.bs_shift; pg += 32) {
+      const int blk = __ldg(p.bt + (size_t)b * p.maxb + pg);
+      if (blk >= 0 && blk < p.nblocks) {
+        const float v = fabsf(__ldg(p.v_scale + (size_t)blk * p.Hkv + g));
+        big = fmaxf(big, v);
+        small = fminf(small, v > 0.f ? v : INFINITY);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+      small = fminf(small, __shfl_xor_sync(kFull, small, o));
+    }
+    wide = small < big * kVRange;
+    top = max((int)(__float_as_uint(pow2_above(big)) >> 23) - 127, wide ? -98 : -118);
+  }
+  static __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+  __device__ __forceinline__ int lift() const { return wide ? 14 : 7; }
+  // O is in units of this
+  __device__ __forceinline__ float unit() const { return pow2(top - lift()); }
+  __device__ __forceinline__ int shift(float v) const {
+    const int e = (int)((__float_as_uint(v) >> 23) & 255) - 127;  // |v| in [2^e, 2^(e + 1))
+    return wide ? min(max(e + 8 - top, -15), 7) : 0;
+  }
+  // (finite, as zero weights have to stay zero; a weight of more than f16 holds becomes infinite)
+  __device__ __forceinline__ float of_weights(float v) const {
+    const float w = v * pow2(lift() - top - shift(v));
+    return fmaxf(fminf(w, 3.402823466e38f), -3.402823466e38f);
+  }
+};
 
 // 32 lanes x 32 bits x 64 columns: thread t of warp w gets columns [col, col + 64) of lane
 // 32 (w % 4) + t, with one wait.
@@ -704,7 +756,7 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
     }
     for (int b = 0; b < T::NSC; ++b) {
       mbar_init(&sc_full[b], 32);  // one cp.async arrival per producer lane
-      mbar_init(&sc_free[b], 4);   // the four softmax warps
+      mbar_init(&sc_free[b], T::BLKS ? 4 + T::NCW : 4);  // the softmax (and widening) warps
     }
     mbar_init(o_free, 4);
     mbar_init(q_full, 4);
@@ -1018,21 +1070,8 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
 
-      // one V scale a page: weights take the scale over a power of two above the item's largest
-      float vref = 1.f, vinv = 1.f;
-      if constexpr (T::BLKS) {
-        float big = 0.f;
-        for (int pg = (t0 >> p.bs_shift) + lane; pg <= (t1 - 1) >> p.bs_shift; pg += 32) {
-          const int blk = __ldg(p.bt + (size_t)b * p.maxb + pg);
-          if (blk >= 0 && blk < p.nblocks)
-            big = fmaxf(big, fabsf(__ldg(p.v_scale + (size_t)blk * p.Hkv + g_kv)));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-        vref = pow2_above(big);
-        vinv = pow2_inverse(vref) * kPLift;
-        vref *= 1.f / kPLift;
-      }
+      VScales vscales{0, false};  // one V scale a page
+      if constexpr (T::BLKS) vscales.of_item(p, b, g_kv, t0, t1, lane);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nsub; ++j, ++g) {
         const int tok0 = t0 + j * SUB, nv = min(SUB, t1 - tok0);  // tokens of the item here
@@ -1135,6 +1174,11 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
             const float2 one2 = make_float2(1.f, 1.f);
             float2 ls2 = z2;
             const float* svs = sks + T::TT;
+            float vw[T::BLKS ? NL / 16 : 1];  // one scale a page: its part in the weights
+            if constexpr (T::BLKS) {
+#pragma unroll
+              for (int q = 0; q < NL / 16; ++q) vw[q] = vscales.of_weights(svs[c0 + 16 * q]);
+            }
 #pragma unroll
             for (int h = 0; h < NL / 32; ++h) {  // 32 tokens = 16 columns at a time
               uint32_t pk[16];
@@ -1143,19 +1187,19 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
                 const float2 t = ffma2(make_float2(x[32 * h + 2 * i], x[32 * h + 2 * i + 1]), one2, nm);
                 float p0 = fast_exp2(t.x), p1 = fast_exp2(t.y);
                 ls2 = ffma2(make_float2(p0, p1), one2, ls2);
-                if constexpr (T::TOKS) {
-                  // the value row's scale enters P (a stale scale past the item's tokens meets
-                  // a zero weight and is dropped)
+                // the value row's scale enters P (a stale scale past the item's tokens meets a
+                // zero weight and is dropped)
+                if constexpr (T::BLKS) {
+                  const float v = vw[(32 * h + 2 * i) / 16];
+                  const float2 pv = ffma2(make_float2(p0, p1), make_float2(v, v), z2);
+                  p0 = pv.x;
+                  p1 = pv.y;
+                } else if constexpr (T::TOKS) {
                   const float2 v2 =
                       SC_REG ? make_float2(vsc[32 * h + 2 * i], vsc[32 * h + 2 * i + 1])
                              : *reinterpret_cast<const float2*>(svs + c0 + 32 * h + 2 * i);
-                  if constexpr (T::BLKS) {
-                    p0 = p0 == 0.f ? 0.f : p0 * (v2.x * vinv);
-                    p1 = p1 == 0.f ? 0.f : p1 * (v2.y * vinv);
-                  } else {
-                    p0 = p0 == 0.f ? 0.f : p0 * v2.x;
-                    p1 = p1 == 0.f ? 0.f : p1 * v2.y;
-                  }
+                  p0 = p0 == 0.f ? 0.f : p0 * v2.x;
+                  p1 = p1 == 0.f ? 0.f : p1 * v2.y;
                 }
                 pk[i] = pack16x2<BF>(p0, p1);
               }
@@ -1244,7 +1288,7 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
         }
       }
       if (!DUAL || hs == 0) {
-        float inv = l_run > 0.f ? (T::BLKS ? vref : vts) / l_run : 0.f;
+        float inv = l_run > 0.f ? (T::BLKS ? vscales.unit() : vts) / l_run : 0.f;
         float lse2 = l_run > 0.f ? m_run + fast_log2(l_run) : -INFINITY;
         // piece 0 finishing the unit: merged with pieces 1 .. ns-1 in the arithmetic of
         // merge_unit
@@ -1354,7 +1398,8 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
       // widening set the step's pace (measured: per-tensor fp8 Sq = 4 decode 94.8 us ->
       // 83.5 us; writing the second slab's two chunks in the opposite order, to spread the
       // stores over the banks, measured slower).
-      auto widen = [&](const char* src, char* dst, int nv) {
+      // shifted(k, lo, hi): what the sixteen values of chunk k take of their page's scale
+      auto widen = [&](const char* src, char* dst, int nv, auto shifted) {
         constexpr int NIT = SUB * 8 / (32 * T::NCW);
         uint4 w[NIT];
 #pragma unroll
@@ -1368,10 +1413,11 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
         for (int k = 0; k < NIT; ++k) {
           const int e = ctid + k * 32 * T::NCW;
           const int rr = e >> 3, c = e & 7;
-          const uint4 lo = make_uint4(e4m3x2_to_h2(w[k].x), e4m3x2_to_h2(w[k].x >> 16),
-                                      e4m3x2_to_h2(w[k].y), e4m3x2_to_h2(w[k].y >> 16));
-          const uint4 hi = make_uint4(e4m3x2_to_h2(w[k].z), e4m3x2_to_h2(w[k].z >> 16),
-                                      e4m3x2_to_h2(w[k].w), e4m3x2_to_h2(w[k].w >> 16));
+          uint4 lo = make_uint4(e4m3x2_to_h2(w[k].x), e4m3x2_to_h2(w[k].x >> 16),
+                                e4m3x2_to_h2(w[k].y), e4m3x2_to_h2(w[k].y >> 16));
+          uint4 hi = make_uint4(e4m3x2_to_h2(w[k].z), e4m3x2_to_h2(w[k].z >> 16),
+                                e4m3x2_to_h2(w[k].w), e4m3x2_to_h2(w[k].w >> 16));
+          shifted(k, lo, hi);
           // dims 16c .. 16c + 15 -> f16 slab c / 4, chunks 2 (c % 4) and 2 (c % 4) + 1
           char* d = dst + (c >> 2) * T::CV_SLAB;
           *reinterpret_cast<uint4*>(d + sw128_chunk(rr, 2 * (c & 3))) = lo;
@@ -1388,6 +1434,9 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
         const int t0 = item.y, t1 = item.z;
         if (t1 <= t0) continue;
         const int nsub = ceil_div(t1 - t0, SUB);
+        const int unit = item.x / p.RB;  // sequence and kv head
+        VScales vscales{0, false};
+        if constexpr (T::BLKS) vscales.of_item(p, unit / p.Hkv, unit % p.Hkv, t0, t1, lane);
         for (int j = 0; j < nsub; ++j, ++g) {
           const int nv = min(SUB, t1 - (t0 + j * SUB));
           const int vslot = (int)(g % T::NV);
@@ -1397,10 +1446,30 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
             const uint32_t x = g - NSP;
             wait_bar(&pv_done[x % NSP], (x / NSP) & 1);
           }
-          widen(smem + T::OFF_V + vslot * T::SLOT, smem + T::OFF_CV + (g % NSP) * T::CV_BUF, nv);
+          const char* src = smem + T::OFF_V + vslot * T::SLOT;
+          char* dst = smem + T::OFF_CV + (g % NSP) * T::CV_BUF;
+          if constexpr (T::BLKS) {
+            // a thread's chunk k lies in rows 16 k .. 16 k + 15, which share a page's scale (rows past
+            // the item's tokens are zeros, and their page has no scale here)
+            static_assert(32 * T::NCW == 16 * 8, "16 rows a pass");
+            const float* sc =
+                reinterpret_cast<const float*>(smem + T::OFF_SC + (g % T::NSC) * T::SC_SLOT) + T::TT;
+            if (vscales.wide) {
+              wait_bar(&sc_full[g % T::NSC], (g / T::NSC) & 1);
+              widen(src, dst, nv, [&](int k, uint4& lo, uint4& hi) {
+                const __half2 f = __float2half2_rn(16 * k < nv ? VScales::pow2(vscales.shift(sc[16 * k])) : 1.f);
+                scale_h2(lo, f);
+                scale_h2(hi, f);
+              });
+            }
+          }
+          if (!vscales.wide) widen(src, dst, nv, [](int, uint4&, uint4&) {});
           if (lane == 0) {
             mbar_arrive(&cv_full[g % NSP]);
             mbar_arrive(&empty_v[vslot]);
+            // (a slot's previous use has long been released by the softmax: the PV of four steps
+            // back, which the widening waits for, came after it)
+            if constexpr (T::BLKS) mbar_arrive(&sc_free[g % T::NSC]);
           }
         }
       }
