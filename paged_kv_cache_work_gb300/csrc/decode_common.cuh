@@ -34,8 +34,6 @@ struct KernelParams {
   int units;
   int ns_dec;  // split units of at most this many pieces are merged here (see merge_if_last)
   int scale_mode;
-  long long sc_block;  // staged scales: the scale of (block, slot, head g) sits at
-  int sc_slot;         // block * sc_block + slot * sc_slot + g
   int Sq, Hq, Hkv, G, M, RB, bs, maxb, nblocks, causal;
   int bs_shift;  // log2(bs): pages are a power of two
   float qk_scale;
@@ -203,8 +201,6 @@ struct TileProducer {
   static constexpr int D = R::D;
   static constexpr int MP = R::MP;
   static constexpr bool TOKS = R::TOKS;
-  // staged scales: one for every token, or one for every 16-token chunk (at its first token)
-  static constexpr int SSTEP = R::BLKS ? 16 : 1;
   const KernelParams* p;
   const CUtensorMap* kmap;
   const CUtensorMap* vmap;
@@ -316,8 +312,8 @@ struct TileProducer {
     // per-token scales of one kv head on a page that holds the whole tile: two contiguous
     // runs of TT floats, copied by two bulk copies that complete on the stage's barrier
     bool scale_bulk = false, ok0 = false;
-    if constexpr (TOKS) {
-      scale_bulk = p->sc_slot == 1 && box_rows == T::TT &&
+    if constexpr (TOKS && !R::BLKS) {
+      scale_bulk = p->Hkv == 1 && box_rows == T::TT &&
                    ((reinterpret_cast<uintptr_t>(p->k_scale) |
                      reinterpret_cast<uintptr_t>(p->v_scale)) & 15) == 0;
       ok0 = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;  // lane 0's box is the tile's one page
@@ -348,15 +344,27 @@ struct TileProducer {
         if (++k >= ntiles) have = false;
         return true;
       }
-      for (int first = 0; first < T::TT; first += 32 * SSTEP) {
-        const int t = first + lane * SSTEP;
-        const int bb = __shfl_sync(kFull, blk, t < T::TT ? (t / box_rows) * T::NSLAB : 0);
-        const int tok = tok0 + t;
-        if (t < T::TT && tok < t1 && bb >= 0 && bb < p->nblocks) {
-          const size_t idx =
-              (size_t)(bb * p->sc_block) + (size_t)((tok & (p->bs - 1)) * p->sc_slot) + g;
-          cp_async_4(sks + t, p->k_scale + idx);
-          cp_async_4(svs + t, p->v_scale + idx);
+      if constexpr (R::BLKS) {  // a page's one scale, at the first token of each 16-token chunk
+        for (int first = 0; first < T::TT; first += 32 * 16) {
+          const int t = first + lane * 16;
+          const int bb = __shfl_sync(kFull, blk, t < T::TT ? (t / box_rows) * T::NSLAB : 0);
+          if (t < T::TT && tok0 + t < t1 && bb >= 0 && bb < p->nblocks) {
+            const size_t idx = (size_t)bb * p->Hkv + g;
+            cp_async_4(sks + t, p->k_scale + idx);
+            cp_async_4(svs + t, p->v_scale + idx);
+          }
+        }
+      } else {
+        // (blk bs + slot) Hkv + g, with the product that is known beforehand taken out
+        const long long block = (long long)p->bs * p->Hkv;
+        for (int t = lane; t < T::TT; t += 32) {
+          const int bb = __shfl_sync(kFull, blk, (t / box_rows) * T::NSLAB);
+          const int tok = tok0 + t;
+          if (tok < t1 && bb >= 0 && bb < p->nblocks) {
+            const size_t idx = (size_t)(bb * block) + (size_t)(tok & (p->bs - 1)) * p->Hkv + g;
+            cp_async_4(sks + t, p->k_scale + idx);
+            cp_async_4(svs + t, p->v_scale + idx);
+          }
         }
       }
       cp_async_arrive_noinc(&full[s]);

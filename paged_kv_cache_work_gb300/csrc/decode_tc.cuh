@@ -469,8 +469,6 @@ struct TcProducer {
   const int4* items;
   const float* kscale;
   const float* vscale;
-  long long sc_block;  // strides of the staged scales (see KernelParams)
-  int sc_slot;
   int maxb, bs, bs_shift, nblocks, Hkv, RB;
   int lane, box_rows, nbox;
   uint32_t box_bytes, nk, nv, nsc;
@@ -493,11 +491,10 @@ struct TcProducer {
     flags = sflags; bt = prm->bt; items = prm->items; kscale = prm->k_scale;
     vscale = prm->v_scale; maxb = prm->maxb; bs = prm->bs; bs_shift = prm->bs_shift;
     nblocks = prm->nblocks; Hkv = prm->Hkv; RB = prm->RB;
-    sc_block = prm->sc_block; sc_slot = prm->sc_slot;
     box_rows = min(bs, T::TT);
     nbox = T::TT / box_rows;
     box_bytes = (uint32_t)box_rows * T::ROWB;
-    scale_bulk = T::TOKS && sc_slot == 1 && box_rows == T::TT &&
+    scale_bulk = T::TOKS && !T::BLKS && Hkv == 1 && box_rows == T::TT &&
                  ((reinterpret_cast<uintptr_t>(kscale) | reinterpret_cast<uintptr_t>(vscale)) & 15) == 0;
     nk = nv = nsc = 0;
     list.init(*prm, first);
@@ -631,7 +628,8 @@ struct TcProducer {
           const bool ok = __shfl_sync(kFull, bx.ok ? 1 : 0, src) != 0;
           const int tok = bx.tok0 + t;
           if (ok && tok < bx.t1) {
-            const size_t idx = (size_t)(blk * sc_block) + (size_t)((tok & (bs - 1)) * sc_slot) + bx.g;
+            const size_t idx = T::BLKS ? (size_t)blk * Hkv + bx.g
+                                       : ((size_t)blk * bs + (tok & (bs - 1))) * Hkv + bx.g;
             cp_async_4(ks + t, kscale + idx);
             cp_async_4(vs + t, vscale + idx);
           }

@@ -76,9 +76,6 @@ KernelParams make_kernel_params(const DecodeArgs& a) {
   p.units = a.v.units;
   p.ns_dec = a.v.ns_dec;
   p.scale_mode = a.scale_mode;
-  const bool per_block = a.scale_mode == PA_SCALE_PER_BLOCK;
-  p.sc_slot = per_block ? 0 : a.p.num_kv_heads;
-  p.sc_block = (long long)a.p.num_kv_heads * (per_block ? 1 : a.p.block_size);
   p.Sq = a.p.max_q_len;
   p.Hq = a.p.num_q_heads;
   p.Hkv = a.p.num_kv_heads;
