@@ -332,7 +332,9 @@ PA_API pa_status pa_append_kv(const pa_config *cfg, const void *k_new, const voi
  *                   or more free pages than num_blocks after the pushes) and
  *                   PA_FLAG_NO_FREE_BLOCKS: nothing is given or taken, new_held and
  *                   new_free_count are copies and every slot is -1.  PA_FLAG_BAD_BLOCK_ID: a page
- *                   in use lies outside [0, num_blocks); its tokens' slots are -1
+ *                   given or taken (it moves all the same) or, with a slot_map, a page of a new
+ *                   token lies outside [0, num_blocks); its tokens' slots are -1.  Pages that stay
+ *                   where they are and hold no new token are not looked at
  *
  * Stream-ordered, allocates nothing, never synchronises.  No two arrays may overlap.
  * PA_ERR_UNSUPPORTED for batch > 4096, a block_size outside the decode's set, or tables or slot

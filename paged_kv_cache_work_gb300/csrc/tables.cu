@@ -151,14 +151,20 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(const TablesPara
     const int at = top - 1 - k;
     return at < F ? p.free_blocks[at] : given(at - F);
   };
-  for (long long k = gtid; k < A; k += threads) {
-    const int b = owner_of(s_take, B, (int)k);
-    p.bt[(size_t)b * p.maxb + s_held[b] + ((int)k - s_take[b])] = taken((int)k);
-  }
-  for (long long r = gtid; r < R - A; r += threads)  // the given pages that nobody takes
-    p.free_blocks[F + r] = given((int)r);
-
+  // an id outside the pool moves as any other does, and is flagged where it moves
+  auto outside = [&](int id) { return id < 0 || id >= p.nblocks; };
   bool bad_id = false;
+  for (long long k = gtid; k < A; k += threads) {
+    const int b = owner_of(s_take, B, (int)k), id = taken((int)k);
+    bad_id |= outside(id);
+    p.bt[(size_t)b * p.maxb + s_held[b] + ((int)k - s_take[b])] = id;
+  }
+  for (long long r = gtid; r < R - A; r += threads) {  // the given pages that nobody takes
+    const int id = given((int)r);
+    bad_id |= outside(id);
+    p.free_blocks[F + r] = id;
+  }
+
   for (long long e = gtid; e < total; e += threads) {
     const int b = (int)p.sq_div.div((uint32_t)e), i = (int)e - b * p.Sq;
     const int q = s_q[b];
@@ -166,10 +172,10 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(const TablesPara
     if (i < q) {
       const int pos = s_n[b] - q + i, page = pos >> p.bs_shift, h = s_held[b];
       const int id = page < h ? p.bt[(size_t)b * p.maxb + page] : taken(s_take[b] + page - h);
-      if (id >= 0 && id < p.nblocks)
-        slot = ((int64_t)id << p.bs_shift) + (pos & (bs - 1));
-      else
+      if (outside(id))
         bad_id = true;
+      else
+        slot = ((int64_t)id << p.bs_shift) + (pos & (bs - 1));
     }
     p.slots[e] = slot;
   }

@@ -156,6 +156,31 @@ def test_a_page_outside_the_pool_gets_no_slot(cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("slots", [True, False])
+@pytest.mark.parametrize("bad", [-1, 5, 1 << 30])
+@pytest.mark.parametrize("how", ["freed", "handed on", "taken"])
+def test_a_page_outside_the_pool_is_flagged_where_it_moves(how, bad, slots, cuda_device, pa):
+    """Given back to the free list, given to another row, or taken from the free list by a row
+    without new tokens: each is flagged, with and without a slot map."""
+    p = dict(n=np.array([16, 0]), q=np.array([0, 0]), held=np.array([3, 0]), bt=np.array([[4, 0, 2], [-1] * 3]),
+             free=np.array([1, 3, -7, -7, -7]), count=2, nblocks=5, maxb=3)
+    if how == "taken":
+        p["free"][1] = bad
+        p["held"][0], p["n"][1] = 1, 30
+    else:
+        p["bt"][0, 1 if how == "freed" else 2] = bad
+        p["n"][1] = 0 if how == "freed" else 20  # (row 1 takes the pages pushed last)
+    want = plain(p, 16, 1)
+    moved = want[0][1][:want[2][1]] + want[1][:want[3]]
+    assert bad in moved and (how == "freed") == (bad not in want[0][1][:want[2][1]])
+    flags = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    d, nh, nc, _ = call(pa, p, 1, 16, cuda_device, flags=flags, slots=slots)
+    assert int(flags.item()) == pa.FLAG_BAD_BLOCK_ID
+    assert d["bt"].cpu().tolist() == want[0] and nh.cpu().tolist() == want[2] and int(nc.item()) == want[3]
+    assert d["free"].cpu().tolist()[:want[3]] == want[1][:want[3]]
+
+
+@pytest.mark.gpu
 def test_captured_and_replayed_with_other_lengths(cuda_device, pa):
     p = problem(7, 30, 4, 16, 300, spare=300)
     d = on_gpu(p, cuda_device)
