@@ -185,6 +185,37 @@ def test_odd_lists(kv, mode, cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv,mode", [("16", "none"), ("8", "none"), ("8", "tensor"), ("8", "token"), ("8", "block")])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 32), (256, 16)])
+def test_a_listed_bad_block_is_skipped(d, bs, kv, mode, cuda_device, pa):
+    """A listed page whose block lies outside the pool, alone in its list, first, last and between
+    others: flagged and left out, and no other row changes a bit."""
+    p = problem(17, 2, 2, 8, 2, d, bs, 400, 12, 1, kv=kv, mode=mode)
+    p["ctx"][:], p["ql"][:] = 400, 2
+    p["bt"] = np.random.default_rng(18).integers(0, p["nblocks"], (2, plain64.pages(400, bs)))
+    p["maxb"] = p["bt"].shape[1]
+    if kv == "16":
+        for c in (p["kc"], p["vc"]):
+            c[~torch.isfinite(c)] = 0.5
+    bad = 5
+    p["sel"][:] = -1
+    for g, row in enumerate(([bad], [bad, 2, 7, 1], [3, 8, 6, bad], [0, 4, bad, 9, 3])):
+        p["sel"][0, g // 2, g % 2, :len(row)] = row
+        p["num"][0, g // 2, g % 2] = len(row)
+    p["sel"][1, :, :, :3], p["num"][1] = (1, 2, 3), 3
+    cfg = config(2, 2, 8, 2, d, bs, p["maxb"], p["nblocks"], kv=kv, mode=mode, causal=1)
+    good, _ = run(p, cfg, cuda_device)
+    lists = lambda b, i, g: [x for x in p["sel"][b, i, g, :p["num"][b, i, g]] if b or x != bad]  # noqa: E731
+    ref, ref_lse, size = reference(p, 1, d, mode, lists)
+    for block in (-1, p["nblocks"], 1 << 30):
+        spoilt = dict(p, bt=p["bt"].copy())
+        spoilt["bt"][0, bad] = block
+        out, lse = run(spoilt, cfg, cuda_device, pa.FLAG_BAD_BLOCK_ID)
+        plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, **rounding(kv, "bf16"))
+        assert torch.equal(out[1], good[1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_ranges_that_leave_f16(d, cuda_device, pa):
     """Queries of 1e6 or 1e-6 with keys that make up for it, V scales of 1e-7 and 1e6, and scales
