@@ -153,66 +153,6 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def plan(cfg: PaConfig, block_tables, context_lens, q_lens, ws, stream=None):
-    _check("pa_plan", load().pa_plan(ctypes.byref(cfg), _ptr(block_tables), _ptr(context_lens),
-                                     _ptr(q_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
-
-
-def decode(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-           q_lens, out, lse, ws, stream=None):
-    _check("pa_decode", load().pa_decode(
-        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_tables), _ptr(context_lens), _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(ws),
-        _nbytes(ws), _stream(stream)))
-
-
-def reduce(cfg: PaConfig, out, lse, ws, stream=None):
-    _check("pa_reduce", load().pa_reduce(ctypes.byref(cfg), _ptr(out), _ptr(lse), _ptr(ws),
-                                         _nbytes(ws), _stream(stream)))
-
-
-def read_flags(ws, stream=None) -> int:
-    """Synchronise and return the device flags of the last step run in ``ws``."""
-    f = ctypes.c_int32(0)
-    st = load().pa_read_flags(_ptr(ws), _nbytes(ws), ctypes.byref(f), _stream(stream))
-    if st not in (OK, ERR_DEVICE):
-        raise PaError("pa_read_flags", st)
-    return f.value
-
-
-def decode_step_static(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                       context_lens, q_lens, out, lse, stream=None):
-    """One decode step on the library's static device scratch, for callers that cannot
-    allocate device memory (no workspace argument; see pa_decode_step_static in pa.h)."""
-    _check("pa_decode_step_static", load().pa_decode_step_static(
-        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_tables), _ptr(context_lens), _ptr(q_lens), _ptr(out), _ptr(lse),
-        _stream(stream)))
-
-
-def gather_kv(cfg: PaConfig, k_cache, v_cache, block_tables, context_lens, k_out, v_out,
-              max_rows: int, row_offsets=None, flags=None, stream=None):
-    """Paged -> contiguous copy of the batch's K and V rows (see pa_gather_kv in pa.h):
-    sequence b lands at rows row_offsets[b] .. row_offsets[b + 1] - 1 of k_out and v_out."""
-    _check("pa_gather_kv", load().pa_gather_kv(
-        ctypes.byref(cfg), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
-        _ptr(k_out), _ptr(v_out), int(max_rows), _ptr(row_offsets), _ptr(flags),
-        _stream(stream)))
-
-
-def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k_cache, v_cache,
-              k_scale=None, v_scale=None, flags=None, stream=None):
-    """Write a step's new K/V rows into their pages, quantised to fp8 for an fp8 cache (see
-    pa_append_kv in pa.h): new row i of sequence b lands at position
-    context_lens[b] - q_lens[b] + i.  Per-token scales are written into k_scale / v_scale; a
-    page's one scale (SCALE_PER_BLOCK) is raised where a new row needs it, and the page's older
-    codes follow."""
-    _check("pa_append_kv", load().pa_append_kv(
-        ctypes.byref(cfg), _ptr(k_new), _ptr(v_new), _ptr(block_tables), _ptr(context_lens),
-        _ptr(q_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(flags),
-        _stream(stream)))
-
-
 _type_cache = None
 
 
@@ -256,6 +196,92 @@ def _columns(call: str, t) -> int:
 
 def _maybe(call: str, device: int, count: int, t, dtypes) -> Optional[int]:
     return None if t is None else _dense(call, device, count, t, dtypes)
+
+
+def _scale(call: str, device: int, cfg: PaConfig, t, f32) -> Optional[int]:
+    """Address of one of a cache's scale arrays, as large as cfg's scale mode has it (a mode that
+    the library refuses: whatever is given)."""
+    mode = cfg.kv_scale_mode
+    if mode == SCALE_NONE:
+        return None
+    if not 0 < mode <= SCALE_PER_BLOCK:
+        return _ptr(t)
+    heads = cfg.num_blocks * cfg.num_kv_heads
+    return _dense(call, device, (0, 1, heads * cfg.block_size, heads)[mode], t, f32)
+
+
+def plan(cfg: PaConfig, block_tables, context_lens, q_lens, ws, stream=None):
+    _check("pa_plan", load().pa_plan(ctypes.byref(cfg), _ptr(block_tables), _ptr(context_lens),
+                                     _ptr(q_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def decode(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+           q_lens, out, lse, ws, stream=None):
+    dev, _, _, f32, _ = _types()
+    name = "pa_decode"
+    _check(name, load().pa_decode(
+        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _scale(name, dev, cfg, k_scale, f32), _scale(name, dev, cfg, v_scale, f32),
+        _ptr(block_tables), _ptr(context_lens), _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def reduce(cfg: PaConfig, out, lse, ws, stream=None):
+    _check("pa_reduce", load().pa_reduce(ctypes.byref(cfg), _ptr(out), _ptr(lse), _ptr(ws),
+                                         _nbytes(ws), _stream(stream)))
+
+
+def read_flags(ws, stream=None) -> int:
+    """Synchronise and return the device flags of the last step run in ``ws``."""
+    f = ctypes.c_int32(0)
+    st = load().pa_read_flags(_ptr(ws), _nbytes(ws), ctypes.byref(f), _stream(stream))
+    if st not in (OK, ERR_DEVICE):
+        raise PaError("pa_read_flags", st)
+    return f.value
+
+
+def decode_step_static(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                       context_lens, q_lens, out, lse, stream=None):
+    """One decode step on the library's static device scratch, for callers that cannot
+    allocate device memory (no workspace argument; see pa_decode_step_static in pa.h)."""
+    dev, _, _, f32, _ = _types()
+    name = "pa_decode_step_static"
+    _check(name, load().pa_decode_step_static(
+        ctypes.byref(cfg), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _scale(name, dev, cfg, k_scale, f32), _scale(name, dev, cfg, v_scale, f32),
+        _ptr(block_tables), _ptr(context_lens), _ptr(q_lens), _ptr(out), _ptr(lse),
+        _stream(stream)))
+
+
+def gather_kv(cfg: PaConfig, k_cache, v_cache, block_tables, context_lens, k_out, v_out,
+              max_rows: int, row_offsets=None, flags=None, stream=None):
+    """Paged -> contiguous copy of the batch's K and V rows (see pa_gather_kv in pa.h):
+    sequence b lands at rows row_offsets[b] .. row_offsets[b + 1] - 1 of k_out and v_out."""
+    _check("pa_gather_kv", load().pa_gather_kv(
+        ctypes.byref(cfg), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+        _ptr(k_out), _ptr(v_out), int(max_rows), _ptr(row_offsets), _ptr(flags),
+        _stream(stream)))
+
+
+def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k_cache, v_cache,
+              k_scale=None, v_scale=None, flags=None, stream=None):
+    """Write a step's new K/V rows into their pages, quantised to fp8 for an fp8 cache (see
+    pa_append_kv in pa.h): new row i of sequence b lands at position
+    context_lens[b] - q_lens[b] + i.  Per-token scales are written into k_scale / v_scale; a
+    page's one scale (SCALE_PER_BLOCK) is raised where a new row needs it, and the page's older
+    codes follow."""
+    dev, i32, _, f32, kinds = _types()
+    name, B, row = "pa_append_kv", cfg.batch, cfg.num_kv_heads * cfg.head_dim
+    kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
+    cache = cfg.num_blocks * cfg.block_size * row
+    _check(name, load().pa_append_kv(
+        ctypes.byref(cfg), _dense(name, dev, B * cfg.max_q_len * row, k_new, kind),
+        _dense(name, dev, B * cfg.max_q_len * row, v_new, kind),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
+        _dense(name, dev, cache, k_cache, cache_kind), _dense(name, dev, cache, v_cache, cache_kind),
+        _scale(name, dev, cfg, k_scale, f32), _scale(name, dev, cfg, v_scale, f32),
+        _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
 def build_tables(cfg: PaConfig, context_lens, q_lens, held_blocks, block_tables, free_blocks,
@@ -329,19 +355,15 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
     """Attention of each row over its listed pages selected [B, Sq, Hkv, top_k], of which the
     first num_selected count (see pa_decode_selected in pa.h).  One launch, no workspace."""
     dev, i32, _, f32, kinds = _types()
-    name, B, Hkv, mode = "pa_decode_selected", cfg.batch, cfg.num_kv_heads, cfg.kv_scale_mode
+    name, B, Hkv = "pa_decode_selected", cfg.batch, cfg.num_kv_heads
     rows, top_k = B * cfg.max_q_len, _columns(name, selected)
     kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
-    heads = cfg.num_blocks * Hkv
-    cache = heads * cfg.block_size * cfg.head_dim
-    scales = (0, 1, heads * cfg.block_size, heads)[mode] if 0 <= mode <= 3 else 0
-    none = mode == SCALE_NONE
+    cache = cfg.num_blocks * cfg.block_size * Hkv * cfg.head_dim
     _check(name, load().pa_decode_selected(
         ctypes.byref(cfg), _dense(name, dev, rows * cfg.num_q_heads * cfg.head_dim, q, kind),
         _dense(name, dev, cache, k_cache, cache_kind),
         _dense(name, dev, cache, v_cache, cache_kind),
-        None if none else _dense(name, dev, scales, k_scale, f32),
-        None if none else _dense(name, dev, scales, v_scale, f32),
+        _scale(name, dev, cfg, k_scale, f32), _scale(name, dev, cfg, v_scale, f32),
         _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
         _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
         _dense(name, dev, rows * Hkv * top_k, selected, i32),

@@ -433,3 +433,59 @@ def test_per_page_scales_refused_on_the_host():
         assert call(fake, fake, mode) == pa.ERR_INVALID_ARG
     many = config(1 << 16, 1 << 20, 8, 2, 128, 16, 8, 32)
     assert app(fake, fake, many) == pa.ERR_UNSUPPORTED  # more page CTAs than a grid has
+
+
+@pytest.mark.parametrize("mode,count", [(pa.SCALE_PER_TENSOR, 1), (pa.SCALE_PER_TOKEN, 32 * 16 * 2), (pa.SCALE_PER_BLOCK, 32 * 2)])
+def test_binding_refuses_scales_that_do_not_fit(mode, count, monkeypatch):
+    """The append writes its scales and the decodes read them, as many as the mode has: an array of
+    another mode, type or layout, or elsewhere than the current GPU, does not reach the library
+    (a stand-in here, with host memory as its current device)."""
+    calls = []
+
+    class Library:
+        def pa_status_string(self, status):
+            return b"refused"
+
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+
+    monkeypatch.setattr(pa, "_lib", Library())
+    here = [-1]  # get_device() of a CPU tensor
+    i32, i64, f32 = (torch.int32,), (torch.int64,), (torch.float32,)
+    kinds = {pa.BF16: (torch.bfloat16,), pa.FP16: (torch.float16,), pa.FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
+    monkeypatch.setattr(pa, "_type_cache", (lambda: here[0], i32, i64, f32, kinds))
+    cfg = config(2, 1, 8, 2, 128, 16, 8, 32, num_ctas=4)
+    cfg.kv_scale_mode = mode
+    new, q = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16), torch.zeros(2, 1, 8, 128, dtype=torch.bfloat16)
+    cache, bt, lens = torch.zeros(32, 16, 2, 128, dtype=torch.uint8), torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    run = dict(
+        append=lambda ks, vs: pa.append_kv(cfg, new, new, bt, lens, lens, cache, cache, ks, vs, lens, stream=0),
+        decode=lambda ks, vs: pa.decode(cfg, q, cache, cache, ks, vs, bt, lens, lens, q, None, ws, stream=0),
+        static=lambda ks, vs: pa.decode_step_static(cfg, q, cache, cache, ks, vs, bt, lens, lens, q, None, stream=0))
+    good = torch.ones(count)
+    bad = [None, torch.ones(count - 1), good.half(), torch.ones(count, 2)[:, 0] if count > 1 else good.double(), good.int()]
+    for name, call in run.items():
+        for s in (good, torch.ones(count + 5), 1 << 20):
+            call(s, s)
+            assert len(calls) == 1 and (s if isinstance(s, int) else s.data_ptr()) in calls.pop()[1], name
+        for s in bad:
+            for pair in ((s, good), (good, s)):
+                with pytest.raises(pa.PaError) as e:
+                    call(*pair)
+                assert e.value.status == pa.ERR_INVALID_ARG and not calls, (name, s)
+        here[0] = 0  # the arrays lie elsewhere than the current device
+        with pytest.raises(pa.PaError):
+            call(good, good)
+        here[0] = -1
+    for k, x in ((1, new[:1]), (2, new.half()), (3, bt[:1]), (4, lens.long()), (5, lens[:1]), (6, cache[1:]), (7, cache.int()),
+                 (10, lens[:0])):
+        args = [cfg, new, new, bt, lens, lens, cache, cache, good, good, lens]
+        args[k] = x
+        with pytest.raises(pa.PaError) as e:
+            pa.append_kv(*args, stream=0)
+        assert e.value.status == pa.ERR_INVALID_ARG and not calls, k
+    cfg.kv_scale_mode = pa.SCALE_NONE  # whatever is given is not passed on
+    run["append"](None, None)
+    run["decode"](good, None)
+    assert [c[1][8:10] if c[0] == "pa_append_kv" else c[1][4:6] for c in calls] == [(None, None)] * 2
