@@ -245,6 +245,8 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
     // query fragments of this warp's rows (A operand, row-major 16 x 16 per k-step)
     uint32_t qa[WR][KSTEPS][4];
     int lim[WR][2];  // keys visible to rows quad and quad + 8 of each tile
+    constexpr bool QS = T::BLKS && QK == Q_BF16;  // query rows scaled into f16's range
+    float q_up[WR][2];                            // (their logits take this)
 #pragma unroll
     for (int w = 0; w < WR; ++w) {
 #pragma unroll
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
               const uint2 v = __ldg(reinterpret_cast<const uint2*>(qrow + (16 * kk + 4 * qi) * 2));
               lo = v.x;
               hi = v.y;
-              if constexpr (QK == Q_BF16) {
+              if constexpr (QK == Q_BF16 && !QS) {
                 const float2 a = bf16x2_to_f2(lo), c = bf16x2_to_f2(hi);
                 lo = pack2<true>(a.x, a.y);
                 hi = pack2<true>(c.x, c.y);
@@ -277,6 +279,26 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
           }
           qa[w][kk][h] = lo;      // a0a1 (h = 0) / a2a3 (h = 1)
           qa[w][kk][2 + h] = hi;  // a4a5 / a6a7
+        }
+        if constexpr (QS) {
+          // times the power of two that brings the row's largest element to [2^7, 2^8)
+          float big = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < KSTEPS; ++kk) {
+            const float2 a = bf16x2_to_f2(qa[w][kk][h]), c = bf16x2_to_f2(qa[w][kk][2 + h]);
+            big = fmaxf(big, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(c.x), fabsf(c.y))));
+          }
+          big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+          const float up = fmaxf(pow2_above(big), 0x1p-100f);  // (mul stays finite)
+          const float mul = pow2_inverse(up) * 256.f;
+          q_up[w][h] = up * (1.f / 256.f);
+#pragma unroll
+          for (int kk = 0; kk < KSTEPS; ++kk) {
+            const float2 a = bf16x2_to_f2(qa[w][kk][h]), c = bf16x2_to_f2(qa[w][kk][2 + h]);
+            qa[w][kk][h] = pack2<true>(a.x * mul, a.y * mul);
+            qa[w][kk][2 + h] = pack2<true>(c.x * mul, c.y * mul);
+          }
         }
       }
     }
@@ -398,7 +420,7 @@ __global__ void __launch_bounds__(MmaTraits<D, MP, KVK, SC>::NTHREADS, 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int tt = (j >> 1) * 8 + 2 * qi + (j & 1);  // token within the chunk
-              float x = sacc[w][j >> 1][2 * h + (j & 1)] * qk_chunk;
+              float x = sacc[w][j >> 1][2 * h + (j & 1)] * (QS ? qk_chunk * q_up[w][h] : qk_chunk);
               if constexpr (T::TOKS && !T::BLKS) x *= sks[c0 + tt];
               const bool vis = c0 + tt < n_in && tok0 + c0 + tt < lim[w][h];
               sv[h][j] = vis ? x : -INFINITY;

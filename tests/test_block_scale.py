@@ -275,11 +275,26 @@ def test_a_page_of_far_larger_scale_costs_the_others_nothing(sq, hq, hkv, d, bs,
         rng = np.random.default_rng(21)
         p = decode_problem(13, 2, sq, hq, hkv, d, bs, longest, dtype, 1)
         far_scales(rng, p, kind, ratio)
-        cfg = config(2, sq, hq, hkv, d, bs, p["maxb"], p["nblocks"], dtype, 1)
-        out, lse = run_decode(pa, p, cfg, cuda_device)
         ref, ref_lse, size = reference(p, 1, float(np.float32(d ** -0.5)))
         slack = 1.1e-4 + longest * 2.0 ** -22 if tensor_core else 2e-5
-        plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, 2.0 ** -11, slack)
+        for ctas in (0, 3):  # an item a step, and items of many steps
+            cfg = config(2, sq, hq, hkv, d, bs, p["maxb"], p["nblocks"], dtype, 1, num_ctas=ctas)
+            out, lse = run_decode(pa, p, cfg, cuda_device)
+            plain64.check_attention(out, lse, ref, ref_lse, size, p["q"].dtype, 2.0 ** -11, slack)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sq,hq,hkv,d", [(1, 4, 1, 128), (2, 4, 2, 64), (1, 8, 1, 256), (5, 4, 1, 256), (10, 4, 1, 256), (4, 16, 1, 128)])
+def test_queries_that_leave_f16(sq, hq, hkv, d, cuda_device, pa):
+    """Queries of 1e6 or 1e-6 with keys that make up for it: as exact as any other."""
+    for factor in (1e6, 1e-6):
+        p = decode_problem(19, 2, sq, hq, hkv, d, 16, 300, "bf16", 1)
+        p["q"] = (p["q"].float() * factor).bfloat16()
+        p["ks"] = p["ks"] / factor
+        cfg = config(2, sq, hq, hkv, d, 16, p["maxb"], p["nblocks"], causal=1)
+        out, lse = run_decode(pa, p, cfg, cuda_device)
+        ref, ref_lse, size = reference(p, 1, float(np.float32(d ** -0.5)))
+        plain64.check_attention(out, lse, ref, ref_lse, size, torch.bfloat16, 2.0 ** -11, 1.1e-4 if sq * hq // hkv > 32 else 2e-5)
 
 
 @pytest.mark.gpu
