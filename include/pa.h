@@ -163,7 +163,7 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * The tables and lengths must be the ones given to pa_plan, with the same contents.  A CTA
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
  * fp8 cache) and of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
- * query rows per kv head at head dim 128, up to 16 at 256) derives its first work item from the
+ * query rows per kv head) derives its first work item from the
  * lengths (the planner's rules) and starts on it while the planner may still be running; it
  * waits for the planner before the rest of its list and before writing anything, and raises
  * PA_FLAG_STALE_PLAN if the planner's first item differs.  The other decode kernels wait for the

@@ -700,12 +700,12 @@ cudaError_t launch_mma_instance(const KernelParams& prm, const CUtensorMap& kmap
   X(MP_, KV_FP8, Q_BF16, SC_TOKEN)  \
   X(MP_, KV_FP8, Q_FP16, SC_NONE)   \
   X(MP_, KV_FP8, Q_FP16, SC_TOKEN)
-// one scale for each page: what the streaming kernel leaves (head dim 256, 17 rows and more)
+// one scale for each page: what the streaming kernel leaves (head dim 256, 33 rows and more)
 #define PA_MMA_PAGES(X, MP_)       \
   X(MP_, KV_FP8, Q_BF16, SC_BLOCK) \
   X(MP_, KV_FP8, Q_FP16, SC_BLOCK)
 #define PA_MMA_ALL(X) \
-  PA_MMA_ROWS(X, 16) PA_MMA_ROWS(X, 32) PA_MMA_ROWS(X, 64) PA_MMA_PAGES(X, 32) PA_MMA_PAGES(X, 64)
+  PA_MMA_ROWS(X, 16) PA_MMA_ROWS(X, 32) PA_MMA_ROWS(X, 64) PA_MMA_PAGES(X, 64)
 
 // A cache row must hold whole 128-byte slabs (a 64-dim fp8 cache stays on CUDA cores).
 constexpr bool mma_fits(int D, int kvk, int scales) {

@@ -99,16 +99,19 @@ inline int decode_merge_limit(int split_merge, int path) {
 // The streaming kernel (an fp8 cache with one scale for each page and kv head): query rows of a
 // tile, the tokens that its warps take in a round, the cost of an item in such rounds (64 long
 // sequences and 32 of four new tokens: 3 rounds 44.9 and 39.3 us a step, 5 rounds 43.5 and 38.1, 7
-// rounds 42.8 and 38.9, 9 rounds 43.3 and 40.9), and the most rows per kv head it takes.  At head
-// dim 128 two tiles beat one of the mma.sync kernel (24 rows, batched GQA: 62 against 107 us; 32
-// rows, long pages: 65 against 100 us); at 256, where the tiles leave room for one CTA an SM, they
-// do not (32 rows: 95 against 81 us; one tile of 16: 73 against 86 us).  64-dim rows: always (4
-// rows: 50 against 93 us on CUDA cores).
+// rounds 42.8 and 38.9, 9 rounds 43.3 and 40.9), and the most rows per kv head it takes.  Two tiles
+// beat one of the mma.sync kernel.  Us a step on 64 sequences with one kv head in pages of 1,024
+// (8,192 to 16,384 tokens at head dim 128, 4,096 to 8,192 at 256), and on 32 with 8 kv heads in
+// pages of 16 (512 to 4,096, 256 to 2,048), streaming against mma.sync: head dim 128, 16 rows 44.6
+// against 54.0 and 38.7 against 56.7, 32 rows 65.3 against 98.4 and 60.1 against 103.9; 256, 16 rows
+// 53.8 against 68.5 and 49.3 against 67.9, 32 rows 86.3 against 92.2 and 80.6 against 93.5; four
+// tiles do not (64 rows at 256: 156.8 against 147.3, 145.5 against 146.2).  No other kernel takes
+// rows of 64 bytes with page scales.
 constexpr int kStreamRows = 16;
 constexpr int stream_round_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
 constexpr int kStreamItemCostRounds = 5;
 constexpr int stream_max_rows(int head_dim) {
-  return head_dim == 64 ? 0x7fffffff : head_dim == 128 ? 32 : 16;
+  return head_dim == 64 ? 0x7fffffff : 32;
 }
 
 // Query rows per kv head above which a 128-dim head runs on the tcgen05 kernel.
