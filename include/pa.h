@@ -173,7 +173,21 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * start (a pa_plan call does so after its own wait on the launch before it): a kernel between
  * pa_plan and pa_decode that writes any of them must not let its dependents start early.
  * A decode that completed leaves the merge counters as pa_plan set them, so pa_decode may
- * run again on the same plan. */
+ * run again on the same plan.
+ *
+ * Rounding.  Logits, the softmax's maxima and sums, and the outputs' accumulators are fp32.  A
+ * weight is rounded once, to the type of the second product's operands: bf16 for a bf16 cache,
+ * f16 for fp16 and fp8 caches (whose codes are exact there; 64-dim fp8 caches without page scales
+ * run in fp32).  With PA_SCALE_PER_TOKEN it is rounded with its token's V scale in it as that is,
+ * so V scales below 2^-14 cost it bits.  With PA_SCALE_PER_BLOCK it keeps its bits whatever the
+ * scales are, unless pages that one row reads differ in theirs by more than 2^60 (2^30 with 33
+ * query rows and more per kv head at head dim 128).  For an fp8 cache a bf16 query is scaled by a
+ * power of two and held in f16, or, with 33 rows and more per kv head at head dim 128, any query
+ * in two or three E4M3 terms: elements below about a thousandth of the row's largest lose bits.
+ *
+ * Keys that a row does not see may hold anything; the values (V) of a key that some of a
+ * sequence's rows see and others do not have to be finite, as a weight of zero meets them in the
+ * same product. */
 PA_API pa_status pa_decode(const pa_config *cfg, const void *q, const void *k_cache, const void *v_cache,
                     const float *k_scale, const float *v_scale, const int32_t *block_tables,
                     const int32_t *context_lens, const int32_t *q_lens, void *out, float *lse,
@@ -276,8 +290,10 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *                          new rows gets scale w (1 for w = 0); any other page keeps its scale
  *                          unless w is larger.  Then the page's scale becomes w and the codes c
  *                          of its older tokens become E4M3(c * old scale / w), the product and
- *                          the quotient each rounded to fp32.  The older scale has to be one
- *                          that an earlier append wrote (positive and finite).  No two
+ *                          the quotient each rounded to fp32.  A scale never falls while its
+ *                          page is in use, so a page that begins with zeros holds what follows
+ *                          no finer than E4M3 at scale 1 does (2^-9).  The older scale has to be
+ *                          one that an earlier append wrote (positive and finite).  No two
  *                          sequences may append to one page in one call.
  *   Quotients are IEEE fp32 divisions.  A NaN element gives a NaN code (0x7f or 0xff).
  * Reads cfg's batch, max_q_len, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
@@ -287,7 +303,8 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *                  aligned; rows i >= q_lens[b] are ignored
  *   block_tables, context_lens, q_lens   device int32, as for pa_plan
  *   k_cache, v_cache   device, [num_blocks, block_size, num_kv_heads, head_dim] in kv_dtype,
- *                  16-byte aligned; only the new rows' slots are written
+ *                  16-byte aligned; the new rows' slots are written, and with
+ *                  PA_SCALE_PER_BLOCK also the older slots of a page whose scale grows
  *   k_scale, v_scale   device fp32 (see the scale modes)
  *   flags          NULL, or a device int32 the call ORs PA_FLAG_* bits into:
  *                  PA_FLAG_BAD_LENGTHS for a sequence whose lengths break the rules of
@@ -366,9 +383,14 @@ PA_API pa_status pa_update_bounds(const pa_config *cfg, const void *k_new,
  * With L the keys that row i sees (as for the decode), page p < ceil(L / block_size) of row i
  * and kv head g scores
  *     max over the group's heads h of  sm_scale * sum_d (max(q_d, 0) hi_d + min(q_d, 0) lo_d)
- * with lo and hi the page's bounds: for sm_scale >= 0 no key of the page has a larger logit.
- * Other pages, and the rows i >= q_lens[b], score -inf.  Products and sums are in fp32; bounds
- * or queries that are not finite give scores that are not (NaN included).
+ * with lo and hi the page's bounds.  For sm_scale >= 0 no key that went into the bounds has a
+ * larger logit, but for rounding: the products are exact and their sums fp32, off by less than
+ * (2 D + 1) 2^-23 of the sum of their magnitudes.  An fp8 cache does not hold those keys but their
+ * codes, each value off by up to 2^-4 of itself (or half a step of E4M3's subnormals, 2^-10 of
+ * the scale), and by as much again each time that its page's scale grows: such a key may score
+ * above its page by what that comes to.
+ * Other pages, and the rows i >= q_lens[b], score -inf.  Bounds or queries that are not finite
+ * give scores that are not (NaN included).
  *   q        [B, Sq, Hq, D] q_dtype, 16-byte aligned
  *   k_bounds [num_blocks, num_kv_heads, 2, head_dim] q_dtype, 16-byte aligned
  *   scores   fp32 [B, Sq, Hkv, max_blocks_per_seq], written whole
@@ -413,7 +435,9 @@ PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
  *                 page outside the sequence's is skipped), PA_FLAG_BAD_BLOCK_ID (a listed page
  *                 whose block lies outside [0, num_blocks) is skipped)
  * One launch, no workspace; the split of a row's pages depends on the sizes alone, so equal
- * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used.
+ * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used.  Rounding is
+ * that of pa_decode, with PA_SCALE_PER_TOKEN as stated there for PA_SCALE_PER_BLOCK, and a query in
+ * f16 for an fp8 cache.  Keys and values that a row does not see may hold anything.
  * PA_ERR_UNSUPPORTED for what the decode does not take, and for lists of 2^31 tokens or more
  * (top_k * block_size). */
 PA_API pa_status pa_decode_selected(const pa_config *cfg, const void *q, const void *k_cache,

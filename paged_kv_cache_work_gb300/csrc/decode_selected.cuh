@@ -7,10 +7,10 @@
 // time (a lane each: list entry, then block table) and streams them (page_stream.cuh).  At the end
 // the warps' states are merged through shared memory, and the CTAs' through distributed shared
 // memory, both in a fixed order.
-//   Measured: 32 sequences with 8 kv heads of 128 and 64 pages of 16 tokens each (16-bit, 134 MB) 24.4
-// us, 81 % of the copy rate, bound by the data of one wave of CTAs with its start and merge; 4 sequences
-// with one kv head and 32 pages of 64 (fp8, 2 MB) 7.4 us, a chain of list, block table, scales,
-// first copies, two merges.
+//   Measured: 32 sequences with 8 kv heads of 128 and 64 pages of 16 tokens each (16-bit, 135 MB) 24.5
+// us, 81 % of the copy rate, bound by the data of one wave of CTAs with its start and merge (256 units
+// on 304 places: 104 SMs hold two of them, 48 one); 4 sequences with one kv head and 32 pages of 64
+// (fp8, 2 MB) 7.6 us, a chain of list, block table, scales, first copies, two merges.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -12,11 +12,11 @@
 // and products start while the planner may still be running; nothing is written (flags included)
 // and no other item is read before the planner has finished.
 //   Measured, plan, decode and reduce: 64 sequences of 8,192 to 16,384 tokens (16 heads on one kv head
-// of 128, 202 MB) 43.1 us, 32 of 512 to 4,096 with four new tokens each (32 heads on 8, 153 MB) 36.9
-// us.  Pages stream at 6.2 TB/s once under way, bound by what two warps a scheduler issue (0.35 of a
+// of 128, 202 MB) 43.9 us, 32 of 512 to 4,096 with four new tokens each (32 heads on 8, 153 MB) 38.2
+// us (43.9 and 41.8 when a tenth of the pages have a scale 1,000 times the others').  Pages stream at 6.2 TB/s once under way, bound by what two warps a scheduler issue (0.35 of a
 // slot a cycle); about 10 us are the planner, the first copies, the last items' merge and the
-// reducer.  The mma.sync kernel, whose CTAs pass tiles through one ring with barriers, took 54.4 and
-// 58.3 us.
+// reducer.  The mma.sync kernel, whose CTAs pass tiles through one ring with barriers, takes 54.1 and
+// 56.7 us.
 #pragma once
 
 #include "page_stream.cuh"

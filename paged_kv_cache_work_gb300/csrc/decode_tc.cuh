@@ -328,7 +328,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
 // f16's 65504) and at least 2^-15 (the least code, 2^-9, is then f16's least subnormal, so every
 // code stays exact), and the weights the rest, v 2^(14 - top - shift), which is in [2^6, 2^7) while
 // shift has room.  A weight then has its 11 bits from 2^-20 of the row's largest on for a scale of
-// 2^-22 of the item's largest, from 2^-12 on for one of 2^-30.
+// 2^-22 of the item's largest, from 2^-12 on for one of 2^-30.  (64 sequences of 8,192 to 16,384
+// tokens on one kv head, a step: 64 rows 102.8 us, 128 rows 114.2; split, as a tenth of the pages have a
+// scale 1,000 times the others', 120 and 157.)
 struct VScales {
   int top;
   bool wide;

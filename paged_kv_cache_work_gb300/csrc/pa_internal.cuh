@@ -98,8 +98,8 @@ inline int decode_merge_limit(int split_merge, int path) {
 
 // The streaming kernel (an fp8 cache with one scale for each page and kv head): query rows of a
 // tile, the tokens that its warps take in a round, the cost of an item in such rounds (64 long
-// sequences and 32 of four new tokens: 3 rounds 44.9 and 39.3 us a step, 5 rounds 43.5 and 38.1, 7
-// rounds 42.8 and 38.9, 9 rounds 43.3 and 40.9), and the most rows per kv head it takes.  Two tiles
+// sequences and 32 of four new tokens: 3 rounds 45.7 and 39.4 us a step, 5 rounds 43.7 and 37.8, 7
+// rounds 43.1 and 39.2, 9 rounds 43.6 and 41.1), and the most rows per kv head it takes.  Two tiles
 // beat one of the mma.sync kernel.  Us a step on 64 sequences with one kv head in pages of 1,024
 // (8,192 to 16,384 tokens at head dim 128, 4,096 to 8,192 at 256), and on 32 with 8 kv heads in
 // pages of 16 (512 to 4,096, 256 to 2,048), streaming against mma.sync: head dim 128, 16 rows 44.6
