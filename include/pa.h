@@ -163,11 +163,10 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * The tables and lengths must be the ones given to pa_plan, with the same contents.  A CTA
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
  * fp8 cache) and of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
- * query rows per kv head) derives its first work item from the
- * lengths (the planner's rules) and starts on it while the planner may still be running; it
- * waits for the planner before the rest of its list and before writing anything, and raises
- * PA_FLAG_STALE_PLAN if the planner's first item differs.  The other decode kernels wait for the
- * planner first.
+ * query rows per kv head) derives its first work item from the lengths (the planner's rules) and
+ * starts on it while the planner may still be running; it waits for the planner before the rest of
+ * its list and before writing anything, and raises PA_FLAG_STALE_PLAN if the planner's first item
+ * differs.  The other decode kernels wait for the planner first.
  * The kernels launch with programmatic dependent launch, so pa_decode reads q, the caches,
  * the scales, the tables and the lengths once the launch before it in the stream has let its dependents
  * start (a pa_plan call does so after its own wait on the launch before it): a kernel between
@@ -177,13 +176,15 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  *
  * Rounding.  Logits, the softmax's maxima and sums, and the outputs' accumulators are fp32.  A
  * weight is rounded once, to the type of the second product's operands: bf16 for a bf16 cache,
- * f16 for fp16 and fp8 caches (whose codes are exact there; 64-dim fp8 caches without page scales
- * run in fp32).  With PA_SCALE_PER_TOKEN it is rounded with its token's V scale in it as that is,
- * so V scales below 2^-14 cost it bits.  With PA_SCALE_PER_BLOCK it keeps its bits whatever the
- * scales are, unless pages that one row reads differ in theirs by more than 2^60 (2^30 with 33
- * query rows and more per kv head at head dim 128).  For an fp8 cache a bf16 query is scaled by a
- * power of two and held in f16, or, with 33 rows and more per kv head at head dim 128, any query
- * in two or three E4M3 terms: elements below about a thousandth of the row's largest lose bits.
+ * f16 for fp16 and fp8 caches (whose codes are exact there).  With PA_SCALE_PER_TOKEN it is rounded
+ * with its token's V scale in it as that is, so V scales below 2^-14 cost it bits.  With
+ * PA_SCALE_PER_BLOCK it keeps its bits whatever the scales are, unless pages that one row reads
+ * differ in theirs by more than 2^60 (2^30 with 33 query rows and more per kv head at head dim
+ * 128).  For an fp8 cache a bf16 query goes into f16: with PA_SCALE_PER_BLOCK times a power of two
+ * that makes it fit, else as it is (past 65504 it becomes infinite); with 33 rows and more per kv
+ * head at head dim 128 any query goes into two or three E4M3 terms, scaled to fit, where elements
+ * below about a thousandth of the row's largest lose bits.  64-dim fp8 caches without page scales
+ * run in fp32 throughout.
  *
  * Keys that a row does not see may hold anything; the values (V) of a key that some of a
  * sequence's rows see and others do not have to be finite, as a weight of zero meets them in the
@@ -435,9 +436,9 @@ PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
  *                 page outside the sequence's is skipped), PA_FLAG_BAD_BLOCK_ID (a listed page
  *                 whose block lies outside [0, num_blocks) is skipped)
  * One launch, no workspace; the split of a row's pages depends on the sizes alone, so equal
- * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used.  Rounding is
- * that of pa_decode, with PA_SCALE_PER_TOKEN as stated there for PA_SCALE_PER_BLOCK, and a query in
- * f16 for an fp8 cache.  Keys and values that a row does not see may hold anything.
+ * inputs give equal bits.  num_ctas, grid_mult and split_merge of cfg are not used.  Weights and
+ * queries are rounded as pa_decode does with PA_SCALE_PER_BLOCK and up to 32 rows per kv head,
+ * whatever the scale mode.  Keys and values that a row does not see may hold anything.
  * PA_ERR_UNSUPPORTED for what the decode does not take, and for lists of 2^31 tokens or more
  * (top_k * block_size). */
 PA_API pa_status pa_decode_selected(const pa_config *cfg, const void *q, const void *k_cache,

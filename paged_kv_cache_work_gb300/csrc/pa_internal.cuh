@@ -105,8 +105,8 @@ inline int decode_merge_limit(int split_merge, int path) {
 // pages of 16 (512 to 4,096, 256 to 2,048), streaming against mma.sync: head dim 128, 16 rows 44.6
 // against 54.0 and 38.7 against 56.7, 32 rows 65.3 against 98.4 and 60.1 against 103.9; 256, 16 rows
 // 53.8 against 68.5 and 49.3 against 67.9, 32 rows 86.3 against 92.2 and 80.6 against 93.5; four
-// tiles do not (64 rows at 256: 156.8 against 147.3, 145.5 against 146.2).  No other kernel takes
-// rows of 64 bytes with page scales.
+// tiles do not always (64 rows at 256: 156.8 against 147.3, 145.5 against 146.2).  No other kernel
+// takes rows of 64 bytes with page scales.
 constexpr int kStreamRows = 16;
 constexpr int stream_round_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
 constexpr int kStreamItemCostRounds = 5;
