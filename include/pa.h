@@ -81,14 +81,25 @@ typedef enum {
   PA_ERR_DEVICE = 5       /* pa_read_flags: the device recorded an input problem */
 } pa_status;
 
-typedef enum { PA_BF16 = 0, PA_FP16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+/* PA_INT4 is a cache's type only: see "4-bit caches" below. */
+typedef enum { PA_BF16 = 0, PA_FP16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
 typedef enum {
   PA_SCALE_NONE = 0,       /* 16-bit cache, or fp8 codes used as they are */
   PA_SCALE_PER_TENSOR = 1, /* k_scale, v_scale: one fp32 each */
   PA_SCALE_PER_TOKEN = 2,  /* k_scale, v_scale: fp32 [num_blocks, block_size, num_kv_heads] */
-  PA_SCALE_PER_BLOCK = 3   /* k_scale, v_scale: fp32 [num_blocks, num_kv_heads] */
+  PA_SCALE_PER_BLOCK = 3,  /* k_scale, v_scale: fp32 [num_blocks, num_kv_heads] */
+  PA_SCALE_AFFINE = 4      /* PA_INT4 caches, and only they: k_scale, v_scale hold pairs (step, low)
+                              of q_dtype, [num_blocks, num_kv_heads, block_size, 2] */
 } pa_scale_mode;
+
+/* 4-bit caches (kv_dtype PA_INT4 with PA_SCALE_AFFINE).  k_cache and v_cache are bytes
+ * [num_blocks, block_size, num_kv_heads, head_dim / 2]: channel 2 j of a row (one token and kv
+ * head) in the low half of byte j, channel 2 j + 1 in the high half, each a code c in 0 .. 15.
+ * A row's pair (step, low) stands in the scale array of its cache, and its values are
+ *     low + step * c.
+ * A page's pairs of one kv head lie together, as its rows of one kv head are read together.
+ * (The pages cited above have no counterpart of this cache.) */
 
 /* Where the log-sum-exp merge of split units runs.  A unit cut into ns pieces can be merged
  * by the last CTA to finish one of its pieces, inside pa_decode (an atomic arrival counter
@@ -114,7 +125,8 @@ enum {
   PA_FLAG_BAD_SELECTION = 16, /* pa_decode_selected: a page count outside [0, top_k] or a listed
                                 page outside the sequence */
   PA_FLAG_NO_FREE_BLOCKS = 32, /* pa_build_tables: fewer free pages than the lengths need */
-  PA_FLAG_BAD_FREE_LIST = 64 /* pa_build_tables: a held or free page count that cannot be */
+  PA_FLAG_BAD_FREE_LIST = 64, /* pa_build_tables: a held or free page count that cannot be */
+  PA_FLAG_BAD_POSITION = 128 /* pa_append_rotated: a position outside [0, table_rows) */
 };
 
 typedef struct {
@@ -127,8 +139,9 @@ typedef struct {
   int32_t max_blocks_per_seq; /* columns of block_tables */
   int32_t num_blocks;         /* physical pages in the pool */
   int32_t q_dtype;            /* pa_dtype of q and out: PA_BF16 or PA_FP16 */
-  int32_t kv_dtype;           /* pa_dtype of the cache: q_dtype or PA_FP8_E4M3 */
-  int32_t kv_scale_mode;      /* pa_scale_mode; PA_SCALE_NONE unless kv_dtype is fp8 */
+  int32_t kv_dtype;           /* pa_dtype of the cache: q_dtype, PA_FP8_E4M3 or PA_INT4 */
+  int32_t kv_scale_mode;      /* pa_scale_mode; PA_SCALE_NONE for a 16-bit cache, PA_SCALE_AFFINE
+                                 for PA_INT4 */
   int32_t causal;             /* 1: new token i sees keys up to its own position */
   float sm_scale;             /* logit scale, usually 1/sqrt(D) */
   int32_t num_ctas;           /* persistent grid size; 0: (SMs of the current device x grid_mult)
@@ -184,13 +197,16 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * that makes it fit, else as it is (past 65504 it becomes infinite); with 33 rows and more per kv
  * head at head dim 128 any query goes into two or three E4M3 terms, scaled to fit, where elements
  * below about a thousandth of the row's largest lose bits.  64-dim fp8 caches without page scales
- * run in fp32 throughout.
+ * run in fp32 throughout.  For a 4-bit cache the codes enter both products as the integers c - 8,
+ * the query in f16 times a power of two that makes it fit, a weight times its row's V step in f16
+ * (11 bits kept as with PA_SCALE_PER_BLOCK), and what low + 8 step adds to logits and outputs is
+ * fp32.
  *
  * Keys that a row does not see may hold anything; the values (V) of a key that some of a
  * sequence's rows see and others do not have to be finite, as a weight of zero meets them in the
  * same product. */
 PA_API pa_status pa_decode(const pa_config *cfg, const void *q, const void *k_cache, const void *v_cache,
-                    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                    const void *k_scale, const void *v_scale, const int32_t *block_tables,
                     const int32_t *context_lens, const int32_t *q_lens, void *out, float *lse,
                     void *ws, size_t ws_bytes, pa_stream stream);
 
@@ -232,8 +248,8 @@ PA_API pa_status pa_read_flags(const void *ws, size_t ws_bytes, int32_t *flags, 
  * available for this scratch (its address is private); device-side input problems leave
  * out unspecified. */
 PA_API pa_status pa_decode_step_static(const pa_config *cfg, const void *q, const void *k_cache,
-                                       const void *v_cache, const float *k_scale,
-                                       const float *v_scale, const int32_t *block_tables,
+                                       const void *v_cache, const void *k_scale,
+                                       const void *v_scale, const int32_t *block_tables,
                                        const int32_t *context_lens, const int32_t *q_lens,
                                        void *out, float *lse, pa_stream stream);
 
@@ -245,7 +261,8 @@ PA_API pa_status pa_decode_step_static(const pa_config *cfg, const void *q, cons
  * row_off[b] .. row_off[b] + context_lens[b] - 1 of k_out and of v_out, where
  * row_off[b] = context_lens[0] + ... + context_lens[b - 1]; a row is one token's
  * [num_kv_heads, head_dim] values exactly as the cache stores them (bf16, fp16 or E4M3
- * codes; the scales of tokens or pages are not copied).  Reads cfg's batch, num_kv_heads, head_dim,
+ * codes; the scales of tokens or pages are not copied; pa_dequant_kv reads codes back as values,
+ * those of 4-bit caches among them, which this call does not take).  Reads cfg's batch, num_kv_heads, head_dim,
  * block_size, max_blocks_per_seq, num_blocks and kv_dtype; the other fields are ignored.
  *
  *   k_cache, v_cache  device, [num_blocks, block_size, num_kv_heads, head_dim], 16-byte aligned
@@ -297,6 +314,15 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *                          one that an earlier append wrote (positive and finite).  No two
  *                          sequences may append to one page in one call.
  *   Quotients are IEEE fp32 divisions.  A NaN element gives a NaN code (0x7f or 0xff).
+ *   4-bit cache (PA_INT4): each row x gets, and its pair in k_scale / v_scale becomes,
+ *     low  = the largest number of q_dtype that is <= min(x),
+ *     step = the least number of q_dtype that is >= (max(x) - low) / 15 (fp32 difference and
+ *            quotient, each rounded to nearest),
+ *     c    = (x - low) / step (fp32 difference and IEEE quotient) rounded to the nearest integer,
+ *            ties to even; 0 when step is 0.
+ *   So low is the least element itself and a value is read back within step / 2, which is a
+ *   thirtieth of the row's range (and half a step of q_dtype in that).  A row that holds a NaN or
+ *   an infinity, or whose range passes fp32, gets step NaN and codes 0: all of it reads back NaN.
  * Reads cfg's batch, max_q_len, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
  * num_blocks, q_dtype, kv_dtype and kv_scale_mode.
  *
@@ -306,7 +332,7 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *   k_cache, v_cache   device, [num_blocks, block_size, num_kv_heads, head_dim] in kv_dtype,
  *                  16-byte aligned; the new rows' slots are written, and with
  *                  PA_SCALE_PER_BLOCK also the older slots of a page whose scale grows
- *   k_scale, v_scale   device fp32 (see the scale modes)
+ *   k_scale, v_scale   device fp32 (see the scale modes), or pairs of q_dtype for a 4-bit cache
  *   flags          NULL, or a device int32 the call ORs PA_FLAG_* bits into:
  *                  PA_FLAG_BAD_LENGTHS for a sequence whose lengths break the rules of
  *                  pa_plan (none of its rows is written), PA_FLAG_BAD_BLOCK_ID for a new row
@@ -318,7 +344,75 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
 PA_API pa_status pa_append_kv(const pa_config *cfg, const void *k_new, const void *v_new,
                               const int32_t *block_tables, const int32_t *context_lens,
                               const int32_t *q_lens, void *k_cache, void *v_cache,
-                              float *k_scale, float *v_scale, int32_t *flags, pa_stream stream);
+                              void *k_scale, void *v_scale, int32_t *flags, pa_stream stream);
+
+/* How pa_append_rotated makes a projection's rows ready for attention. */
+typedef struct {
+  const void *q_weight;     /* q_dtype [head_dim], or NULL: queries are not normalised */
+  const void *k_weight;     /* the same for keys */
+  float eps;                /* added to the mean square; finite and >= 0 */
+  int32_t rotary_dim;       /* channels that rotate, the first ones of a head: a multiple of 16, at
+                               most head_dim; 0: none (cos_sin and positions are not read) */
+  int32_t interleaved;      /* pair p is channels 2 p, 2 p + 1 (1) or p, p + rotary_dim / 2 (0) */
+  const float *cos_sin;     /* fp32 [table_rows, rotary_dim], 16-byte aligned: the cosines of a
+                               position's rotary_dim / 2 angles, then their sines */
+  int32_t table_rows;
+  const int32_t *positions; /* int32 [num_axes, batch, max_q_len], or NULL: every axis is at the
+                               row's cache position */
+  int32_t num_axes;         /* 1 to 3 */
+  int32_t axis_pairs[3];    /* the first axis_pairs[0] pairs take their angle from the first axis's
+                               position, the next axis_pairs[1] from the second's, ...; they add up
+                               to rotary_dim / 2 */
+  int64_t q_stride, k_stride, v_stride; /* elements from one token's rows of q, k_new and v_new to
+                               the next token's, multiples of 8; 0: the rows lie dense */
+} pa_rotary;
+
+/* Normalise and rotate a step's queries and keys and write its K/V rows into their pages, in one
+ * pass.  (The pages cited above have no counterpart.)
+ *
+ * For each new row i < q_lens[b] of each q and k head x (fp32 throughout, one rounding at the end):
+ *     y_c = x_c / sqrt(mean(x^2) + eps) * weight_c          (with a weight; else y = x)
+ *     (z_a, z_b) = (y_a cos - y_b sin, y_b cos + y_a sin)   for each pair (a, b), with the angle of
+ *                                                           its axis's position
+ * z of a query goes to q_out, z of a key to k_out (both rounded to q_dtype) and, quantised from fp32
+ * as pa_append_kv quantises, into its page; values go into their pages as they are.  Keys, values,
+ * scales, tables and lengths are those of pa_append_kv, for every cache but one with
+ * PA_SCALE_PER_BLOCK (PA_ERR_UNSUPPORTED: a page's scale needs all its new rows; take k_out and give
+ * it to pa_append_kv).
+ *
+ *   q [batch, max_q_len, num_q_heads, head_dim], k_new, v_new [batch, max_q_len, num_kv_heads,
+ *                  head_dim] in q_dtype, 16-byte aligned; tokens may lie apart (the strides: slices
+ *                  of one projection's output)
+ *   q_out          dense, as q; may be q itself if that is dense.  Rows i >= q_lens[b] are left as
+ *                  they were
+ *   k_out          NULL, or dense, as k_new: the rotated keys (what pa_update_bounds wants); may be
+ *                  k_new itself if that is dense
+ *   k_cache, v_cache   both, or both NULL with k_out given: nothing goes into pages (v_new, scales
+ *                  and block_tables are not read then and may be NULL)
+ *   flags          NULL, or a device int32: PA_FLAG_BAD_LENGTHS (nothing of that sequence is
+ *                  written), PA_FLAG_BAD_POSITION (nothing of that token is written),
+ *                  PA_FLAG_BAD_BLOCK_ID (that token's K and V do not go into a page)
+ * Reads cfg's batch, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+ * max_blocks_per_seq, num_blocks, q_dtype, kv_dtype and kv_scale_mode.  Stream-ordered, allocates
+ * nothing, never synchronises. */
+PA_API pa_status pa_append_rotated(const pa_config *cfg, const pa_rotary *rotary, const void *q,
+                                   const void *k_new, const void *v_new,
+                                   const int32_t *block_tables, const int32_t *context_lens,
+                                   const int32_t *q_lens, void *q_out, void *k_out, void *k_cache,
+                                   void *v_cache, void *k_scale, void *v_scale, int32_t *flags,
+                                   pa_stream stream);
+
+/* Read a quantised cache back: the rows that pa_gather_kv copies, as values of q_dtype.
+ *
+ * Row row_off[b] + t of k_out (and v_out) holds the values of sequence b's token t: the code times
+ * its scale (fp8), or low + step * code (4-bit), in fp32 and rounded to q_dtype once.  Arguments,
+ * checks and flags are those of pa_gather_kv, with k_scale and v_scale as for pa_decode and q_dtype
+ * the type of k_out and v_out.  PA_ERR_UNSUPPORTED for a 16-bit cache (pa_gather_kv copies it). */
+PA_API pa_status pa_dequant_kv(const pa_config *cfg, const void *k_cache, const void *v_cache,
+                               const void *k_scale, const void *v_scale,
+                               const int32_t *block_tables, const int32_t *context_lens,
+                               void *k_out, void *v_out, int64_t max_rows, int32_t *row_offsets,
+                               int32_t *flags, pa_stream stream);
 
 /* Grow and shrink block tables from the requests' lengths, on the GPU.  (The pages cited above
  * have no counterpart.)
@@ -427,7 +521,8 @@ PA_API pa_status pa_select_blocks(const pa_config *cfg, const float *scores,
  * selected[b][i][g][0 .. num_selected[b][i][g]) that lie below L (the keys the row sees, as for
  * the decode): out and lse as for pa_decode with the softmax over those keys alone; a row with
  * none gets out = 0, lse = -inf.  The list may be in any order; a page listed twice counts
- * twice.  Any cache, scale mode and head grouping that pa_decode takes.
+ * twice.  Any cache, scale mode and head grouping that pa_decode takes but a 4-bit cache
+ * (PA_ERR_UNSUPPORTED).
  *   selected      int32 [B, Sq, Hkv, top_k] logical pages (columns of block_tables)
  *   num_selected  int32 [B, Sq, Hkv]
  *   lse           [B, Sq, Hq] fp32 or NULL

@@ -17,12 +17,12 @@ from typing import Optional
 __all__ = ["PaConfig", "PaError", "load", "workspace_size", "plan", "decode", "reduce",
            "decode_step_static", "STATIC_SCRATCH_BYTES", "append_kv", "gather_kv",
            "build_tables", "update_bounds", "score_blocks", "select_blocks",
-           "decode_selected",
+           "decode_selected", "append_rotated", "dequant_kv", "PaRotary",
            "read_flags", "status_string", "config_for", "paged_attention", "LIB_PATH",
-           "BF16", "FP16", "FP8_E4M3", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
-           "SCALE_PER_BLOCK",
+           "BF16", "FP16", "FP8_E4M3", "INT4", "SCALE_NONE", "SCALE_PER_TENSOR", "SCALE_PER_TOKEN",
+           "SCALE_PER_BLOCK", "SCALE_AFFINE",
            "FLAG_BAD_LENGTHS", "FLAG_BAD_BLOCK_ID", "FLAG_WAIT_TIMEOUT", "FLAG_STALE_PLAN",
-           "FLAG_BAD_SELECTION", "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST",
+           "FLAG_BAD_SELECTION", "FLAG_NO_FREE_BLOCKS", "FLAG_BAD_FREE_LIST", "FLAG_BAD_POSITION",
            "EXPORTED_SYMBOLS",
            "MERGE_AUTO", "MERGE_IN_DECODE", "MERGE_IN_REDUCE"]
 
@@ -32,16 +32,17 @@ LIB_PATH = os.path.join(_PKG, "libpa103.so")
 # pa_status
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE = range(6)
 # pa_dtype, pa_scale_mode, flags
-BF16, FP16, FP8_E4M3 = 0, 1, 2
-SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN, SCALE_PER_BLOCK = 0, 1, 2, 3
+BF16, FP16, FP8_E4M3, INT4 = 0, 1, 2, 3
+SCALE_NONE, SCALE_PER_TENSOR, SCALE_PER_TOKEN, SCALE_PER_BLOCK, SCALE_AFFINE = 0, 1, 2, 3, 4
 FLAG_BAD_LENGTHS, FLAG_BAD_BLOCK_ID, FLAG_WAIT_TIMEOUT, FLAG_STALE_PLAN = 1, 2, 4, 8
 FLAG_BAD_SELECTION, FLAG_NO_FREE_BLOCKS, FLAG_BAD_FREE_LIST = 16, 32, 64
+FLAG_BAD_POSITION = 128
 MERGE_AUTO, MERGE_IN_DECODE, MERGE_IN_REDUCE = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("pa_workspace_size", "pa_plan", "pa_decode", "pa_reduce", "pa_read_flags",
                     "pa_status_string", "pa_decode_step_static", "pa_gather_kv", "pa_append_kv",
                     "pa_build_tables", "pa_update_bounds", "pa_score_blocks", "pa_select_blocks",
-                    "pa_decode_selected")
+                    "pa_decode_selected", "pa_append_rotated", "pa_dequant_kv")
 
 # Bytes of the device array behind pa_decode_step_static (PA_STATIC_SCRATCH_BYTES).
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -54,6 +55,16 @@ class PaConfig(ctypes.Structure):
         "max_blocks_per_seq", "num_blocks", "q_dtype", "kv_dtype", "kv_scale_mode", "causal")] + [
         ("sm_scale", ctypes.c_float), ("num_ctas", ctypes.c_int32), ("grid_mult", ctypes.c_int32),
         ("split_merge", ctypes.c_int32)]
+
+
+class PaRotary(ctypes.Structure):
+    """Mirror of pa_rotary."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("cos_sin", ctypes.c_void_p), ("table_rows", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("num_axes", ctypes.c_int32),
+                ("axis_pairs", ctypes.c_int32 * 3), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 class PaError(RuntimeError):
@@ -100,6 +111,10 @@ def load(path: str = LIB_PATH):
     L.pa_decode_selected.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
                                      vp, vp]
     L.pa_decode_selected.restype = ctypes.c_int
+    L.pa_append_rotated.argtypes = [cfgp, ctypes.POINTER(PaRotary)] + [vp] * 14
+    L.pa_append_rotated.restype = ctypes.c_int
+    L.pa_dequant_kv.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, vp, vp]
+    L.pa_dequant_kv.restype = ctypes.c_int
     L.pa_status_string.argtypes = [ctypes.c_int]
     L.pa_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -163,7 +178,7 @@ def _types():
     if _type_cache is None:
         import torch
         cache = {BF16: (torch.bfloat16,), FP16: (torch.float16,),
-                 FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
+                 FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), INT4: (torch.uint8,)}
         device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _type_cache = device, (torch.int32,), (torch.int64,), (torch.float32,), cache
     device, i32, i64, f32, cache = _type_cache
@@ -204,10 +219,18 @@ def _scale(call: str, device: int, cfg: PaConfig, t, f32) -> Optional[int]:
     mode = cfg.kv_scale_mode
     if mode == SCALE_NONE:
         return None
-    if not 0 < mode <= SCALE_PER_BLOCK:
+    if not 0 < mode <= SCALE_AFFINE:
         return _ptr(t)
     heads = cfg.num_blocks * cfg.num_kv_heads
+    if mode == SCALE_AFFINE:  # pairs (step, low) in the queries' type
+        return _dense(call, device, 2 * heads * cfg.block_size, t, _types()[4].get(cfg.q_dtype, ()))
     return _dense(call, device, (0, 1, heads * cfg.block_size, heads)[mode], t, f32)
+
+
+def _cache_elements(cfg: PaConfig) -> int:
+    """Elements (bytes, for a 4-bit cache) of a K or V cache."""
+    n = cfg.num_blocks * cfg.block_size * cfg.num_kv_heads * cfg.head_dim
+    return n // 2 if cfg.kv_dtype == INT4 else n
 
 
 def plan(cfg: PaConfig, block_tables, context_lens, q_lens, ws, stream=None):
@@ -265,15 +288,15 @@ def gather_kv(cfg: PaConfig, k_cache, v_cache, block_tables, context_lens, k_out
 
 def append_kv(cfg: PaConfig, k_new, v_new, block_tables, context_lens, q_lens, k_cache, v_cache,
               k_scale=None, v_scale=None, flags=None, stream=None):
-    """Write a step's new K/V rows into their pages, quantised to fp8 for an fp8 cache (see
+    """Write a step's new K/V rows into their pages, quantised for an fp8 or 4-bit cache (see
     pa_append_kv in pa.h): new row i of sequence b lands at position
-    context_lens[b] - q_lens[b] + i.  Per-token scales are written into k_scale / v_scale; a
-    page's one scale (SCALE_PER_BLOCK) is raised where a new row needs it, and the page's older
-    codes follow."""
+    context_lens[b] - q_lens[b] + i.  Per-token scales, and a 4-bit cache's pairs (step, low)
+    [num_blocks, Hkv, block_size, 2], are written into k_scale / v_scale; a page's one scale
+    (SCALE_PER_BLOCK) is raised where a new row needs it, and the page's older codes follow."""
     dev, i32, _, f32, kinds = _types()
     name, B, row = "pa_append_kv", cfg.batch, cfg.num_kv_heads * cfg.head_dim
     kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
-    cache = cfg.num_blocks * cfg.block_size * row
+    cache = _cache_elements(cfg)
     _check(name, load().pa_append_kv(
         ctypes.byref(cfg), _dense(name, dev, B * cfg.max_q_len * row, k_new, kind),
         _dense(name, dev, B * cfg.max_q_len * row, v_new, kind),
@@ -373,7 +396,103 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
         _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
-_DT = {"bf16": BF16, "fp16": FP16, "fp8": FP8_E4M3}
+def _token_stride(call: str, t, rows: int, heads: int, dim: int) -> int:
+    """Elements between the tokens of [B, Sq, heads, dim] rows, each token's dense (0 for an address:
+    the rows lie dense)."""
+    if isinstance(t, int):
+        return 0
+    shape, stride = tuple(t.shape), t.stride()
+    if len(shape) != 4 or shape[0] * shape[1] < rows or shape[2:] != (heads, dim) or stride[3] != 1 \
+            or (heads > 1 and stride[2] != dim):
+        raise PaError(call, ERR_INVALID_ARG)
+    step = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else heads * dim
+    if shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * step:
+        raise PaError(call, ERR_INVALID_ARG)
+    return step
+
+
+def _rows(call: str, device: int, t, dtypes) -> int:
+    """Address of rows that need not lie dense (_token_stride looks at how they lie)."""
+    if isinstance(t, int):
+        return t
+    try:
+        if t.dtype in dtypes and t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise PaError(call, ERR_INVALID_ARG)
+
+
+def append_rotated(cfg: PaConfig, q, k_new, v_new, block_tables, context_lens, q_lens, q_out,
+                   k_cache, v_cache, k_scale=None, v_scale=None, *, cos_sin=None,
+                   interleaved: bool = False, positions=None, axis_pairs=None, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, k_out=None, flags=None, stream=None):
+    """Normalise (q_weight, k_weight) and rotate (cos_sin [positions, rotary_dim] fp32: cosines, then
+    sines) a step's queries and keys, into q_out and k_out, and write its K/V rows into their pages,
+    in one pass (see pa_append_rotated in pa.h).  q, k_new and v_new may be slices of one projection's
+    output.  positions [axes, B, Sq] default to the cache positions; axis_pairs: how many of the
+    rotated pairs follow each axis.  With k_cache and v_cache None nothing goes into pages."""
+    dev, i32, _, f32, kinds = _types()
+    name, B, D = "pa_append_rotated", cfg.batch, cfg.head_dim
+    kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
+    tokens, hq, hkv = B * cfg.max_q_len, cfg.num_q_heads, cfg.num_kv_heads
+    r = PaRotary(eps=eps, interleaved=int(interleaved))
+    r.q_weight = _maybe(name, dev, D, q_weight, kind)
+    r.k_weight = _maybe(name, dev, D, k_weight, kind)
+    if cos_sin is not None:
+        if len(getattr(cos_sin, "shape", ())) != 2:
+            raise PaError(name, ERR_INVALID_ARG)
+        r.table_rows, r.rotary_dim = cos_sin.shape
+        r.cos_sin = _dense(name, dev, r.table_rows * r.rotary_dim, cos_sin, f32)
+        pairs = list(axis_pairs) if axis_pairs is not None else [r.rotary_dim // 2]
+        if not 1 <= len(pairs) <= 3:
+            raise PaError(name, ERR_INVALID_ARG)
+        r.num_axes = len(pairs)
+        r.axis_pairs[:len(pairs)] = pairs
+        r.positions = _maybe(name, dev, len(pairs) * tokens, positions, i32)
+    r.q_stride = _token_stride(name, q, tokens, hq, D)
+    r.k_stride = _token_stride(name, k_new, tokens, hkv, D)
+    stores = k_cache is not None or v_cache is not None
+    pages = scales = (None, None)
+    vp = table = None
+    if stores:
+        r.v_stride = _token_stride(name, v_new, tokens, hkv, D)
+        vp = _rows(name, dev, v_new, kind)
+        table = _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32)
+        cache = _cache_elements(cfg)
+        pages = tuple(_dense(name, dev, cache, t, cache_kind) for t in (k_cache, v_cache))
+        scales = tuple(_scale(name, dev, cfg, t, f32) for t in (k_scale, v_scale))
+    _check(name, load().pa_append_rotated(
+        ctypes.byref(cfg), ctypes.byref(r), _rows(name, dev, q, kind), _rows(name, dev, k_new, kind),
+        vp, table, _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
+        _dense(name, dev, tokens * hq * D, q_out, kind), _maybe(name, dev, tokens * hkv * D, k_out, kind),
+        *pages, *scales, _maybe(name, dev, 1, flags, i32), _stream(stream)))
+
+
+def dequant_kv(cfg: PaConfig, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, k_out,
+               v_out, max_rows: Optional[int] = None, row_offsets=None, flags=None, stream=None):
+    """The batch's rows of an fp8 or 4-bit cache as values of q_dtype in contiguous buffers (see
+    pa_dequant_kv in pa.h): sequence b lands at rows row_offsets[b] .. row_offsets[b + 1] - 1 of k_out
+    and v_out, which have room for max_rows rows (by default what both hold)."""
+    dev, i32, _, f32, kinds = _types()
+    name, B, row = "pa_dequant_kv", cfg.batch, cfg.num_kv_heads * cfg.head_dim
+    kind, cache_kind, cache = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ()), _cache_elements(cfg)
+    if max_rows is None:
+        try:
+            max_rows = min(k_out.numel(), v_out.numel()) // max(1, row)
+        except AttributeError:
+            raise PaError(name, ERR_INVALID_ARG) from None
+    _check(name, load().pa_dequant_kv(
+        ctypes.byref(cfg), _dense(name, dev, cache, k_cache, cache_kind),
+        _dense(name, dev, cache, v_cache, cache_kind), _scale(name, dev, cfg, k_scale, f32),
+        _scale(name, dev, cfg, v_scale, f32),
+        _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32),
+        _dense(name, dev, B, context_lens, i32), _dense(name, dev, max_rows * row, k_out, kind),
+        _dense(name, dev, max_rows * row, v_out, kind), int(max_rows),
+        _maybe(name, dev, B + 1, row_offsets, i32), _maybe(name, dev, 1, flags, i32), _stream(stream)))
+
+
+_DT = {"bf16": BF16, "fp16": FP16, "fp8": FP8_E4M3, "int4": INT4}
 _SM = {"none": SCALE_NONE, "tensor": SCALE_PER_TENSOR, "token": SCALE_PER_TOKEN,
        "block": SCALE_PER_BLOCK}
 
@@ -389,7 +508,8 @@ def config_for(inp: dict, num_ctas: int = 0, grid_mult: int = 0,
                    max_blocks_per_seq=inp["block_tables"].shape[1],
                    num_blocks=inp["k_cache"].shape[0], q_dtype=_DT[w.q_dtype],
                    kv_dtype=_DT[w.kv_dtype],
-                   kv_scale_mode=_SM[w.scale_mode] if w.kv_dtype == "fp8" else SCALE_NONE,
+                   kv_scale_mode=_SM[w.scale_mode] if w.kv_dtype == "fp8" else
+                   SCALE_AFFINE if w.kv_dtype == "int4" else SCALE_NONE,
                    causal=int(w.causal), sm_scale=float(inp["sm_scale"]), num_ctas=num_ctas,
                    grid_mult=grid_mult, split_merge=split_merge)
     q = inp["q"]

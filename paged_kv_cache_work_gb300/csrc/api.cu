@@ -26,10 +26,10 @@ pa_status validate(const pa_config* c) {
   if (c->batch < 1 || c->max_q_len < 1 || c->num_q_heads < 1 || c->num_kv_heads < 1 ||
       c->max_blocks_per_seq < 1 || c->num_blocks < 1 || c->head_dim < 1 || c->block_size < 1)
     return PA_ERR_INVALID_ARG;
-  if (c->q_dtype < PA_BF16 || c->q_dtype > PA_FP8_E4M3 || c->kv_dtype < PA_BF16 ||
-      c->kv_dtype > PA_FP8_E4M3)
+  if (c->q_dtype < PA_BF16 || c->q_dtype > PA_INT4 || c->kv_dtype < PA_BF16 ||
+      c->kv_dtype > PA_INT4)
     return PA_ERR_INVALID_ARG;
-  if (c->kv_scale_mode < PA_SCALE_NONE || c->kv_scale_mode > PA_SCALE_PER_BLOCK)
+  if (!scale_mode_known(*c))
     return PA_ERR_INVALID_ARG;
   if (c->causal != 0 && c->causal != 1) return PA_ERR_INVALID_ARG;
   if (!std::isfinite(c->sm_scale)) return PA_ERR_INVALID_ARG;
@@ -41,8 +41,7 @@ pa_status validate(const pa_config* c) {
   if (!is_pow2(c->block_size) || c->block_size < 16 || c->block_size > 1024)
     return PA_ERR_UNSUPPORTED;
   if (c->q_dtype != PA_BF16 && c->q_dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
-  if (c->kv_dtype != c->q_dtype && c->kv_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
-  if (c->kv_dtype != PA_FP8_E4M3 && c->kv_scale_mode != PA_SCALE_NONE) return PA_ERR_UNSUPPORTED;
+  if (!kv_kind_taken(*c)) return PA_ERR_UNSUPPORTED;
   const long long rows = (long long)(c->num_q_heads / c->num_kv_heads) * c->max_q_len;
   if (rows > (1 << 20)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
@@ -187,7 +186,7 @@ pa_status pa_plan(const pa_config* cfg, const int32_t* block_tables, const int32
 }
 
 pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
-                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                    const void* k_scale, const void* v_scale, const int32_t* block_tables,
                     const int32_t* context_lens, const int32_t* q_lens, void* out, float* lse,
                     void* ws, size_t ws_bytes, pa_stream stream) {
   Variant v;
@@ -200,16 +199,20 @@ pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, co
     return PA_ERR_INVALID_ARG;
   if (lse && !aligned(lse, 4)) return PA_ERR_INVALID_ARG;
   if (cfg->kv_scale_mode != PA_SCALE_NONE) {
-    if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    const uintptr_t to = cfg->kv_dtype == PA_INT4 ? 16 : 4;
+    if (!k_scale || !v_scale || !aligned(k_scale, to) || !aligned(v_scale, to))
       return PA_ERR_INVALID_ARG;
   }
   if ((st = check_ws(ws, ws_bytes, L)) != PA_OK) return st;
 
   const int box_rows = v.path == 3 ? 16 : cfg->block_size < v.tt ? cfg->block_size : v.tt;
-  CUtensorMap kmap, vmap;
-  if (!kv_tensor_map(&kmap, k_cache, *cfg, box_rows, v.path >= 1) ||
-      !kv_tensor_map(&vmap, v_cache, *cfg, box_rows, v.path >= 1))
+  CUtensorMap kmap{}, vmap{};
+  if (v.path == 4) {
+    // (the 4-bit kernel reads the caches by address)
+  } else if (!kv_tensor_map(&kmap, k_cache, *cfg, box_rows, v.path >= 1) ||
+             !kv_tensor_map(&vmap, v_cache, *cfg, box_rows, v.path >= 1)) {
     return PA_ERR_CUDA;
+  }
 
   DecodeArgs a;
   a.p = problem_args(*cfg, block_tables, context_lens, q_lens);
@@ -226,7 +229,10 @@ pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, co
   a.L = L;
   a.v = v;
   a.q_kind = cfg->q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
-  a.kv_kind = cfg->kv_dtype == PA_FP8_E4M3 ? KV_FP8 : cfg->kv_dtype == PA_FP16 ? KV_FP16 : KV_BF16;
+  a.kv_kind = cfg->kv_dtype == PA_INT4       ? KV_INT4
+              : cfg->kv_dtype == PA_FP8_E4M3 ? KV_FP8
+              : cfg->kv_dtype == PA_FP16     ? KV_FP16
+                                             : KV_BF16;
   cudaError_t e = launch_decode(a, kmap, vmap, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -270,6 +276,7 @@ pa_status pa_decode_selected(const pa_config* cfg, const void* q, const void* k_
       !aligned(selected, 4) || !aligned(num_selected, 4) || !aligned(lse, 4) || !aligned(flags, 4))
     return PA_ERR_INVALID_ARG;
   const pa_config& c = *cfg;
+  if (c.kv_dtype == PA_INT4) return PA_ERR_UNSUPPORTED;
   const int mode = c.kv_scale_mode;
   if (mode != PA_SCALE_NONE &&
       (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))

@@ -1,0 +1,96 @@
+// Rows of a 4-bit cache: codes c in 0 .. 15, two a byte, and a pair (step, low) of the queries' type
+// for each token and kv head; a value is low + step c.
+//
+// A warp quantises a row whose lanes hold D / 32 consecutive elements each.  low is the row's least
+// element rounded down to the pair's type (an element itself when the row has that type), step the
+// least number of the type that is not below (max - low) / 15, so that every quotient lies in
+// [0, 15] and none is clipped.  One row of pairs for a page and kv head lies together: the decode
+// copies a tile's pairs as one run.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+#if defined(__CUDACC__)
+
+// (step, low) of a pair's four bytes as fp32.
+template <int QK>
+__device__ __forceinline__ float2 pair_values(uint32_t w) {
+  if constexpr (QK == Q_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// The largest number of the pair's type that is <= x / the least that is >= x (bits).
+template <int QK>
+__device__ __forceinline__ uint16_t round_down(float x) {
+  if constexpr (QK == Q_BF16) {
+    const uint32_t u = __float_as_uint(x);  // a negative number's magnitude grows
+    return (uint16_t)(((u >> 31) ? u + 0xffffu : u) >> 16);
+  } else {
+    return __half_as_ushort(__float2half_rd(x));
+  }
+}
+template <int QK>
+__device__ __forceinline__ uint16_t round_up_nonneg(float x) {
+  if constexpr (QK == Q_BF16)
+    return (uint16_t)((__float_as_uint(x) + 0xffffu) >> 16);
+  else
+    return __half_as_ushort(__float2half_ru(x));
+}
+
+// y / s correctly rounded for y = 0 or y in [2^-70, 2^70] and s in [2^-60, 2^60]: with the
+// reciprocal r correctly rounded, one step of Markstein's ("Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990): q = y r, q + (y - q s) r.
+__device__ __forceinline__ float quotient(float y, float s, float r) {
+  const float q = __fmul_rn(y, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
+}
+
+// The warp's row, E elements a lane: its codes (the lane's first in the lowest four bits) and pair.
+template <int QK, int E>
+__device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], uint32_t* pair) {
+  float lo = x[0], hi = x[0];
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    lo = fminf(lo, x[k]);
+    hi = fmaxf(hi, x[k]);
+    nan |= x[k] != x[k];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  const uint32_t low_bits = round_down<QK>(lo);
+  const float low = pair_values<QK>(low_bits << 16).y;
+  const float range = hi - low;
+  if (__any_sync(kFull, nan) || !(range < INFINITY)) {
+    *pair = 0x7fffu | low_bits << 16;  // step NaN (in both types)
+    return 0;
+  }
+  const uint32_t step_bits = round_up_nonneg<QK>(__fdiv_rn(range, 15.f));
+  const float step = pair_values<QK>(step_bits).x;
+  *pair = step_bits | low_bits << 16;
+  if (step == 0.f) return 0;
+  uint32_t codes = 0;
+  const bool plain = step >= 0x1p-60f && step <= 0x1p60f;
+  const float inv = __fdiv_rn(1.f, step);
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    const float y = x[k] - low;
+    // (a y below 2^-70 gives a quotient below a half by either way of dividing)
+    const float q = plain ? quotient(y, step, inv) : __fdiv_rn(y, step);
+    // the integer nearest to q in [0, 15] in the low bits of 2^23 + q (ties to even)
+    codes |= (__float_as_uint(q + 8388608.f) & 15u) << (4 * k);
+  }
+  return codes;
+}
+
+#endif  // __CUDACC__
+}  // namespace pa

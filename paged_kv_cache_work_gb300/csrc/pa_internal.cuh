@@ -17,7 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kFull = 0xffffffffu;
 
-enum KvKind { KV_BF16 = 0, KV_FP16 = 1, KV_FP8 = 2 };
+enum KvKind { KV_BF16 = 0, KV_FP16 = 1, KV_FP8 = 2, KV_INT4 = 3 };
 enum QKind { Q_BF16 = 0, Q_FP16 = 1 };
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -29,7 +29,8 @@ __host__ __device__ constexpr size_t round_up_sz(size_t a, size_t b) { return (a
 // tiles of `mp` (a power of two); a unit of work is one (sequence, kv head, row
 // tile), and `tt` is the number of tokens staged per pipeline stage.
 struct Variant {
-  int path;         // 0: CUDA-core kernel, 1: mma.sync kernel, 2: tcgen05 kernel, 3: streaming kernel
+  int path;         // 0: CUDA-core kernel, 1: mma.sync kernel, 2: tcgen05 kernel, 3: streaming kernel,
+                    // 4: 4-bit kernel
   int rows;         // M = G * Sq
   int mp;           // rows per unit (padded to a power of two)
   int rb;           // row tiles per kv head
@@ -37,7 +38,7 @@ struct Variant {
   int units;        // B * Hkv * rb
   int ctas;         // persistent grid size C
   int ctas_per_sm;  // decode CTAs resident per SM
-  int bpe;          // bytes per cache element
+  int bpe;          // bytes per cache element (0: half a byte)
   int item_cost;    // tokens of work a unit costs on top of its own (a tile multiple)
   int ns_dec;       // the decode merges a split unit of at most this many pieces itself
   int sms;          // SMs of the device when the grid was sized from it, else 0
@@ -75,10 +76,23 @@ inline int staged_scales(int mode) {
   return mode == PA_SCALE_PER_TOKEN ? SC_TOKEN : mode == PA_SCALE_PER_BLOCK ? SC_BLOCK : SC_NONE;
 }
 
+// A cache's type and scale mode that go together: the queries' 16 bits without scales, fp8 with any
+// mode but pairs, 4 bits with pairs.
+inline bool scale_mode_known(const pa_config& c) {
+  return c.kv_scale_mode >= PA_SCALE_NONE &&
+         c.kv_scale_mode <= (c.kv_dtype == PA_INT4 ? PA_SCALE_AFFINE : PA_SCALE_PER_BLOCK);
+}
+inline bool kv_kind_taken(const pa_config& c) {
+  if (c.kv_dtype == PA_INT4) return c.kv_scale_mode == PA_SCALE_AFFINE;
+  if (c.kv_dtype == PA_FP8_E4M3) return true;
+  return c.kv_dtype == c.q_dtype && c.kv_scale_mode == PA_SCALE_NONE;
+}
+
 // CTAs of the decode instance for these parameters that fit on one SM.
 int simt_ctas_per_sm(int head_dim, int mp, int kvk, bool toks);
 int mma_ctas_per_sm(int head_dim, int mp, int kvk, int scales);
 int stream_ctas_per_sm(int head_dim);
+int int4_ctas_per_sm(int head_dim, int mp);
 // Largest row tile of the tensor-core decode kernel.
 constexpr int kMmaMaxRows = 64;
 
@@ -114,6 +128,12 @@ constexpr int stream_max_rows(int head_dim) {
   return head_dim == 64 ? 0x7fffffff : 32;
 }
 
+// The 4-bit kernel: query rows of a tile, the tokens that a CTA's warps take in a round, and the cost
+// of an item in such rounds.
+constexpr int int4_tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
+constexpr int kInt4RoundTokens = 64;
+constexpr int kInt4ItemCostRounds = 5;
+
 // Query rows per kv head above which a 128-dim head runs on the tcgen05 kernel.
 constexpr int kTcMinRows = 33;
 
@@ -129,6 +149,17 @@ constexpr int kTcMinRows = 33;
 inline Variant make_variant(const pa_config& c) {
   Variant v{};
   v.rows = (c.num_q_heads / c.num_kv_heads) * c.max_q_len;
+  if (c.kv_dtype == PA_INT4) {
+    v.path = 4;
+    v.mp = int4_tile_rows(v.rows);
+    v.rb = ceil_div(v.rows, v.mp);
+    v.tt = kInt4RoundTokens;
+    v.item_cost = kInt4ItemCostRounds * v.tt;
+    v.units = c.batch * c.num_kv_heads * v.rb;
+    v.ctas_per_sm = int4_ctas_per_sm(c.head_dim, v.mp);
+    v.ns_dec = decode_merge_limit(c.split_merge, v.path);
+    return v;
+  }
   v.bpe = c.kv_dtype == PA_FP8_E4M3 ? 1 : 2;
   v.path = c.head_dim * v.bpe >= 128 ? 1 : 0;
   if (v.path == 1 && c.head_dim >= 128 && v.rows >= kTcMinRows &&
@@ -284,8 +315,8 @@ struct DecodeArgs {
   const void* q;
   const void* k_cache;
   const void* v_cache;
-  const float* k_scale;
-  const float* v_scale;
+  const void* k_scale;
+  const void* v_scale;
   int scale_mode;
   float qk_scale;  // sm_scale * log2(e)
   void* out;

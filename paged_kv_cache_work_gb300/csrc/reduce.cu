@@ -32,6 +32,12 @@ cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, co
 
 cudaError_t launch_stream(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int, int,
                           cudaStream_t);
+cudaError_t launch_int4_d64(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d128(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d256(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
+int int4_ctas_per_sm_d64(int);
+int int4_ctas_per_sm_d128(int);
+int int4_ctas_per_sm_d256(int);
 int mma_ctas_per_sm_d64(int, int, int);
 int mma_ctas_per_sm_d128(int, int, int);
 int mma_ctas_per_sm_d256(int, int, int);
@@ -55,11 +61,19 @@ int mma_ctas_per_sm(int head_dim, int mp, int kvk, int scales) {
   }
 }
 
+int int4_ctas_per_sm(int head_dim, int mp) {
+  switch (head_dim) {
+    case 64: return int4_ctas_per_sm_d64(mp);
+    case 128: return int4_ctas_per_sm_d128(mp);
+    default: return int4_ctas_per_sm_d256(mp);
+  }
+}
+
 KernelParams make_kernel_params(const DecodeArgs& a) {
   KernelParams p{};
   p.q = a.q;
-  p.k_scale = a.k_scale;
-  p.v_scale = a.v_scale;
+  p.k_scale = static_cast<const float*>(a.k_scale);
+  p.v_scale = static_cast<const float*>(a.v_scale);
   p.bt = a.p.block_tables;
   p.ctx = a.p.context_lens;
   p.qlens = a.p.q_lens;
@@ -100,6 +114,17 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CU
   const KernelParams prm = make_kernel_params(a);
   const int scales = staged_scales(a.scale_mode);
   const bool toks = scales != SC_NONE;
+  if (a.v.path == 4) {
+    const Int4View cache{static_cast<const char*>(a.k_cache), static_cast<const char*>(a.v_cache),
+                         static_cast<const uint32_t*>(a.k_scale),
+                         static_cast<const uint32_t*>(a.v_scale)};
+    switch (a.p.head_dim) {
+      case 64: return launch_int4_d64(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 128: return launch_int4_d128(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 256: return launch_int4_d256(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
+      default: return cudaErrorNotSupported;
+    }
+  }
   if (a.v.path == 3)
     return launch_stream(prm, kmap, vmap, a.v.ctas, a.p.head_dim, a.q_kind, s);
   if (a.v.path == 2) {

@@ -37,7 +37,7 @@ pa_status scratch_on_current_device(void** out) {
 
 extern "C" pa_status pa_decode_step_static(const pa_config* cfg, const void* q,
                                            const void* k_cache, const void* v_cache,
-                                           const float* k_scale, const float* v_scale,
+                                           const void* k_scale, const void* v_scale,
                                            const int32_t* block_tables,
                                            const int32_t* context_lens, const int32_t* q_lens,
                                            void* out, float* lse, pa_stream stream) {

@@ -1,0 +1,392 @@
+"""pa_append_rotated against 64 bits: norms, rotations of every layout, axes, strides, caches; equality
+with the separate append where the two define the same rounding; flags, refusals, graphs."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_work_gb300 as pa
+import plain64
+import plain_int4 as plain
+
+KINDS = {"bf16": (torch.bfloat16, pa.BF16), "fp16": (torch.float16, pa.FP16)}
+CACHES = {"16": (None, pa.SCALE_NONE), "8none": (pa.FP8_E4M3, pa.SCALE_NONE), "8tensor": (pa.FP8_E4M3, pa.SCALE_PER_TENSOR),
+          "8token": (pa.FP8_E4M3, pa.SCALE_PER_TOKEN), "4": (pa.INT4, pa.SCALE_AFFINE)}
+
+
+def config(B, sq, hq, hkv, d, bs, maxb, nblocks, dtype="bf16", kv="16", **kw):
+    kind, mode = CACHES[kv]
+    return pa.PaConfig(batch=B, max_q_len=sq, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs,
+                       max_blocks_per_seq=maxb, num_blocks=nblocks, q_dtype=KINDS[dtype][1],
+                       kv_dtype=KINDS[dtype][1] if kind is None else kind, kv_scale_mode=mode, sm_scale=d ** -0.5, **kw)
+
+
+def ints(x, dev):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)
+
+
+def angles(rows, rd):
+    a = np.arange(rows)[:, None] * 10000.0 ** (-np.arange(0, rd, 2) / rd)
+    return torch.from_numpy(np.concatenate((np.cos(a), np.sin(a)), 1)).float()
+
+
+class Problem:
+    def __init__(self, seed, B, sq, hq, hkv, d, bs, dtype, kv, rd, axes, interleaved, norm, fused):
+        rng = np.random.default_rng(seed)
+        t = KINDS[dtype][0]
+        self.__dict__.update(B=B, sq=sq, hq=hq, hkv=hkv, d=d, bs=bs, dtype=dtype, kv=kv, rd=rd, interleaved=interleaved, t=t)
+        self.ql = rng.integers(0, sq + 1, B)
+        self.ql[0] = sq
+        self.ctx = self.ql + rng.integers(0, 3 * bs, B)
+        self.bt, self.nblocks = plain.tables(rng, self.ctx, bs)
+        qkv = torch.from_numpy(rng.standard_normal((B, sq, hq + 2 * hkv, d)) * rng.choice([0.1, 1, 4], (B, sq, 1, 1))).to(t)
+        self.fused, self.qkv = fused, qkv
+        self.q, self.k, self.v = qkv[:, :, :hq], qkv[:, :, hq:hq + hkv], qkv[:, :, hq + hkv:]
+        self.wq = torch.from_numpy(1 + 0.3 * rng.standard_normal(d)).to(t) if norm in ("both", "q") else None
+        self.wk = torch.from_numpy(1 + 0.3 * rng.standard_normal(d)).to(t) if norm in ("both", "k") else None
+        rows = int(self.ctx.max()) + 1
+        self.cs = angles(rows, rd) if rd else None
+        half = rd // 2
+        self.axis_pairs = {1: [half], 2: [half // 4, half - half // 4], 3: [half - 2 * (half // 3), half // 3, half // 3]}[axes]
+        self.pos = None if axes == 1 else torch.from_numpy(rng.integers(0, rows, (axes, B, sq)).astype(np.int32))
+        shape = (self.nblocks, bs, hkv, d)
+        if kv == "16":
+            make = lambda: torch.from_numpy(rng.standard_normal(shape)).to(t)  # noqa: E731
+        elif kv == "4":
+            make = lambda: torch.from_numpy(rng.integers(0, 256, (*shape[:3], d // 2)).astype(np.uint8))  # noqa: E731
+        else:
+            make = lambda: torch.from_numpy(rng.integers(0, 0x78, shape).astype(np.uint8))  # noqa: E731
+        self.kc, self.vc = make(), make()
+        self.ks = self.vs = None
+        if kv == "8tensor":
+            self.ks, self.vs = torch.tensor([0.03]), torch.tensor([0.02])
+        elif kv == "8token":
+            self.ks, self.vs = torch.ones(shape[:3]), torch.ones(shape[:3])
+        elif kv == "4":
+            self.ks, self.vs = torch.ones(shape[0], hkv, bs, 2, dtype=t), torch.ones(shape[0], hkv, bs, 2, dtype=t)
+        self.cfg = config(B, sq, hq, hkv, d, bs, self.bt.shape[1], self.nblocks, dtype, kv)
+
+    def on(self, dev):
+        g = lambda x: None if x is None else x.to(dev)  # noqa: E731
+        if self.fused:
+            qkv = self.qkv.to(dev)
+            q, k, v = qkv[:, :, :self.hq], qkv[:, :, self.hq:self.hq + self.hkv], qkv[:, :, self.hq + self.hkv:]
+        else:
+            q, k, v = (x.contiguous().to(dev) for x in (self.q, self.k, self.v))
+        self.dev = dict(q=q, k=k, v=v, bt=ints(self.bt, dev), ctx=ints(self.ctx, dev), ql=ints(self.ql, dev),
+                        qo=torch.full((self.B, self.sq, self.hq, self.d), 5.0, dtype=self.t, device=dev),
+                        ko=torch.full((self.B, self.sq, self.hkv, self.d), 5.0, dtype=self.t, device=dev),
+                        kc=g(self.kc), vc=g(self.vc), ks=g(self.ks), vs=g(self.vs), flags=ints([0], dev),
+                        kw=dict(cos_sin=g(self.cs), interleaved=self.interleaved, positions=g(self.pos),
+                                axis_pairs=self.axis_pairs if self.cs is not None else None, q_weight=g(self.wq),
+                                k_weight=g(self.wk), eps=1e-5))
+        return self.dev
+
+    def call(self, dev, k_out=True):
+        x = self.on(dev)
+        pa.append_rotated(self.cfg, x["q"], x["k"], x["v"], x["bt"], x["ctx"], x["ql"], x["qo"], x["kc"], x["vc"],
+                          x["ks"], x["vs"], k_out=x["ko"] if k_out else None, flags=x["flags"], **x["kw"])
+        return x
+
+    def rotated(self, b, i):
+        """The token's q and k heads in 64 bits."""
+        pos = [self.ctx[b] - self.ql[b] + i] * 3 if self.pos is None else self.pos[:, b, i].tolist()
+        cs = None if self.cs is None else self.cs.double().numpy()
+        f = lambda x, w: plain.rotate(x.double().numpy(), None if w is None else w.double().numpy(),  # noqa: E731
+                                      float(np.float32(1e-5)), cs, pos, self.axis_pairs, self.interleaved)
+        return f(self.q[b, i], self.wq), f(self.k[b, i], self.wk)
+
+
+# fp32: a sum of D squares, a root, a division, two products and the rotation's three operations, each
+# off by at most 2^-24 of the magnitudes that enter it, come to less than 16 of them for a rotated pair
+FP32 = 16 * 2.0 ** -24
+
+
+def off(got, want, pair_size, t):
+    """Within half a step of the type t of an fp32 value."""
+    half = torch.finfo(t).eps / 2
+    tol = half * np.abs(want) + FP32 * pair_size * 1.01 + torch.finfo(t).smallest_normal * half
+    return np.abs(got - want) <= tol * (1 + 2.0 ** -9)
+
+
+def sizes(x, rd, interleaved):
+    """Magnitude of the pair that each channel of [H, D] belongs to."""
+    s = np.abs(x).copy()
+    half = rd // 2
+    for p in range(half):
+        i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + half)
+        s[:, i] = s[:, j] = np.abs(x[:, i]) + np.abs(x[:, j])
+    return s
+
+
+CASES = [
+    # B, Sq, Hq, Hkv, D, bs, dtype, cache, rotary_dim, axes, interleaved, norm, fused
+    (3, 1, 8, 2, 128, 16, "bf16", "16", 128, 1, False, "both", True), (2, 5, 4, 4, 64, 16, "fp16", "16", 64, 1, True, "both", False),
+    (2, 3, 3, 1, 256, 32, "bf16", "16", 256, 3, False, "both", True), (1, 40, 2, 1, 128, 64, "bf16", "16", 32, 1, False, None, True),
+    (2, 4, 6, 3, 64, 128, "bf16", "16", 16, 1, False, "k", False), (2, 4, 5, 1, 256, 16, "fp16", "16", 64, 3, True, "q", True),
+    (2, 2, 4, 2, 128, 16, "fp16", "16", 0, 1, False, "both", False), (2, 6, 4, 2, 128, 16, "bf16", "16", 96, 2, False, None, True),
+    (3, 4, 8, 2, 128, 16, "bf16", "8token", 128, 1, False, "both", True), (2, 3, 4, 1, 64, 32, "fp16", "8token", 64, 1, True, None, False),
+    (2, 3, 4, 1, 256, 1024, "bf16", "8tensor", 128, 1, False, "both", True), (2, 3, 4, 2, 128, 16, "bf16", "8none", 128, 3, False, "both", False),
+    (3, 4, 8, 2, 128, 16, "bf16", "4", 128, 1, False, "both", True), (2, 7, 4, 1, 64, 32, "fp16", "4", 32, 1, True, "both", False),
+    (2, 3, 4, 2, 256, 16, "bf16", "4", 256, 3, False, None, True), (1, 1, 1, 1, 128, 16, "bf16", "4", 128, 1, False, "both", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES)
+def test_matches_64_bits(case, cuda_device, pa):
+    p = Problem(17, *case)
+    x = p.call(cuda_device)
+    assert int(x["flags"].item()) == 0
+    qo, ko = x["qo"].double().cpu().numpy(), x["ko"].double().cpu().numpy()
+    kc = x["kc"].cpu()
+    for b in range(p.B):
+        for i in range(p.sq):
+            if i >= p.ql[b]:  # rows behind a sequence's last: as they were
+                assert (qo[b, i] == 5).all() and (ko[b, i] == 5).all()
+                continue
+            zq, zk = p.rotated(b, i)
+            assert off(qo[b, i], zq, sizes(zq, p.rd, p.interleaved), p.t).all()
+            assert off(ko[b, i], zk, sizes(zk, p.rd, p.interleaved), p.t).all()
+            pos = p.ctx[b] - p.ql[b] + i
+            blk, slot = p.bt[b, pos // p.bs], pos % p.bs
+            if p.kv == "16":
+                assert torch.equal(kc[blk, slot], x["ko"][b, i].cpu())
+                assert torch.equal(x["vc"][blk, slot].cpu(), p.v[b, i])
+                continue
+            # half a step of the cache's codes around the 64-bit key, and the fp32 error of the key
+            for g in range(p.hkv):
+                want, slack = zk[g], FP32 * sizes(zk, p.rd, p.interleaved)[g] * 1.01
+                if p.kv == "4":
+                    step, low = (float(f) for f in x["ks"][blk, g, slot])
+                    got = plain.unpack(kc[blk, slot, g].numpy()) * step + low
+                    rs, rl = plain.to_type((want.max() - low) / 15, p.t, True), plain.to_type(want.min(), p.t, False)
+                    unit = torch.finfo(p.t).eps
+                    assert abs(step - rs) <= unit * rs and abs(low - rl) <= unit * abs(rl)
+                    assert (np.abs(got - want) <= step / 2 + slack + 2.0 ** -22 * (abs(low) + 15 * step)).all()
+                else:
+                    scale = {"8none": 1.0, "8tensor": 0.03}.get(p.kv) or float(x["ks"][blk, slot, g])
+                    scale = float(np.float32(scale))
+                    if p.kv == "8token":
+                        assert abs(scale - np.abs(want).max() / 448) <= scale * 2.0 ** -20
+                    got = kc[blk, slot, g].view(torch.float8_e4m3fn).double().numpy() * scale
+                    clip = np.clip(want, -448 * scale, 448 * scale)
+                    assert (np.abs(got - clip) <= 2.0 ** -4 * np.abs(clip) * 1.001 + scale * 2.0 ** -10 + slack).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [c for c in CASES if c[7] != "16"] + [CASES[0], CASES[3]])
+def test_values_as_the_append_writes_them(case, cuda_device, pa):
+    """V rows, and K rows where nothing turns or normalises them, are pa_append_kv's bit for bit; what
+    no new row belongs to is left as it was."""
+    case = list(case)
+    case[8], case[9], case[11] = 0, 1, None
+    p = Problem(23, *case)
+    x = p.call(cuda_device, k_out=False)
+    g = lambda t: None if t is None else t.to(cuda_device)  # noqa: E731
+    kc, vc, ks, vs = g(p.kc), g(p.vc), g(p.ks), g(p.vs)
+    pa.append_kv(p.cfg, p.k.contiguous().to(cuda_device), p.v.contiguous().to(cuda_device), x["bt"], x["ctx"], x["ql"],
+                 kc, vc, ks, vs)
+    assert torch.equal(x["kc"].view(torch.uint8), kc.view(torch.uint8))
+    assert torch.equal(x["vc"].view(torch.uint8), vc.view(torch.uint8))
+    if ks is not None:
+        assert torch.equal(x["ks"], ks) and torch.equal(x["vs"], vs)
+
+
+@pytest.mark.gpu
+def test_rotates_in_place_and_without_pages(cuda_device, pa):
+    """q_out and k_out may be q and k; without caches nothing else is touched; the keys then go into
+    pages with one scale by pa_append_kv, whose bounds they give too."""
+    p = Problem(3, 2, 4, 8, 2, 128, 16, "bf16", "16", 128, 1, False, "both", False)
+    x = p.call(cuda_device)
+    q, k = p.q.contiguous().to(cuda_device), p.k.contiguous().to(cuda_device)
+    pa.append_rotated(p.cfg, q, k, None, None, x["ctx"], x["ql"], q, None, None, k_out=k, flags=x["flags"], **x["kw"])
+    for b in range(p.B):
+        n = p.ql[b]
+        assert torch.equal(q[b, :n], x["qo"][b, :n]) and torch.equal(k[b, :n], x["ko"][b, :n])
+        assert torch.equal(q[b, n:].cpu(), p.q[b, n:]) and torch.equal(k[b, n:].cpu(), p.k[b, n:])
+
+
+@pytest.mark.gpu
+def test_flags(cuda_device, pa):
+    p = Problem(4, 3, 4, 4, 2, 128, 16, "bf16", "4", 64, 3, False, "both", True)
+    clean = p.call(cuda_device)
+    assert int(clean["flags"].item()) == 0
+    kept = {n: clean[n].clone() for n in ("qo", "ko", "kc", "vc")}
+    # a position outside the table: that token is not written at all
+    p.pos[1, 0, 1] = p.cs.shape[0]
+    x = p.call(cuda_device)
+    assert int(x["flags"].item()) == pa.FLAG_BAD_POSITION
+    assert (x["qo"][0, 1] == 5).all() and (x["ko"][0, 1] == 5).all()
+    assert torch.equal(x["qo"][0, 0], kept["qo"][0, 0]) and torch.equal(x["qo"][1:], kept["qo"][1:])
+    pos = int(p.ctx[0] - p.ql[0] + 1)
+    blk, slot = int(p.bt[0, pos // 16]), pos % 16
+    assert torch.equal(x["kc"][blk, slot].cpu(), p.kc[blk, slot])
+    p.pos[1, 0, 1] = -1
+    assert int(p.call(cuda_device)["flags"].item()) == pa.FLAG_BAD_POSITION
+    p.pos[1, 0, 1] = 0
+    # a page outside the pool: queries are rotated all the same
+    first = int(p.ctx[0] - p.ql[0]) // 16
+    was = p.bt.copy()
+    p.bt[0, first] = p.nblocks
+    x = p.call(cuda_device)
+    assert int(x["flags"].item()) == pa.FLAG_BAD_BLOCK_ID
+    assert torch.equal(x["qo"][0, 0], kept["qo"][0, 0]) and torch.equal(x["ko"][0, 0], kept["ko"][0, 0])
+    # a bad length: nothing of that sequence
+    p.bt, p.ql[2] = was, 5
+    x = p.call(cuda_device)
+    assert int(x["flags"].item()) == pa.FLAG_BAD_LENGTHS
+    assert (x["qo"][2] == 5).all() and torch.equal(x["qo"][1], kept["qo"][1])
+
+
+@pytest.mark.gpu
+def test_replays_in_a_graph(cuda_device, pa):
+    p = Problem(8, 3, 2, 8, 2, 128, 16, "bf16", "8token", 128, 1, False, "both", True)
+    want = {n: t.clone() for n, t in p.call(cuda_device).items() if n in ("qo", "kc", "vc", "ks")}
+    x = p.on(cuda_device)
+    call = lambda: pa.append_rotated(p.cfg, x["q"], x["k"], x["v"], x["bt"], x["ctx"], x["ql"], x["qo"], x["kc"],  # noqa: E731
+                                     x["vc"], x["ks"], x["vs"], flags=x["flags"], **x["kw"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        x["qo"].fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in want.items():
+            assert torch.equal(x[n].view(torch.uint8), t.view(torch.uint8)), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,dtype", [("16", "bf16"), ("8token", "bf16"), ("4", "bf16"), ("4", "fp16")])
+def test_prompt_then_step(kv, dtype, cuda_device, pa):
+    """A prompt and a step of draft tokens through rotation, pages and decode, against 64 bits on the
+    values that the cache holds; scores depend on the distance of positions alone."""
+    dev, B, hq, hkv, d, bs = cuda_device, 2, 8, 2, 128, 16
+    t = KINDS[dtype][0]
+    rng = np.random.default_rng(2)
+    end = np.array([60, 37])
+    bt, nblocks = plain.tables(rng, end, bs)
+    cs = angles(64, d)
+    kind, _ = CACHES[kv]
+    byte = kind is not None
+    shape = (nblocks, bs, hkv, d // 2 if kv == "4" else d)
+    kc, vc = (torch.zeros(shape, dtype=torch.uint8 if byte else t, device=dev) for _ in "kv")
+    scale = {"8token": (shape[:3], torch.float32), "4": ((nblocks, hkv, bs, 2), t)}.get(kv)
+    ks, vs = (None if scale is None else torch.zeros(scale[0], dtype=scale[1], device=dev) for _ in "kv")
+    w = torch.from_numpy(1 + 0.2 * rng.standard_normal(d)).to(t).to(dev)
+    dbt = ints(bt, dev)
+    for sq, ql in ((56, end - 4), (4, np.array([4, 4]))):
+        ctx = ql if sq == 56 else end
+        cfg = config(B, sq, hq, hkv, d, bs, bt.shape[1], nblocks, dtype, kv, causal=1)
+        qkv = torch.from_numpy(rng.standard_normal((B, sq, hq + 2 * hkv, d))).to(t).to(dev)
+        q = torch.zeros(B, sq, hq, d, dtype=t, device=dev)
+        args = dbt, ints(ctx, dev), ints(ql, dev)
+        pa.append_rotated(cfg, qkv[:, :, :hq], qkv[:, :, hq:hq + hkv], qkv[:, :, hq + hkv:], *args, q, kc, vc, ks, vs,
+                          cos_sin=cs.to(dev), q_weight=w, k_weight=w)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=dev)
+        ws = torch.empty(pa.workspace_size(cfg), dtype=torch.uint8, device=dev)
+        pa.plan(cfg, *args, ws)
+        pa.decode(cfg, q, kc, vc, ks, vs, *args, out, lse, ws)
+        pa.reduce(cfg, out, lse, ws)
+        if kv == "4":
+            k64, v64 = plain.values(kc.cpu(), ks.cpu()), plain.values(vc.cpu(), vs.cpu())
+            pair = vs.cpu().double().numpy().transpose(0, 2, 1, 3)
+            mid = pair[..., 1:] + 8 * pair[..., :1]
+            mag = np.abs(v64 - mid) + np.abs(mid)
+        else:
+            k64, v64 = (plain64.values(c.cpu(), None if s is None else s.cpu(), kv[1:]) for c, s in ((kc, ks), (vc, vs)))
+            mag = np.abs(v64)
+        ref = plain.attend(q.cpu(), k64, v64, mag, bt, ctx, ql, 1, float(np.float32(d ** -0.5)), nblocks)
+        # f16 weights, but bf16 ones for a bf16 cache; 33 rows and more of an fp8 cache have their query
+        # in E4M3 terms, good to about 2^-9 of the logits' magnitudes: the prompt there is not compared
+        if not (kv == "8token" and sq == 56):
+            plain64.check_attention(out, lse, *ref, t, 2.0 ** -8 if kv == "16" and dtype == "bf16" else 2.0 ** -11)
+
+
+# ---- refusals (no GPU) ---------------------------------------------------------------------------
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(pa.LIB_PATH):
+        from paged_kv_cache_work_gb300.build import build
+        build()
+    return pa.load()
+
+
+FAKE = 1 << 20  # never dereferenced: every call below is rejected on the host
+
+
+def rotary(**kw):
+    r = pa.PaRotary(q_weight=FAKE, k_weight=FAKE, eps=1e-6, rotary_dim=128, interleaved=0, cos_sin=FAKE, table_rows=100,
+                    positions=None, num_axes=1)
+    r.axis_pairs[0] = 64
+    for n, v in kw.items():
+        if n == "axis_pairs":
+            r.axis_pairs[:] = v
+        else:
+            setattr(r, n, v)
+    return r
+
+
+def call(lib, cfg, r, **kw):
+    a = dict(q=FAKE, k=FAKE + 65536, v=FAKE, bt=FAKE, ctx=FAKE, ql=FAKE, qo=FAKE + 4096, ko=None, kc=FAKE, vc=FAKE,
+             ks=None, vs=None, flags=None, stream=None)
+    a.update(kw)
+    return lib.pa_append_rotated(ctypes.byref(cfg) if cfg else None, ctypes.byref(r) if r else None, *a.values())
+
+
+def base(kv="16", **kw):
+    return config(2, 1, 8, 2, 128, 16, 8, 32, kv=kv, **kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(rotary_dim=-16), dict(interleaved=2),
+    dict(cos_sin=None), dict(table_rows=0), dict(num_axes=0), dict(num_axes=4), dict(axis_pairs=(63, 0, 0)),
+    dict(num_axes=2, axis_pairs=(65, -1, 0)), dict(q_stride=-8), dict(q_stride=8), dict(k_stride=257), dict(v_stride=128),
+    dict(q_weight=FAKE + 2), dict(cos_sin=FAKE + 4), dict(positions=FAKE + 2)])
+def test_bad_rotary(lib, kw):
+    assert call(lib, base(), rotary(**kw)) == pa.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=24, axis_pairs=(12, 0, 0)), dict(rotary_dim=144, axis_pairs=(72, 0, 0))])
+def test_unsupported_rotary(lib, kw):
+    assert call(lib, base(), rotary(**kw)) == pa.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(k=None), dict(v=None), dict(bt=None), dict(ctx=None), dict(ql=None), dict(qo=None),
+    dict(kc=None), dict(vc=None), dict(kc=None, vc=None), dict(q=FAKE + 8), dict(qo=FAKE + 2), dict(vc=FAKE + 4),
+    dict(flags=FAKE + 1), dict(ko=FAKE + 8)])
+def test_bad_pointers(lib, kw):
+    assert call(lib, base(), rotary(), **kw) == pa.ERR_INVALID_ARG
+
+
+def test_other_refusals(lib):
+    r = rotary()
+    assert call(lib, None, r) == pa.ERR_INVALID_ARG and call(lib, base(), None) == pa.ERR_INVALID_ARG
+    for kv in ("8token", "8tensor", "4"):
+        assert call(lib, base(kv), r) == pa.ERR_INVALID_ARG  # no scales
+        assert call(lib, base(kv), r, ks=FAKE, vs=FAKE + 2) == pa.ERR_INVALID_ARG
+    assert call(lib, base("4"), r, ks=FAKE, vs=FAKE + 8) == pa.ERR_INVALID_ARG
+    c = base("8token")
+    c.kv_scale_mode = pa.SCALE_PER_BLOCK
+    assert call(lib, c, r, ks=FAKE, vs=FAKE) == pa.ERR_UNSUPPORTED
+    for n, v, want in (("head_dim", 96, pa.ERR_UNSUPPORTED), ("block_size", 24, pa.ERR_UNSUPPORTED), ("batch", 0, pa.ERR_INVALID_ARG),
+                       ("num_q_heads", 7, pa.ERR_UNSUPPORTED), ("kv_dtype", pa.FP16, pa.ERR_UNSUPPORTED),
+                       ("q_dtype", pa.INT4, pa.ERR_UNSUPPORTED), ("kv_scale_mode", 9, pa.ERR_INVALID_ARG)):
+        c = base()
+        setattr(c, n, v)
+        assert call(lib, c, r) == want, n
+    # in place only where the rows lie dense
+    assert call(lib, base(), rotary(q_stride=2048), qo=FAKE) == pa.ERR_INVALID_ARG
+    assert call(lib, base(), rotary(k_stride=2048), ko=FAKE + 65536) == pa.ERR_INVALID_ARG
+
+
+def test_binding_refuses_rows_that_do_not_fit():
+    cfg = base()
+    x = torch.zeros(2, 1, 8, 128, dtype=torch.bfloat16)
+    for bad in (x.transpose(2, 3), x[:, :, :4], x.float(), x[..., ::2]):
+        with pytest.raises(pa.PaError):
+            pa.append_rotated(cfg, bad, x, x, x, x, x, x, None, None, k_out=x)
