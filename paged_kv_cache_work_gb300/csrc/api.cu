@@ -123,35 +123,38 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Descriptor of a cache [num_blocks, block_size, Hkv, D] seen as a 4-D tensor (D innermost)
 // with a box of one head's rows of one page.  CUDA-core kernel: {D, 1, rows, 1}, no swizzle.
 // Tensor-core kernels: {128 bytes of D, 1, rows, 1} with the 128-byte swizzle, one box per
-// 128-byte column slab (64-byte rows: the whole row, with the 64-byte swizzle).
+// 128-byte column slab (64-byte rows: the whole row, with the 64-byte swizzle; 32-byte rows: as it
+// lies).
 bool kv_tensor_map(CUtensorMap* m, const void* base, const pa_config& c, int box_rows, bool slabs) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
-  const int bpe = c.kv_dtype == PA_FP8_E4M3 ? 1 : 2;
-  CUtensorMapDataType dt = c.kv_dtype == PA_FP8_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                           : c.kv_dtype == PA_FP16   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_kv_heads,
-                        (cuuint64_t)c.block_size, (cuuint64_t)c.num_blocks};
-  cuuint64_t strides[3] = {(cuuint64_t)c.head_dim * bpe,
-                           (cuuint64_t)c.num_kv_heads * c.head_dim * bpe,
-                           (cuuint64_t)c.block_size * c.num_kv_heads * c.head_dim * bpe};
-  const bool narrow = c.head_dim * bpe < 128;  // 64-byte rows: one slab of them
-  const cuuint32_t inner = slabs && !narrow ? (cuuint32_t)(128 / bpe) : (cuuint32_t)c.head_dim;
+  const int bpe = c.kv_dtype == PA_FP8_E4M3 || c.kv_dtype == PA_INT4 ? 1 : 2;
+  CUtensorMapDataType dt = bpe == 1                ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                           : c.kv_dtype == PA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int width = c.kv_dtype == PA_INT4 ? c.head_dim / 2 : c.head_dim;  // elements of a row
+  cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)c.num_kv_heads, (cuuint64_t)c.block_size,
+                        (cuuint64_t)c.num_blocks};
+  cuuint64_t strides[3] = {(cuuint64_t)width * bpe, (cuuint64_t)c.num_kv_heads * width * bpe,
+                           (cuuint64_t)c.block_size * c.num_kv_heads * width * bpe};
+  const int row = width * bpe;
+  const bool narrow = row < 128;  // 64- or 32-byte rows: one slab of them
+  const cuuint32_t inner = slabs && !narrow ? (cuuint32_t)(128 / bpe) : (cuuint32_t)width;
   cuuint32_t box[4] = {inner, 1, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   // L2 fetches no more than a head's row at a time: past it lies the next head's, which another CTA
   // reads at another time (128-byte rows, 8 kv heads, 150 MB of cache: 172 MB read and 39.9 us a
   // step with 256 bytes, 36.9 us with 128; one kv head: 43.4 us either way)
-  const auto promotion = c.head_dim * bpe >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                         : c.head_dim * bpe >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  const auto promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                         : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                         : row >= 64  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                      : CU_TENSOR_MAP_L2_PROMOTION_NONE;
   std::memset(m, 0, sizeof(*m));
   CUresult r = enc(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   !slabs   ? CU_TENSOR_MAP_SWIZZLE_NONE
-                   : narrow ? CU_TENSOR_MAP_SWIZZLE_64B
-                            : CU_TENSOR_MAP_SWIZZLE_128B,
+                   !slabs || row < 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                   : narrow           ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B,
                    promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -205,14 +208,12 @@ pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, co
   }
   if ((st = check_ws(ws, ws_bytes, L)) != PA_OK) return st;
 
-  const int box_rows = v.path == 3 ? 16 : cfg->block_size < v.tt ? cfg->block_size : v.tt;
-  CUtensorMap kmap{}, vmap{};
-  if (v.path == 4) {
-    // (the 4-bit kernel reads the caches by address)
-  } else if (!kv_tensor_map(&kmap, k_cache, *cfg, box_rows, v.path >= 1) ||
-             !kv_tensor_map(&vmap, v_cache, *cfg, box_rows, v.path >= 1)) {
+  const int tile_rows = v.path == 4 ? int4_tile_tokens(cfg->head_dim, v.mp) : v.tt;
+  const int box_rows = v.path == 3 ? 16 : cfg->block_size < tile_rows ? cfg->block_size : tile_rows;
+  CUtensorMap kmap, vmap;
+  if (!kv_tensor_map(&kmap, k_cache, *cfg, box_rows, v.path >= 1) ||
+      !kv_tensor_map(&vmap, v_cache, *cfg, box_rows, v.path >= 1))
     return PA_ERR_CUDA;
-  }
 
   DecodeArgs a;
   a.p = problem_args(*cfg, block_tables, context_lens, q_lens);

@@ -1,6 +1,9 @@
 // Persistent split-KV paged decode over a 4-bit cache: the planner's work list, each item's 16-token
 // chunks going to the warps of a CTA in turn, which attend on their own (int4_attention.cuh) and
 // merge at the item's end, as in the streaming decode over fp8 pages.
+//
+// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V), and bulk copies of
+// their pairs, into a ring of the warp's own, with no barrier between warps while data streams.
 #pragma once
 
 #include "int4_attention.cuh"
@@ -11,24 +14,46 @@ template <class T>
 struct DecodeInt4Smem {
   static constexpr int NW = 4;
   static constexpr int NTHREADS = NW * 32;
+  static constexpr int TK = int4_tile_tokens(T::D, T::ROWS);  // tokens of a warp's tile
+  static constexpr int SUB = TK / 16;                         // its chunks
+  static constexpr int NST = 3;           // stages of a warp's ring
+  static constexpr int TILE = TK * T::ROW;           // bytes of a K (or V) tile
+  static constexpr int PAIRS = 2 * TILE;             // offset of the K rows' pairs, then the V rows'
+  static constexpr int STAGE = round_up(2 * TILE + 2 * TK * 4, 8 * T::ROW);  // (a swizzle's period)
+  static constexpr int RING = NW * NST * STAGE;
   static constexpr int STATES = NW * T::O_SLOT;
-  static constexpr int OFF_ML = round_up(STATES, 128);
-  static constexpr int OFF_PEND = OFF_ML + cmax(NW * T::ROWS * 8, 2 * T::ROWS * 4);
-  static constexpr int BYTES = OFF_PEND + 16;
+  static constexpr int OFF_ML = round_up(cmax(RING, STATES), 128);
+  static constexpr int OFF_BAR = OFF_ML + cmax(NW * T::ROWS * 8, 2 * T::ROWS * 4);
+  static constexpr int OFF_PEND = OFF_BAR + NW * NST * 8;
+  static constexpr int BYTES = OFF_PEND + 16 + 1024;  // (alignment)
   static constexpr int CTAS_PER_SM = T::D == 256 ? 2 : T::NT == 1 ? 4 : 3;
-  static_assert(BYTES <= 227 * 1024, "shared memory");
+  static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
 template <class T>
 __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>::CTAS_PER_SM)
-    decode_int4_kernel(const KernelParams p, const Int4View cache) {
+    decode_int4_kernel(const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const KernelParams p,
+                       const Int4View cache) {
   using M = DecodeInt4Smem<T>;
-  constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, NT = T::NT;
-  extern __shared__ __align__(16) char smem[];
+  constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, NT = T::NT, SUB = M::SUB, NST = M::NST;
+  static_assert(NST == 3, "two tiles in flight");
+  extern __shared__ char smem_raw[];
+  char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, qi = lane & 3;
+  char* const ring = smem + warp * NST * M::STAGE;
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + M::OFF_BAR) + warp * NST;
   int* const pend = reinterpret_cast<int*>(smem + M::OFF_PEND);    // [4]
   float* const obuf = reinterpret_cast<float*>(smem);              // [NW][ROWS][OSTR]
   float2* const ml = reinterpret_cast<float2*>(smem + M::OFF_ML);  // [NW][ROWS] (max, sum)
+  if (lane == 0) {  // (a warp's barriers are its own)
+    for (int s = 0; s < NST; ++s) mbar_init(&bar[s], 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  __syncwarp();
+  const int box = min(p.bs, M::TK);  // tokens of a box: a page's, or a tile's
   const int4 first = first_item_of(p, blockIdx.x, gridDim.x, lane);
   int it = 0, items = 1, list = 0;  // this CTA's items begin at p.items[list]
   int4 item_next = first;
@@ -42,6 +67,9 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     if (f.x != first.x || f.y != first.y || f.z != first.z || f.w != first.w) bad |= PA_FLAG_STALE_PLAN;
   };
   int2 pend_even = make_int2(-1, 0), pend_odd = make_int2(-1, 0);  // held by thread 0
+  int st = 0;  // stage of the warp's next tile to read, and its barrier's phase
+  uint32_t phase = 0;
+  bool failed = false;  // copies that never came: this warp reads no more
   for (; it < items; ++it) {
     const int4 item = item_next;
     if (it > 0 && it + 1 < items) item_next = p.items[list + it + 1];
@@ -55,7 +83,51 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     }
     const int b = u / (p.Hkv * p.RB), g = (u / p.RB) % p.Hkv, rb = u % p.RB;
     const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
-    const int chunks = (t1 - t0 + 15) >> 4;
+    const int tiles = (t1 - t0 + M::TK - 1) / M::TK;
+    const int my = failed ? 0 : (tiles - warp + NW - 1) / NW;  // this warp's tiles
+
+    // lane l looks up chunk base + l of the warp's chunks (SUB a tile); `held` says which of these
+    // are in the pool, `held_before` which of the 32 before them
+    int blk = -1, base = -32;
+    uint32_t held = 0, held_before = 0;
+    auto look_up = [&](int x0) {
+      base = x0;
+      const int x = x0 + lane, tok = t0 + ((warp + NW * (x / SUB)) * SUB + x % SUB) * 16;
+      blk = -1;
+      if (x / SUB < my && tok < t1) {
+        blk = __ldg(p.bt + (size_t)b * p.maxb + (tok >> p.bs_shift));
+        if (blk < 0 || blk >= p.nblocks) {
+          bad |= PA_FLAG_BAD_BLOCK_ID;
+          blk = -1;
+        }
+      }
+      held_before = held;
+      held = __ballot_sync(kFull, blk >= 0);
+    };
+    // the boxes of tile j into stage s: a lane a box
+    auto issue = [&](int j, int s) {
+      if (j >= my) return;
+      if (SUB * j >= base + 32) look_up(SUB * j);
+      const int lane0 = SUB * j - base, c = lane - lane0;
+      const bool copies = c >= 0 && c < SUB && blk >= 0 && (16 * c & (box - 1)) == 0;
+      const uint32_t boxes = __popc(__ballot_sync(kFull, copies));
+      if (lane == 0) mbar_arrive_expect_tx(&bar[s], boxes * 2u * (uint32_t)(box * (T::ROW + 4)));
+      __syncwarp();
+      if (copies) {
+        const int tok = t0 + ((warp + NW * j) * SUB + c) * 16, slot_in = tok & (p.bs - 1);
+        char* const dst = ring + s * M::STAGE + c * 16 * T::ROW;
+        tma_load_4d(dst, &kmap, &bar[s], 0, g, slot_in, blk);
+        tma_load_4d(dst + M::TILE, &vmap, &bar[s], 0, g, slot_in, blk);
+        const size_t at = (((size_t)blk * p.Hkv + g) << p.bs_shift) + slot_in;
+        char* const pairs = ring + s * M::STAGE + M::PAIRS + c * 16 * 4;
+        bulk_load_1d(pairs, cache.k_pair + at, box * 4, &bar[s]);
+        bulk_load_1d(pairs + M::TK * 4, cache.v_pair + at, box * 4, &bar[s]);
+      }
+    };
+    if (my > 0) look_up(0);
+    __syncwarp();
+    issue(0, st);
+    issue(1, st == 2 ? 0 : st + 1);
 
     T att;
     att.clear();
@@ -82,49 +154,51 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     }
     least = __reduce_min_sync(kFull, least);
 
-    for (int c = warp; c < chunks; c += NW) {
-      const int tok = t0 + 16 * c, rows = min(t1 - tok, 16);
-      const int blk = __ldg(p.bt + (size_t)b * p.maxb + (tok >> p.bs_shift));
-      if (blk < 0 || blk >= p.nblocks) {
-        bad |= PA_FLAG_BAD_BLOCK_ID;
-        continue;
+    for (int j = 0; j < my; ++j) {
+      if (!stream_wait(&bar[st], phase)) {
+        bad |= PA_FLAG_WAIT_TIMEOUT;
+        if (j + 1 < my) mbar_wait_drain(&bar[st == 2 ? 0 : st + 1], st == 2 ? phase ^ 1 : phase);
+        failed = true;
+        break;
       }
-      const int at = tok & (p.bs - 1);
-      const size_t row0 = (((size_t)blk << p.bs_shift) + at) * p.Hkv + g;
-      const size_t pair0 = (((size_t)blk * p.Hkv + g) << p.bs_shift) + at;
-      const size_t stride = (size_t)p.Hkv * T::ROW;
-      float2 ks[1][2], vs[1][2];
+      __syncwarp();
+      issue(j + 2, st == 0 ? 2 : st - 1);
+      const int x = SUB * j - base;  // (tile j + 2's look-up may have come in between)
+      const uint32_t here = (x >= 0 ? held >> x : held_before >> (x + 32)) & ((1u << SUB) - 1);
+      const int tok = t0 + (warp + NW * j) * M::TK;
+      const bool all = here == (1u << SUB) - 1 && tok + M::TK <= min(t1, least);
+      const char* const stage = ring + st * M::STAGE;
+      const uint32_t* const kp = reinterpret_cast<const uint32_t*>(stage + M::PAIRS);
+      float2 ks[SUB][2], vs[SUB][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool ok = quad + 8 * h < rows;  // (what lies behind the last token may hold anything)
-        ks[0][h] = ok ? pair_values<T::QK>(__ldg(cache.k_pair + pair0 + quad + 8 * h)) : make_float2(0.f, 0.f);
-        vs[0][h] = ok ? pair_values<T::QK>(__ldg(cache.v_pair + pair0 + quad + 8 * h)) : make_float2(0.f, 0.f);
-      }
-      auto kw = [&](int, int h, uint32_t (&w)[T::KW]) {
-        const char* src = cache.k + row0 * T::ROW + (quad + 8 * h) * stride + qi * T::KW * 4;
+      for (int c = 0; c < SUB; ++c)
 #pragma unroll
-        for (int i = 0; i < T::KW; i += 2) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 4 * i));
-          w[i] = v.x;
-          w[i + 1] = v.y;
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * c + 8 * h + quad;
+          ks[c][h] = pair_values<T::QK>(kp[r]);
+          vs[c][h] = pair_values<T::QK>(kp[M::TK + r]);
+          if (!all) {  // (what lies behind the last token, or was not copied, may hold anything)
+            const bool ok = (here >> c & 1) && tok + r < t1;
+            ks[c][h] = ok ? ks[c][h] : make_float2(0.f, 0.f);
+            vs[c][h] = ok ? vs[c][h] : make_float2(0.f, 0.f);
+          }
         }
-      };
-      auto vw = [&](int, int h, int e, uint32_t (&w)[T::VW]) {
-        const int r = 2 * qi + 8 * h + (T::first_token(qi) ^ e);
-        const char* src = cache.v + row0 * T::ROW + r * stride + quad * T::VW * 4;
-#pragma unroll
-        for (int i = 0; i < T::VW; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src + 4 * i));
-      };
-      att.template tile<1>(
-          kw, vw, ks, vs, rows == 16 && tok + 16 <= least,
-          [&](int, int h, int t) {
-            const int x = tok + quad + 8 * h;
-            return make_uint2(x < min(lim[t].x, tok + rows), x < min(lim[t].y, tok + rows));
+      const uint32_t kt = smem_addr(stage);
+      att.template tile<SUB>(
+          kt, kt + M::TILE, ks, vs, all,
+          [&](int c, int h, int t) {
+            const int x = tok + 16 * c + 8 * h + quad, end = (here >> c & 1) ? t1 : 0;
+            return make_uint2(x < min(lim[t].x, end), x < min(lim[t].y, end));
           },
           lane);
+      if (++st == NST) {
+        st = 0;
+        phase ^= 1;
+      }
     }
 
     // ---- merge the warps, and write the rows (whole, or a piece's partial)
+    __syncthreads();  // every warp is done with its stages
     att.stage_state(obuf, ml, warp, lane);
     if (it == 0) {
       wait_planner();
@@ -155,6 +229,8 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     }
     const bool in_dec = slot >= 0 && __ldg(&p.unit_info[u].y) <= p.ns_dec;
     if (in_dec) __threadfence();
+    // the states lie where the next item's copies go
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     if (in_dec && tid == 0) publish_piece(p, u, slot, &pend_even, &pend_odd);
   }
@@ -166,12 +242,13 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     pend[3] = pend_odd.y;
   }
   __syncthreads();
-  finish_pending<D, ROWS, T::QK, NW>(p, pend, obuf, M::STATES / 4, reinterpret_cast<float*>(ml));
+  finish_pending<D, ROWS, T::QK, NW>(p, pend, obuf, M::RING / 4, reinterpret_cast<float*>(ml));
   zero_empty_units<D, ROWS, T::QK, M::NTHREADS>(p);
 }
 
 template <int D, int NT, int QK>
-cudaError_t launch_int4_instance(const KernelParams& prm, const Int4View& cache, int grid,
+cudaError_t launch_int4_instance(const KernelParams& prm, const Int4View& cache,
+                                 const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
                                  cudaStream_t s) {
   using T = Int4Attention<D, NT, QK>;
   using M = DecodeInt4Smem<T>;
@@ -189,18 +266,18 @@ cudaError_t launch_int4_instance(const KernelParams& prm, const Int4View& cache,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, prm, cache);
+  return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, prm, cache);
 }
 
 // Both row tiles of a head dim.
 template <int D>
-cudaError_t launch_int4_dim(const KernelParams& prm, const Int4View& cache, int grid, int mp, int qk,
-                            cudaStream_t s) {
+cudaError_t launch_int4_dim(const KernelParams& prm, const Int4View& cache, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, int grid, int mp, int qk, cudaStream_t s) {
   if (mp == 8)
-    return qk == Q_BF16 ? launch_int4_instance<D, 1, Q_BF16>(prm, cache, grid, s)
-                        : launch_int4_instance<D, 1, Q_FP16>(prm, cache, grid, s);
-  return qk == Q_BF16 ? launch_int4_instance<D, 2, Q_BF16>(prm, cache, grid, s)
-                      : launch_int4_instance<D, 2, Q_FP16>(prm, cache, grid, s);
+    return qk == Q_BF16 ? launch_int4_instance<D, 1, Q_BF16>(prm, cache, kmap, vmap, grid, s)
+                        : launch_int4_instance<D, 1, Q_FP16>(prm, cache, kmap, vmap, grid, s);
+  return qk == Q_BF16 ? launch_int4_instance<D, 2, Q_BF16>(prm, cache, kmap, vmap, grid, s)
+                      : launch_int4_instance<D, 2, Q_FP16>(prm, cache, kmap, vmap, grid, s);
 }
 
 }  // namespace pa

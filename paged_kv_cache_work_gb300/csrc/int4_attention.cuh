@@ -53,10 +53,44 @@ struct Int4Attention {
   static constexpr int MB = D / 16;        // 16-channel blocks of the output
   static constexpr int OSTR = D + 4;       // floats between rows of a staged accumulator
   static constexpr int O_SLOT = ROWS * OSTR * 4;
-  // which of the tokens 2 qi, 2 qi + 1 a lane reads first (page rows in shared memory then lie in
-  // distinct banks)
+
+  // Rows of a tile in shared memory: as the TMA boxes bring them, 16-byte pieces swizzled over rows of
+  // 64 bytes (by bits 1 and 2 of the row) and 128 (by its low three bits).  Which of the tokens
+  // 2 qi, 2 qi + 1 a lane reads first is chosen so that a phase's lanes lie in distinct banks.
   static __device__ __forceinline__ int first_token(int qi) {
     return D == 128 ? qi & 1 : D == 64 ? qi >> 1 : 0;
+  }
+  // The lane's words of the K row of token quad + 8 h of chunk c.
+  static __device__ __forceinline__ void k_words(uint32_t tile, int c, int h, int lane, uint32_t (&w)[KW]) {
+    const int quad = lane >> 2, qi = lane & 3;
+    const uint32_t row = tile + (16 * c + 8 * h + quad) * ROW;
+    if constexpr (D == 64) {
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(row + 8 * qi));
+    } else {
+#pragma unroll
+      for (int j = 0; j < KW / 4; ++j) {
+        const int piece = D == 128 ? qi ^ (quad >> 1) : (2 * qi + j) ^ quad;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3])
+                     : "r"(row + (piece << 4)));
+      }
+    }
+  }
+  // Its words of the V row of one of the tokens 2 qi, 2 qi + 1 (+ 8 h), the first one for e = 0.
+  static __device__ __forceinline__ void v_words(uint32_t tile, int c, int h, int e, int lane,
+                                                 uint32_t (&w)[VW]) {
+    const int quad = lane >> 2, qi = lane & 3, r = 2 * qi + (first_token(qi) ^ e);
+    const uint32_t row = tile + (16 * c + 8 * h + r) * ROW;
+    if constexpr (D == 64)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(row + 4 * quad));
+    else if constexpr (D == 128)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(w[0]), "=r"(w[1])
+                   : "r"(row + (((quad >> 1) ^ qi) << 4) + 8 * (quad & 1)));
+    else
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(row + ((quad ^ r) << 4)));
   }
 
   uint32_t qb[KSTEPS][NT][2];
@@ -170,13 +204,12 @@ struct Int4Attention {
     }
   }
 
-  // SUB chunks of 16 tokens.  kw(s, h): the lane's words of the K row of token quad + 8 h of chunk s;
-  // vw(s, h, e): its words of the V row of token 2 qi + 8 h + (first_token or the other, e = 0, 1);
-  // ks, vs [s][h]: (step, low) of token quad + 8 h, zero where no row may see the token;
-  // sees(s, h, t): which of the rows 8 t + 2 qi, + 1 see token quad + 8 h of chunk s; all: every row
+  // SUB chunks of 16 tokens, their K rows at shared address kt and V rows at vt.
+  // ks, vs [c][h]: (step, low) of token quad + 8 h, zero where no row may see the token;
+  // sees(c, h, t): which of the rows 8 t + 2 qi, + 1 see token quad + 8 h of chunk c; all: every row
   // sees every token.
-  template <int SUB, class FK, class FV, class FS>
-  __device__ __forceinline__ void tile(FK kw, FV vw, const float2 (&ks)[SUB][2],
+  template <int SUB, class FS>
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const float2 (&ks)[SUB][2],
                                        const float2 (&vs)[SUB][2], bool all, FS sees, int lane) {
     const int qi = lane & 3;
     float2 x[SUB][2][NT];  // logits of token quad + 8 h
@@ -186,8 +219,8 @@ struct Int4Attention {
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
       uint32_t w[2][KW];
-      kw(c, 0, w[0]);
-      kw(c, 1, w[1]);
+      k_words(kt, c, 0, lane, w[0]);
+      k_words(kt, c, 1, lane, w[1]);
 #pragma unroll
       for (int i = 0; i < KW; ++i)
 #pragma unroll
@@ -283,8 +316,8 @@ struct Int4Attention {
         uint32_t w[2][2][VW];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          vw(c, h, 0, w[h][0]);
-          vw(c, h, 1, w[h][1]);
+          v_words(vt, c, h, 0, lane, w[h][0]);
+          v_words(vt, c, h, 1, lane, w[h][1]);
         }
 #pragma unroll
         for (int i = 0; i < VW; ++i)

@@ -131,7 +131,8 @@ constexpr int stream_max_rows(int head_dim) {
 // The 4-bit kernel: query rows of a tile, the tokens that a CTA's warps take in a round, and the cost
 // of an item in such rounds.
 constexpr int int4_tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
-constexpr int kInt4RoundTokens = 64;
+constexpr int int4_tile_tokens(int head_dim, int mp) { return head_dim == 256 && mp == 16 ? 16 : 32; }
+constexpr int kInt4RoundTokens = 128;
 constexpr int kInt4ItemCostRounds = 5;
 
 // Query rows per kv head above which a 128-dim head runs on the tcgen05 kernel.

@@ -32,9 +32,12 @@ cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, co
 
 cudaError_t launch_stream(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int, int,
                           cudaStream_t);
-cudaError_t launch_int4_d64(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
-cudaError_t launch_int4_d128(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
-cudaError_t launch_int4_d256(const KernelParams&, const Int4View&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d64(const KernelParams&, const Int4View&, const CUtensorMap&,
+                            const CUtensorMap&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d128(const KernelParams&, const Int4View&, const CUtensorMap&,
+                            const CUtensorMap&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d256(const KernelParams&, const Int4View&, const CUtensorMap&,
+                            const CUtensorMap&, int, int, int, cudaStream_t);
 int int4_ctas_per_sm_d64(int);
 int int4_ctas_per_sm_d128(int);
 int int4_ctas_per_sm_d256(int);
@@ -119,9 +122,9 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CU
                          static_cast<const uint32_t*>(a.k_scale),
                          static_cast<const uint32_t*>(a.v_scale)};
     switch (a.p.head_dim) {
-      case 64: return launch_int4_d64(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
-      case 128: return launch_int4_d128(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
-      case 256: return launch_int4_d256(prm, cache, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 64: return launch_int4_d64(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 128: return launch_int4_d128(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 256: return launch_int4_d256(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
       default: return cudaErrorNotSupported;
     }
   }
