@@ -41,14 +41,6 @@ struct KernelParams {
   int batch, tt, tt_shift, item_cost;
 };
 
-// Where a 4-bit cache's rows and their (step, low) pairs lie.
-struct Int4View {
-  const char* k;
-  const char* v;
-  const uint32_t* k_pair;  // [num_blocks, Hkv, bs]
-  const uint32_t* v_pair;
-};
-
 // The first work item of CTA c of C, derived from the lengths with the planner's own rules
 // and integer arithmetic (the concatenated token space of plan.cu: each unit its tile-padded
 // length plus the item cost, cut into C equal tile-aligned pieces), so that a CTA can start

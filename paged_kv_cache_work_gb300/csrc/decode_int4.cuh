@@ -2,7 +2,7 @@
 // chunks going to the warps of a CTA in turn, which attend on their own (int4_attention.cuh) and
 // merge at the item's end, as in the streaming decode over fp8 pages.
 //
-// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V), and bulk copies of
+// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V) and of
 // their pairs, into a ring of the warp's own, with no barrier between warps while data streams.
 #pragma once
 
@@ -16,25 +16,36 @@ struct DecodeInt4Smem {
   static constexpr int NTHREADS = NW * 32;
   static constexpr int TK = int4_tile_tokens(T::D, T::ROWS);  // tokens of a warp's tile
   static constexpr int SUB = TK / 16;                         // its chunks
-  static constexpr int NST = 3;           // stages of a warp's ring
-  static constexpr int TILE = TK * T::ROW;           // bytes of a K (or V) tile
-  static constexpr int PAIRS = 2 * TILE;             // offset of the K rows' pairs, then the V rows'
-  static constexpr int STAGE = round_up(2 * TILE + 2 * TK * 4, 8 * T::ROW);  // (a swizzle's period)
+  static constexpr int NST = 3;                               // stages of a warp's ring
+  static constexpr int TILE = TK * T::ROW;                    // bytes of a K (or V) tile
+  static constexpr int STAGE = 2 * TILE;                      // (a multiple of its swizzle's period)
+  // A stage's pairs, K rows' before V rows': a box's begin on 128 bytes, as a tensor copy's
+  // destination has to, so those of 16-token boxes lie 128 bytes apart.
+  static constexpr int VPAIRS = SUB * 128;
+  static constexpr int PAIRS = 2 * VPAIRS;
   static constexpr int RING = NW * NST * STAGE;
   static constexpr int STATES = NW * T::O_SLOT;
   static constexpr int OFF_ML = round_up(cmax(RING, STATES), 128);
-  static constexpr int OFF_BAR = OFF_ML + cmax(NW * T::ROWS * 8, 2 * T::ROWS * 4);
+  static constexpr int OFF_QUERY = OFF_ML + round_up(cmax(NW * T::ROWS * 8, 2 * T::ROWS * 4), 128);
+  static constexpr int OFF_FACTORS = OFF_QUERY + T::QUERY;
+  static constexpr int OFF_PAIRS = OFF_FACTORS + NW * TK * 16;
+  static constexpr int OFF_BAR = OFF_PAIRS + NW * NST * PAIRS;
   static constexpr int OFF_PEND = OFF_BAR + NW * NST * 8;
   static constexpr int BYTES = OFF_PEND + 16 + 1024;  // (alignment)
-  static constexpr int CTAS_PER_SM = T::D == 256 ? 2 : T::NT == 1 ? 4 : 3;
+  static constexpr int CT1 = 3, CT2 = 2;
+  static constexpr int CTAS_PER_SM = T::D == 256 ? 2 : T::NT == 1 ? CT1 : CT2;
+  static_assert(OFF_PAIRS % 128 == 0 && PAIRS % 128 == 0 && 16 * T::ROW % 128 == 0 &&
+                    STAGE % (8 * T::ROW) == 0 && STAGE % 128 == 0,
+                "a tensor copy's destination");
   static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
 template <class T>
 __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>::CTAS_PER_SM)
     decode_int4_kernel(const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap, const KernelParams p,
-                       const Int4View cache) {
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ CUtensorMap kpmap,
+                       const __grid_constant__ CUtensorMap vpmap, const KernelParams p) {
   using M = DecodeInt4Smem<T>;
   constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, NT = T::NT, SUB = M::SUB, NST = M::NST;
   static_assert(NST == 3, "two tiles in flight");
@@ -42,18 +53,25 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
   char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, qi = lane & 3;
   char* const ring = smem + warp * NST * M::STAGE;
+  char* const pairs = smem + M::OFF_PAIRS + warp * NST * M::PAIRS;
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + M::OFF_BAR) + warp * NST;
   int* const pend = reinterpret_cast<int*>(smem + M::OFF_PEND);    // [4]
   float* const obuf = reinterpret_cast<float*>(smem);              // [NW][ROWS][OSTR]
+  uint4* const query = reinterpret_cast<uint4*>(smem + M::OFF_QUERY);
+  float4* const factors = reinterpret_cast<float4*>(smem + M::OFF_FACTORS) + warp * M::TK;
   float2* const ml = reinterpret_cast<float2*>(smem + M::OFF_ML);  // [NW][ROWS] (max, sum)
   if (lane == 0) {  // (a warp's barriers are its own)
-    for (int s = 0; s < NST; ++s) mbar_init(&bar[s], 1);
+    for (int s = 0; s < NST; ++s) mbar_init(&bar[s], SUB);
     fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&kpmap);
+    tma_prefetch_desc(&vpmap);
   }
   __syncwarp();
   const int box = min(p.bs, M::TK);  // tokens of a box: a page's, or a tile's
+  const int t = lane % M::TK, pair_at = 4 * t + (box < M::TK && t >= 16 ? 64 : 0);  // a lane's token
+  const uint32_t box_bytes = 2u * (uint32_t)(box * (T::ROW + 4));
   const int4 first = first_item_of(p, blockIdx.x, gridDim.x, lane);
   int it = 0, items = 1, list = 0;  // this CTA's items begin at p.items[list]
   int4 item_next = first;
@@ -86,8 +104,8 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     const int tiles = (t1 - t0 + M::TK - 1) / M::TK;
     const int my = failed ? 0 : (tiles - warp + NW - 1) / NW;  // this warp's tiles
 
-    // lane l looks up chunk base + l of the warp's chunks (SUB a tile); `held` says which of these
-    // are in the pool, `held_before` which of the 32 before them
+    // lane l looks up the block of chunk base + l of the warp's chunks, SUB a tile (-1: none, or outside
+    // the pool).  `held` says which of these are in the pool, `held_before` which of the 32 before them.
     int blk = -1, base = -32;
     uint32_t held = 0, held_before = 0;
     auto look_up = [&](int x0) {
@@ -104,25 +122,27 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
       held_before = held;
       held = __ballot_sync(kFull, blk >= 0);
     };
-    // the boxes of tile j into stage s: a lane a box
+    // The boxes of tile j into stage s: a lane a chunk, which arrives with what it copies (where a box
+    // holds the tile, the first chunk's lane copies it).
     auto issue = [&](int j, int s) {
       if (j >= my) return;
       if (SUB * j >= base + 32) look_up(SUB * j);
-      const int lane0 = SUB * j - base, c = lane - lane0;
-      const bool copies = c >= 0 && c < SUB && blk >= 0 && (16 * c & (box - 1)) == 0;
-      const uint32_t boxes = __popc(__ballot_sync(kFull, copies));
-      if (lane == 0) mbar_arrive_expect_tx(&bar[s], boxes * 2u * (uint32_t)(box * (T::ROW + 4)));
-      __syncwarp();
-      if (copies) {
-        const int tok = t0 + ((warp + NW * j) * SUB + c) * 16, slot_in = tok & (p.bs - 1);
-        char* const dst = ring + s * M::STAGE + c * 16 * T::ROW;
-        tma_load_4d(dst, &kmap, &bar[s], 0, g, slot_in, blk);
-        tma_load_4d(dst + M::TILE, &vmap, &bar[s], 0, g, slot_in, blk);
-        const size_t at = (((size_t)blk * p.Hkv + g) << p.bs_shift) + slot_in;
-        char* const pairs = ring + s * M::STAGE + M::PAIRS + c * 16 * 4;
-        bulk_load_1d(pairs, cache.k_pair + at, box * 4, &bar[s]);
-        bulk_load_1d(pairs + M::TK * 4, cache.v_pair + at, box * 4, &bar[s]);
+      const int c = lane - (SUB * j - base);
+      if (c >= 0 && c < SUB) {
+        if (blk >= 0 && (16 * c & (box - 1)) == 0) {
+          mbar_arrive_expect_tx(&bar[s], box_bytes);
+          const int slot_in = (t0 + (warp + NW * j) * M::TK + 16 * c) & (p.bs - 1);
+          char* const dst = ring + s * M::STAGE + c * 16 * T::ROW;
+          tma_load_4d(dst, &kmap, &bar[s], 0, g, slot_in, blk);
+          tma_load_4d(dst + M::TILE, &vmap, &bar[s], 0, g, slot_in, blk);
+          char* const to = pairs + s * M::PAIRS + c * 128;
+          tma_load_4d(to, &kpmap, &bar[s], slot_in, g, blk, 0);
+          tma_load_4d(to + M::VPAIRS, &vpmap, &bar[s], slot_in, g, blk, 0);
+        } else {
+          mbar_arrive(&bar[s]);
+        }
       }
+      __syncwarp();
     };
     if (my > 0) look_up(0);
     __syncwarp();
@@ -138,21 +158,14 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
           return reinterpret_cast<const char*>(p.q) +
                  (((size_t)b * p.Sq + rg / p.G) * p.Hq + (size_t)g * p.G + rg % p.G) * D * 2;
         },
-        p.qk_scale, lane);
-    int2 lim[NT];  // keys that this thread's rows see, and the least of the tile's
-    int least = 0x7fffffff;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      auto limit = [&](int r) {
-        const int rg = rb * ROWS + r;
-        if (rg >= p.M) return 0;
-        const int i = rg / p.G, keys = i < ql ? (p.causal ? n - ql + i + 1 : n) : 0;
-        least = min(least, keys);
-        return keys;
-      };
-      lim[t] = make_int2(limit(8 * t + 2 * qi), limit(8 * t + 2 * qi + 1));
-    }
-    least = __reduce_min_sync(kFull, least);
+        p.qk_scale, query, warp, lane);
+    auto limit = [&](int r) {  // the keys that row r of the tile sees, -1 for a padding row
+      const int rg = rb * ROWS + r, i = rg / p.G;
+      return rg >= p.M ? -1 : i >= ql ? 0 : p.causal ? n - ql + i + 1 : n;
+    };
+    int least = limit(lane % ROWS);
+    least = __reduce_min_sync(kFull, least < 0 ? 0x7fffffff : least);
+    __syncthreads();  // the queries are there
 
     for (int j = 0; j < my; ++j) {
       if (!stream_wait(&bar[st], phase)) {
@@ -166,31 +179,34 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
       const int x = SUB * j - base;  // (tile j + 2's look-up may have come in between)
       const uint32_t here = (x >= 0 ? held >> x : held_before >> (x + 32)) & ((1u << SUB) - 1);
       const int tok = t0 + (warp + NW * j) * M::TK;
-      const bool all = here == (1u << SUB) - 1 && tok + M::TK <= min(t1, least);
-      const char* const stage = ring + st * M::STAGE;
-      const uint32_t* const kp = reinterpret_cast<const uint32_t*>(stage + M::PAIRS);
-      float2 ks[SUB][2], vs[SUB][2];
-#pragma unroll
-      for (int c = 0; c < SUB; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * c + 8 * h + quad;
-          ks[c][h] = pair_values<T::QK>(kp[r]);
-          vs[c][h] = pair_values<T::QK>(kp[M::TK + r]);
-          if (!all) {  // (what lies behind the last token, or was not copied, may hold anything)
-            const bool ok = (here >> c & 1) && tok + r < t1;
-            ks[c][h] = ok ? ks[c][h] : make_float2(0.f, 0.f);
-            vs[c][h] = ok ? vs[c][h] : make_float2(0.f, 0.f);
-          }
-        }
-      const uint32_t kt = smem_addr(stage);
-      att.template tile<SUB>(
-          kt, kt + M::TILE, ks, vs, all,
-          [&](int c, int h, int t) {
-            const int x = tok + 16 * c + 8 * h + quad, end = (here >> c & 1) ? t1 : 0;
-            return make_uint2(x < min(lim[t].x, end), x < min(lim[t].y, end));
-          },
-          lane);
+      const uint32_t kt = smem_addr(ring + st * M::STAGE);
+      // a lane a token: its factors
+      const char* const pair = pairs + st * M::PAIRS + pair_at;
+      const float2 kp = pair_values<T::QK>(*reinterpret_cast<const uint32_t*>(pair));
+      const float2 vp = pair_values<T::QK>(*reinterpret_cast<const uint32_t*>(pair + M::VPAIRS));
+      float4 f = make_float4(kp.x, __fmaf_rn(8.f, kp.x, kp.y), vp.x, __fmaf_rn(8.f, vp.x, vp.y));
+      const float unit = att.vref;
+      const bool fits = fabsf(vp.x) <= unit && fabsf(vp.x) >= unit * kVRange;
+      if (here == (1u << SUB) - 1 && tok + M::TK <= min(t1, least) && __all_sync(kFull, fits)) {
+        f.z *= pow2_inverse(unit) * kPLift;
+        factors[t] = f;
+        __syncwarp();
+        att.template tile<SUB, true>(kt, kt + M::TILE, query, factors,
+                                     [](int, int, int) { return make_uint2(1, 1); }, lane);
+      } else {
+        // (what lies behind the last token, or was not copied, may hold anything)
+        const bool ok = (here >> (t >> 4) & 1) && tok + t < t1;
+        factors[t] = ok ? f : make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
+        att.template tile<SUB, false>(
+            kt, kt + M::TILE, query, factors,
+            [&](int c, int h, int i) {
+              const int x = tok + 16 * c + 8 * h + quad, end = (here >> c & 1) ? t1 : 0;
+              const int row = 8 * i + 2 * qi;
+              return make_uint2(x < min(limit(row), end), x < min(limit(row + 1), end));
+            },
+            lane);
+      }
       if (++st == NST) {
         st = 0;
         phase ^= 1;
@@ -247,8 +263,7 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
 }
 
 template <int D, int NT, int QK>
-cudaError_t launch_int4_instance(const KernelParams& prm, const Int4View& cache,
-                                 const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
+cudaError_t launch_int4_instance(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid,
                                  cudaStream_t s) {
   using T = Int4Attention<D, NT, QK>;
   using M = DecodeInt4Smem<T>;
@@ -266,18 +281,18 @@ cudaError_t launch_int4_instance(const KernelParams& prm, const Int4View& cache,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, prm, cache);
+  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], prm);
 }
 
 // Both row tiles of a head dim.
 template <int D>
-cudaError_t launch_int4_dim(const KernelParams& prm, const Int4View& cache, const CUtensorMap& kmap,
-                            const CUtensorMap& vmap, int grid, int mp, int qk, cudaStream_t s) {
+cudaError_t launch_int4_dim(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid, int mp,
+                            int qk, cudaStream_t s) {
   if (mp == 8)
-    return qk == Q_BF16 ? launch_int4_instance<D, 1, Q_BF16>(prm, cache, kmap, vmap, grid, s)
-                        : launch_int4_instance<D, 1, Q_FP16>(prm, cache, kmap, vmap, grid, s);
-  return qk == Q_BF16 ? launch_int4_instance<D, 2, Q_BF16>(prm, cache, kmap, vmap, grid, s)
-                      : launch_int4_instance<D, 2, Q_FP16>(prm, cache, kmap, vmap, grid, s);
+    return qk == Q_BF16 ? launch_int4_instance<D, 1, Q_BF16>(prm, maps, grid, s)
+                        : launch_int4_instance<D, 1, Q_FP16>(prm, maps, grid, s);
+  return qk == Q_BF16 ? launch_int4_instance<D, 2, Q_BF16>(prm, maps, grid, s)
+                      : launch_int4_instance<D, 2, Q_FP16>(prm, maps, grid, s);
 }
 
 }  // namespace pa

@@ -3,9 +3,9 @@
 
 namespace pa {
 
-cudaError_t launch_int4_d64(const KernelParams& prm, const Int4View& cache, const CUtensorMap& kmap,
-                          const CUtensorMap& vmap, int grid, int mp, int qk, cudaStream_t s) {
-  return launch_int4_dim<64>(prm, cache, kmap, vmap, grid, mp, qk, s);
+cudaError_t launch_int4_d64(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid, int mp,
+                           int qk, cudaStream_t s) {
+  return launch_int4_dim<64>(prm, maps, grid, mp, qk, s);
 }
 int int4_ctas_per_sm_d64(int mp) {
   return mp == 8 ? DecodeInt4Smem<Int4Attention<64, 1, Q_BF16>>::CTAS_PER_SM

@@ -12,6 +12,12 @@
 // so a K row's words are operands as they lie.  A V operand holds one channel of two tokens: one byte
 // permute brings the halves of two tokens' words together.  P^T comes from S^T through movmatrix.
 //
+// What bounds it are the instructions of the few warps whose state fits the registers, so little is
+// done twice: the queries' fragments lie in shared memory, one copy a CTA; a lane a token makes a
+// token's factors from its pairs; of a K word's two masked halves one is taken as 64 + c, the 72 too
+// much being in the logits' accumulators from the start (72 times the sum of those channels' queries);
+// a tile that every row sees whole, with V steps that fit the accumulators' unit, passes no mask.
+//
 // Thread (quad, qi) = (lane / 4, lane % 4): tokens quad and quad + 8 of a chunk and query rows
 // 8 t + 2 qi, + 1 of the logits; tokens 2 qi, 2 qi + 1 (+ 8) of V.
 #pragma once
@@ -27,6 +33,11 @@ __device__ __forceinline__ uint32_t int4_even(uint32_t w) {
   asm("{\n .reg .b32 t;\n lop3.b32 t, %1, 0x000f000f, %2, 0xea;\n sub.rn.f16x2 %0, t, %3;\n}"
       : "=r"(r)
       : "r"(w), "r"(0x64006400u), "r"(0x64086408u));
+  return r;
+}
+__device__ __forceinline__ uint32_t int4_odd_64(uint32_t w) {  // 64 + c
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(r) : "r"(w), "r"(0x54005400u));
   return r;
 }
 __device__ __forceinline__ uint32_t int4_odd(uint32_t w) {
@@ -49,10 +60,10 @@ struct Int4Attention {
   static constexpr int ROW = D / 2;        // bytes of a cached row
   static constexpr int KW = D / 32;        // words of a K row that a lane holds (two k-steps each)
   static constexpr int VW = D / 64;        // words of a V row that a lane holds (8 channels each)
-  static constexpr int KSTEPS = D / 16;
   static constexpr int MB = D / 16;        // 16-channel blocks of the output
   static constexpr int OSTR = D + 4;       // floats between rows of a staged accumulator
   static constexpr int O_SLOT = ROWS * OSTR * 4;
+  static constexpr int QUERY = KW * 32 * NT * 16;  // bytes of the queries' fragments
 
   // Rows of a tile in shared memory: as the TMA boxes bring them, 16-byte pieces swizzled over rows of
   // 64 bytes (by bits 1 and 2 of the row) and 128 (by its low three bits).  Which of the tokens
@@ -60,20 +71,19 @@ struct Int4Attention {
   static __device__ __forceinline__ int first_token(int qi) {
     return D == 128 ? qi & 1 : D == 64 ? qi >> 1 : 0;
   }
-  // The lane's words of the K row of token quad + 8 h of chunk c.
-  static __device__ __forceinline__ void k_words(uint32_t tile, int c, int h, int lane, uint32_t (&w)[KW]) {
+  // The lane's words of the K row of token quad + 8 h of chunk c: group j of GW.
+  static constexpr int GW = cmin(KW, 4);
+  static __device__ __forceinline__ void k_words(uint32_t tile, int c, int h, int j, int lane,
+                                                 uint32_t (&w)[GW]) {
     const int quad = lane >> 2, qi = lane & 3;
     const uint32_t row = tile + (16 * c + 8 * h + quad) * ROW;
     if constexpr (D == 64) {
       asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(row + 8 * qi));
     } else {
-#pragma unroll
-      for (int j = 0; j < KW / 4; ++j) {
-        const int piece = D == 128 ? qi ^ (quad >> 1) : (2 * qi + j) ^ quad;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3])
-                     : "r"(row + (piece << 4)));
-      }
+      const int piece = D == 128 ? qi ^ (quad >> 1) : (2 * qi + j) ^ quad;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(row + (piece << 4)));
     }
   }
   // Its words of the V row of one of the tokens 2 qi, 2 qi + 1 (+ 8 h), the first one for e = 0.
@@ -93,9 +103,10 @@ struct Int4Attention {
                    : "r"(row + ((quad ^ r) << 4)));
   }
 
-  uint32_t qb[KSTEPS][NT][2];
-  float2 scale[NT], qsum[NT];  // of rows 8 t + 2 qi, + 1: logit scale (log2 units), sum of q (as scaled)
-  float2 m[NT], l[NT], low[NT];
+  // Of rows 8 t + 2 qi, + 1: the logit's factor (log2 units, >= 0), the sum of q (as scaled), -72 times
+  // its sum over the channels that K words hold in odd nibbles, minus the running maximum in log2
+  // units, and the sums of the weights and of the weights times low + 8 step.
+  float2 scale[NT], qsum[NT], start[NT], base[NT], l[NT], low[NT];
   float o[MB][NT][4];  // channels 8 W + 2 j, + 1 of the two rows, in units of vref / kPLift
   float vref, vtop;
 
@@ -103,16 +114,17 @@ struct Int4Attention {
     vref = vtop = kPow2Least;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t] = make_float2(-INFINITY, -INFINITY);
+      base[t] = make_float2(INFINITY, INFINITY);
       l[t] = low[t] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < MB; ++j) o[j][t][0] = o[j][t][1] = o[j][t][2] = o[j][t][3] = 0.f;
     }
   }
 
-  // row_of(r): query row r of the tile, or null for a padding row.
+  // row_of(r): query row r of the tile, or null for a padding row.  The rows' fragments go to `query`
+  // in shared memory: [KW][32 lanes][NT][4 words], of which warp `warp` of four writes its share.
   template <class F>
-  __device__ __forceinline__ void load_q(F row_of, float qk_scale, int lane) {
+  __device__ __forceinline__ void load_q(F row_of, float qk_scale, uint4* query, int warp, int lane) {
     const int quad = lane >> 2, qi = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -151,34 +163,48 @@ struct Int4Attention {
             h[w][e] = pack2<true>(a.x * mul, a.y * mul);
           }
       }
-      float sum = 0.f;
+      if (qk_scale < 0.f) {  // the sign goes into the query: a row's largest logit is its largest product
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[w][e] ^= 0x80008000u;
+      }
+      float even = 0.f, odd = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 a = f16x2_to_f2(h[w][e]);
-          sum += a.x + a.y;
+          even += a.x;
+          odd += a.y;
         }
         // pairs of channels (0, 4), (1, 5), (2, 6), (3, 7), as a word's nibbles come
-        qb[2 * w][t][0] = __byte_perm(h[w][0], h[w][2], 0x5410);
-        qb[2 * w][t][1] = __byte_perm(h[w][0], h[w][2], 0x7632);
-        qb[2 * w + 1][t][0] = __byte_perm(h[w][1], h[w][3], 0x5410);
-        qb[2 * w + 1][t][1] = __byte_perm(h[w][1], h[w][3], 0x7632);
+        if (warp == w % 4)
+          query[(w * 32 + lane) * NT + t] =
+              make_uint4(__byte_perm(h[w][0], h[w][2], 0x5410), __byte_perm(h[w][0], h[w][2], 0x7632),
+                         __byte_perm(h[w][1], h[w][3], 0x5410), __byte_perm(h[w][1], h[w][3], 0x7632));
       }
-      sum += __shfl_xor_sync(kFull, sum, 1);
-      sum += __shfl_xor_sync(kFull, sum, 2);
-      // row r's sum and scale are with the lanes 4 r .. 4 r + 3
-      const float sc = qk_scale * up;
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        even += __shfl_xor_sync(kFull, even, d);
+        odd += __shfl_xor_sync(kFull, odd, d);
+      }
+      // row r's sums and scale are with the lanes 4 r .. 4 r + 3
+      const float sc = fabsf(qk_scale) * up, sum = even + odd, st = -72.f * odd;
       scale[t] = make_float2(__shfl_sync(kFull, sc, 8 * qi), __shfl_sync(kFull, sc, 8 * qi + 4));
       qsum[t] = make_float2(__shfl_sync(kFull, sum, 8 * qi), __shfl_sync(kFull, sum, 8 * qi + 4));
+      start[t] = make_float2(__shfl_sync(kFull, st, 8 * qi), __shfl_sync(kFull, st, 8 * qi + 4));
     }
   }
 
-  // The running maxima follow the logits x only when one beats its row's by 2^8.
+  // The running maxima follow the raw logits mx only when one beats its row's by 2^8.  (A row that has
+  // seen no key has base +inf, and a masked logit gives -inf or NaN, which beats nothing.)
   __device__ __forceinline__ void follow(const float2 (&mx)[NT]) {
     bool beaten = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) beaten |= mx[t].x > m[t].x + 8.f || mx[t].y > m[t].y + 8.f;
+    for (int t = 0; t < NT; ++t)
+      beaten |= __fmaf_rn(mx[t].x, scale[t].x, base[t].x) > 8.f ||
+                __fmaf_rn(mx[t].y, scale[t].y, base[t].y) > 8.f;
     if (!__any_sync(kFull, beaten)) return;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -188,10 +214,13 @@ struct Int4Attention {
         a.x = fmaxf(a.x, __shfl_xor_sync(kFull, a.x, d));
         a.y = fmaxf(a.y, __shfl_xor_sync(kFull, a.y, d));
       }
-      const float2 n = make_float2(a.x > m[t].x + 8.f ? a.x : m[t].x, a.y > m[t].y + 8.f ? a.y : m[t].y);
-      const float2 f = make_float2(n.x == m[t].x ? 1.f : fast_exp2(m[t].x - n.x),
-                                   n.y == m[t].y ? 1.f : fast_exp2(m[t].y - n.y));
-      m[t] = n;
+      const bool up[2] = {__fmaf_rn(a.x, scale[t].x, base[t].x) > 8.f,
+                          __fmaf_rn(a.y, scale[t].y, base[t].y) > 8.f};
+      const float2 n = make_float2(up[0] ? -(a.x * scale[t].x) : base[t].x,
+                                   up[1] ? -(a.y * scale[t].y) : base[t].y);
+      const float2 f = make_float2(up[0] ? fast_exp2(n.x - base[t].x) : 1.f,
+                                   up[1] ? fast_exp2(n.y - base[t].y) : 1.f);
+      base[t] = n;
       l[t] = fmul2(l[t], f);
       low[t] = fmul2(low[t], f);
 #pragma unroll
@@ -204,157 +233,167 @@ struct Int4Attention {
     }
   }
 
-  // SUB chunks of 16 tokens, their K rows at shared address kt and V rows at vt.
-  // ks, vs [c][h]: (step, low) of token quad + 8 h, zero where no row may see the token;
-  // sees(c, h, t): which of the rows 8 t + 2 qi, + 1 see token quad + 8 h of chunk c; all: every row
-  // sees every token.
-  template <int SUB, class FS>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const float2 (&ks)[SUB][2],
-                                       const float2 (&vs)[SUB][2], bool all, FS sees, int lane) {
-    const int qi = lane & 3;
-    float2 x[SUB][2][NT];  // logits of token quad + 8 h
+  // O^T += V^T P^T for SUB chunks, the weights times their V steps as operands in pb.
+  template <int SUB>
+  __device__ __forceinline__ void add_values(uint32_t vt, const uint32_t (&pb)[SUB][NT][2], int lane) {
+    const uint32_t sel = first_token(lane & 3) ? 0x1054u : 0x5410u;  // low halves of tokens 2 qi, 2 qi + 1
 #pragma unroll
     for (int c = 0; c < SUB; ++c) {
-      float s[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      uint32_t w[2][KW];
-      k_words(kt, c, 0, lane, w[0]);
-      k_words(kt, c, 1, lane, w[1]);
-#pragma unroll
-      for (int i = 0; i < KW; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t u0 = k ? w[0][i] >> 8 : w[0][i], u1 = k ? w[1][i] >> 8 : w[1][i];
-          const uint32_t a[4] = {int4_even(u0), int4_even(u1), int4_odd(u0), int4_odd(u1)};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<true>(s[t], a, qb[2 * i + k][t][0], qb[2 * i + k][t][1]);
-        }
+      uint32_t w[2][2][VW];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float step = ks[c][h].x, mid = __fmaf_rn(8.f, step, ks[c][h].y);
+        v_words(vt, c, h, 0, lane, w[h][0]);
+        v_words(vt, c, h, 1, lane, w[h][1]);
+      }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float2 v = fmul2(make_float2(mid, mid), qsum[t]);
-          v = ffma2(make_float2(s[t][2 * h], s[t][2 * h + 1]), make_float2(step, step), v);
-          v = fmul2(v, scale[t]);
-          if (!all) {
-            const uint2 ok = sees(c, h, t);
-            v.x = ok.x ? v.x : -INFINITY;
-            v.y = ok.y ? v.y : -INFINITY;
+      for (int i = 0; i < VW; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // channels 0 .. 3, 4 .. 7 of the word
+          uint32_t z[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) z[h] = __byte_perm(w[h][0][i], w[h][1][i], sel + (k ? 0x2222u : 0u));
+          const uint32_t y[2] = {z[0] >> 8, z[1] >> 8};
+          const uint32_t a[4] = {int4_even(z[0]), int4_odd(z[0]), int4_even(z[1]), int4_odd(z[1])};
+          const uint32_t b[4] = {int4_even(y[0]), int4_odd(y[0]), int4_even(y[1]), int4_odd(y[1])};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816<true>(o[4 * i + 2 * k][t], a, pb[c][t][0], pb[c][t][1]);
+            mma16816<true>(o[4 * i + 2 * k + 1][t], b, pb[c][t][0], pb[c][t][1]);
           }
-          x[c][h][t] = v;
-        }
-      }
-    }
-    float2 mx[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      mx[t] = x[0][0][t];
-#pragma unroll
-      for (int c = 0; c < SUB; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[t].x = fmaxf(mx[t].x, x[c][h][t].x);
-          mx[t].y = fmaxf(mx[t].y, x[c][h][t].y);
         }
     }
-    follow(mx);
-    // the largest finite V step (its magnitude) below `end`: warp-uniform
-    auto largest = [&](float end) -> float {
-      float a = 0.f;
+  }
+
+  // SUB chunks of 16 tokens, their K rows at shared address kt, V rows at vt, the queries' fragments
+  // at `query` and the tokens' factors at `factors`: (K step, K low + 8 step, V factor, V low + 8
+  // step), zeros where no row may see the token.
+  // HOT: every row sees every token, and the V factor is the V step over the accumulators' unit times
+  // kPLift.  Otherwise it is the V step itself, and sees(c, h, t) says which of the rows 8 t + 2 qi, + 1
+  // see token quad + 8 h of chunk c.
+  template <int SUB, bool HOT, class FS>
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const uint4* query,
+                                       const float4* factors, FS sees, int lane) {
+    const int quad = lane >> 2;
+    float s[SUB][NT][4];
 #pragma unroll
-      for (int c = 0; c < SUB; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v = fabsf(vs[c][h].x);
-          a = fmaxf(a, v < end ? v : 0.f);
-        }
-      return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
-    };
-    // the unit to the step v, if need be; the least step that it serves (0: any)
-    auto serve = [&](float v) -> float {
-      if (v > vref || (v > 0.f && v < vref * kVRange)) {
-        const float f = move_v_unit(v, vref, vtop);
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][t][e] *= f;
-      }
-      return v < vref * kVRange ? 0.f : vref * kVRange;
-    };
-    // weights (a masked logit, -inf, gives 0, also while the row has seen no key) and O^T += V^T P^T
-    // for the V steps that `factor` does not make zero
-    auto attend = [&](auto factor, bool first) {
-      uint32_t pb[SUB][NT][2];
+    for (int c = 0; c < SUB; ++c)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float2 base = make_float2(m[t].x == -INFINITY ? 0.f : -m[t].x,
-                                        m[t].y == -INFINITY ? 0.f : -m[t].y);
+        s[c][t][0] = s[c][t][2] = start[t].x;
+        s[c][t][1] = s[c][t][3] = start[t].y;
+      }
+#pragma unroll
+    for (int j = 0; j < KW / GW; ++j) {
+      uint32_t w[SUB][2][GW];
+#pragma unroll
+      for (int c = 0; c < SUB; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) k_words(kt, c, h, j, lane, w[c][h]);
+#pragma unroll
+      for (int i = 0; i < GW; ++i) {
+        uint4 q[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) q[t] = query[((j * GW + i) * 32 + lane) * NT + t];
 #pragma unroll
         for (int c = 0; c < SUB; ++c)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float step = vs[c][h].x, f = factor(step);
-            float2 p = fadd2(x[c][h][t], base);
-            p.x = fast_exp2(p.x);
-            p.y = fast_exp2(p.y);
-            if (first) {
-              const float mid = __fmaf_rn(8.f, step, vs[c][h].y);
-              l[t] = fadd2(l[t], p);
-              low[t] = ffma2(p, make_float2(mid, mid), low[t]);
-            }
-            p = fmul2(p, make_float2(f, f));
-            pb[c][t][h] = transpose8(pack2<true>(p.x, p.y));
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t u0 = k ? w[c][0][i] >> 8 : w[c][0][i], u1 = k ? w[c][1][i] >> 8 : w[c][1][i];
+            const uint32_t a[4] = {int4_even(u0), int4_even(u1), int4_odd_64(u0), int4_odd_64(u1)};
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              mma16816<true>(s[c][t], a, k ? q[t].z : q[t].x, k ? q[t].w : q[t].y);
           }
       }
-      const uint32_t sel = first_token(qi) ? 0x1054u : 0x5410u;  // low halves of tokens 2 qi, 2 qi + 1
+    }
+    // raw logits, of token quad + 8 h
+    float2 mx[NT];
 #pragma unroll
-      for (int c = 0; c < SUB; ++c) {
-        uint32_t w[2][2][VW];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          v_words(vt, c, h, 0, lane, w[h][0]);
-          v_words(vt, c, h, 1, lane, w[h][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < VW; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {  // channels 0 .. 3, 4 .. 7 of the word
-            uint32_t z[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) z[h] = __byte_perm(w[h][0][i], w[h][1][i], sel + (k ? 0x2222u : 0u));
-            const uint32_t y[2] = {z[0] >> 8, z[1] >> 8};
-            const uint32_t a[4] = {int4_even(z[0]), int4_odd(z[0]), int4_even(z[1]), int4_odd(z[1])};
-            const uint32_t b[4] = {int4_even(y[0]), int4_odd(y[0]), int4_even(y[1]), int4_odd(y[1])};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma16816<true>(o[4 * i + 2 * k][t], a, pb[c][t][0], pb[c][t][1]);
-              mma16816<true>(o[4 * i + 2 * k + 1][t], b, pb[c][t][0], pb[c][t][1]);
-            }
-          }
-      }
-    };
-    bool mine = true;
+    for (int t = 0; t < NT; ++t) mx[t] = make_float2(-INFINITY, -INFINITY);
+    float2 vf[SUB][2];
 #pragma unroll
     for (int c = 0; c < SUB; ++c)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float a = fabsf(vs[c][h].x);
-        mine &= a <= vref && (a >= vref * kVRange || a == 0.f);
+        const float4 f = factors[16 * c + 8 * h + quad];
+        vf[c][h] = make_float2(f.z, f.w);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float x0 = __fmaf_rn(s[c][t][2 * h], f.x, f.y * qsum[t].x);
+          float x1 = __fmaf_rn(s[c][t][2 * h + 1], f.x, f.y * qsum[t].y);
+          if (!HOT) {
+            const uint2 ok = sees(c, h, t);
+            x0 = ok.x ? x0 : -INFINITY;
+            x1 = ok.y ? x1 : -INFINITY;
+          }
+          mx[t].x = fmaxf(mx[t].x, x0);
+          mx[t].y = fmaxf(mx[t].y, x1);
+          s[c][t][2 * h] = x0;
+          s[c][t][2 * h + 1] = x1;
+        }
       }
-    if (__all_sync(kFull, mine)) {  // the unit serves every step of the tile, as a rule
-      const float vinv = pow2_inverse(vref) * kPLift;
-      attend([&](float v) { return v * vinv; }, true);
-    } else {  // a pass for the steps that one unit serves after the other, from the largest on
+    follow(mx);
+    // weights exp2(scale x - maximum), summed alone and times low + 8 step, then times `factor` of
+    // their V factor as operands; a masked logit (-inf) gives 0
+    auto weigh = [&](auto factor, bool sums, uint32_t (&pb)[SUB][NT][2]) {
+#pragma unroll
+      for (int c = 0; c < SUB; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = factor(vf[c][h].x), mid = vf[c][h].y;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float x0 = s[c][t][2 * h], x1 = s[c][t][2 * h + 1];
+            float2 e = make_float2(fast_exp2(__fmaf_rn(x0, scale[t].x, base[t].x)),
+                                   fast_exp2(__fmaf_rn(x1, scale[t].y, base[t].y)));
+            if (!HOT) {
+              e.x = x0 == -INFINITY ? 0.f : e.x;
+              e.y = x1 == -INFINITY ? 0.f : e.y;
+            }
+            if (sums) {
+              l[t] = fadd2(l[t], e);
+              low[t].x = __fmaf_rn(e.x, mid, low[t].x);
+              low[t].y = __fmaf_rn(e.y, mid, low[t].y);
+            }
+            pb[c][t][h] = transpose8(pack2<true>(e.x * f, e.y * f));
+          }
+        }
+    };
+    uint32_t pb[SUB][NT][2];
+    if constexpr (HOT) {
+      weigh([&](float v) { return v; }, true, pb);
+      add_values<SUB>(vt, pb, lane);
+    } else {
+      // the largest finite V step (its magnitude) below `end`: warp-uniform
+      auto largest = [&](float end) -> float {
+        float a = 0.f;
+#pragma unroll
+        for (int c = 0; c < SUB; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float v = fabsf(vf[c][h].x);
+            a = fmaxf(a, v < end ? v : 0.f);
+          }
+        return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
+      };
+      // a pass for the steps that one unit serves after the other, from the largest on
       float done = __uint_as_float(0x7fc00000u);  // steps from here on are in o (NaN: none yet)
 #pragma unroll 1
       for (float v = largest(INFINITY); v > 0.f || done != done;) {
-        const float floor = serve(v), vinv = pow2_inverse(vref) * kPLift;
-        // (NaN and infinity are in, in the first pass at least)
-        attend([&](float a) { return fabsf(a) < floor || fabsf(a) >= done ? 0.f : a * vinv; }, done != done);
+        if (v > vref || (v > 0.f && v < vref * kVRange)) {  // the unit to the step v
+          const float f = move_v_unit(v, vref, vtop);
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j][t][e] *= f;
+        }
+        // the least step that it serves (0: any); NaN and infinity are in, in the first pass at least
+        const float floor = v < vref * kVRange ? 0.f : vref * kVRange;
+        const float vinv = pow2_inverse(vref) * kPLift;
+        weigh([&](float a) { return fabsf(a) < floor || fabsf(a) >= done ? 0.f : a * vinv; }, done != done, pb);
+        add_values<SUB>(vt, pb, lane);
         done = floor;
         v = largest(floor);
       }
@@ -385,8 +424,8 @@ struct Int4Attention {
             make_float2(__fmaf_rn(o[j][t][1], f, low[t].y), __fmaf_rn(o[j][t][3], f, low[t].y));
       }
       if (quad == 0) {
-        ml[r] = make_float2(m[t].x, l[t].x);
-        ml[r + 1] = make_float2(m[t].y, l[t].y);
+        ml[r] = make_float2(-base[t].x, l[t].x);
+        ml[r + 1] = make_float2(-base[t].y, l[t].y);
       }
     }
   }

@@ -328,9 +328,9 @@ struct DecodeArgs {
   int q_kind, kv_kind;
 };
 
-// Returns cudaErrorNotSupported when no kernel instance matches.
-cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          cudaStream_t s);
+// maps: of the K and V caches and, for a 4-bit cache, of their pairs.  Returns cudaErrorNotSupported
+// when no kernel instance matches.
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t s);
 
 cudaError_t launch_reduce(const DecodeArgs& a, cudaStream_t s);
 

@@ -32,12 +32,9 @@ cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, co
 
 cudaError_t launch_stream(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int, int,
                           cudaStream_t);
-cudaError_t launch_int4_d64(const KernelParams&, const Int4View&, const CUtensorMap&,
-                            const CUtensorMap&, int, int, int, cudaStream_t);
-cudaError_t launch_int4_d128(const KernelParams&, const Int4View&, const CUtensorMap&,
-                            const CUtensorMap&, int, int, int, cudaStream_t);
-cudaError_t launch_int4_d256(const KernelParams&, const Int4View&, const CUtensorMap&,
-                            const CUtensorMap&, int, int, int, cudaStream_t);
+cudaError_t launch_int4_d64(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
+cudaError_t launch_int4_d128(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
+cudaError_t launch_int4_d256(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
 int int4_ctas_per_sm_d64(int);
 int int4_ctas_per_sm_d128(int);
 int int4_ctas_per_sm_d256(int);
@@ -112,19 +109,16 @@ KernelParams make_kernel_params(const DecodeArgs& a) {
   return p;
 }
 
-cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          cudaStream_t s) {
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t s) {
+  const CUtensorMap &kmap = maps[0], &vmap = maps[1];
   const KernelParams prm = make_kernel_params(a);
   const int scales = staged_scales(a.scale_mode);
   const bool toks = scales != SC_NONE;
   if (a.v.path == 4) {
-    const Int4View cache{static_cast<const char*>(a.k_cache), static_cast<const char*>(a.v_cache),
-                         static_cast<const uint32_t*>(a.k_scale),
-                         static_cast<const uint32_t*>(a.v_scale)};
     switch (a.p.head_dim) {
-      case 64: return launch_int4_d64(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
-      case 128: return launch_int4_d128(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
-      case 256: return launch_int4_d256(prm, cache, kmap, vmap, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 64: return launch_int4_d64(prm, maps, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 128: return launch_int4_d128(prm, maps, a.v.ctas, a.v.mp, a.q_kind, s);
+      case 256: return launch_int4_d256(prm, maps, a.v.ctas, a.v.mp, a.q_kind, s);
       default: return cudaErrorNotSupported;
     }
   }
