@@ -15,108 +15,23 @@
 // the quotient, ties to even, magnitudes past 448 saturating to 448.  A 4-bit cache receives codes of
 // the row between its least and largest element and their step and low (int4.cuh).
 //
-// One warp per (sequence, new row, kv head): each lane holds D / 32 consecutive elements
-// (8 to 16 bytes of input), the row's amax is a shuffle reduction, and the codes go out as
-// one 2-, 4- or 8-byte store per lane.  The work is a few bytes per new token, a latency-bound
-// kernel on the path before pa_plan / pa_decode.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+// D / 8 lanes a row and one to four rows a warp's step, 16 bytes of input a lane, a token's K and V rows
+// over as many warps as fill the GPU (append_row.cuh).  The work is a few bytes per new token, a
+// latency-bound kernel on the path before pa_plan / pa_decode.
 #include <cstdint>
 
 #include "append_row.cuh"
 
 namespace pa {
-namespace {
 
-constexpr int kAppendWarps = 8;
-
-struct AppendParams {
-  const char* k_new;
-  const char* v_new;
-  const int32_t* bt;
-  const int32_t* ctx;
-  const int32_t* qlens;
-  char* k_cache;
-  char* v_cache;
-  void* k_scale;
-  void* v_scale;
-  int32_t* flags;
-  long long rows;  // B * Sq * Hkv
-  int Sq, Hkv, bs, bs_shift, maxb, nblocks, scale_mode;
-};
-
-template <int D, int QK, int KIND>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
-  constexpr int E = D / 32;  // elements per lane: 2, 4 or 8
-  const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * kAppendWarps;
-  grid_dependency_wait();
-  for (long long row = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5); row < p.rows;
-       row += warps) {
-    const int g = (int)(row % p.Hkv);
-    const int i = (int)((row / p.Hkv) % p.Sq);
-    const int b = (int)(row / ((long long)p.Hkv * p.Sq));
-    const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
-    const long long cap = (long long)p.maxb * p.bs;
-    if (ql < 0 || ql > p.Sq || n < ql || (long long)n > cap) {
-      if (lane == 0 && i == 0 && g == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
-      continue;
-    }
-    if (i >= ql) continue;
-    const int pos = n - ql + i;
-    const int blk = __ldg(p.bt + (size_t)b * p.maxb + (pos >> p.bs_shift));
-    if (blk < 0 || blk >= p.nblocks) {
-      if (lane == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
-      continue;
-    }
-    const size_t crow = ((size_t)blk * p.bs + (pos & (p.bs - 1))) * p.Hkv + g;  // cache row
-    const size_t src = (size_t)row * D + (size_t)lane * E;                       // element
-    const RowPlace at{blk, pos & (p.bs - 1), g};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {  // K, then V
-      char* cache = t ? p.v_cache : p.k_cache;
-      void* scale = t ? p.v_scale : p.k_scale;
-      uint32_t w[E / 2];
-      load_row16<E>((t ? p.v_new : p.k_new) + src * 2, w);
-      if constexpr (KIND == STORE_16) {  // the row's bits
-        store_row16<E>(cache + (crow * D + (size_t)lane * E) * 2, w);
-      } else {
-        float x[E];
-        widen_row<QK, E>(w, x);
-        if constexpr (KIND == STORE_FP8)
-          put_fp8<D>(x, cache, static_cast<float*>(scale), crow, p.scale_mode, lane);
-        else
-          put_int4<D, QK>(x, cache, scale, crow, at, p.Hkv, p.bs, lane);
-      }
-    }
+cudaError_t launch_append(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s) {
+  switch (head_dim) {
+    case 64: return launch_append_d<64, false>(p, qk, kind, s);
+    case 128: return launch_append_d<128, false>(p, qk, kind, s);
+    default: return launch_append_d<256, false>(p, qk, kind, s);
   }
-  grid_dependents_launch();
 }
 
-template <int D>
-cudaError_t launch_append_d(const AppendParams& p, int qk, int kind, int grid, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kAppendWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-#define PA_APPEND(KIND_)                                                                     \
-  if (kind == KIND_)                                                                         \
-    return qk == Q_BF16 ? cudaLaunchKernelEx(&cfg, append_kernel<D, Q_BF16, KIND_>, p)       \
-                        : cudaLaunchKernelEx(&cfg, append_kernel<D, Q_FP16, KIND_>, p);
-  PA_APPEND(STORE_16)
-  PA_APPEND(STORE_FP8)
-  PA_APPEND(STORE_INT4)
-#undef PA_APPEND
-  return cudaErrorNotSupported;
-}
-
-}  // namespace
 }  // namespace pa
 
 using namespace pa;
@@ -154,7 +69,13 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
     return append_block(c, k_new, v_new, block_tables, context_lens, q_lens, k_cache, v_cache,
                         static_cast<float*>(k_scale), static_cast<float*>(v_scale), flags,
                         reinterpret_cast<cudaStream_t>(stream));
-  AppendParams p;
+  const long long tokens = (long long)c.batch * c.max_q_len;
+  if (tokens > INT32_MAX || (long long)c.num_kv_heads > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  AppendParams p{};
   p.k_new = static_cast<const char*>(k_new);
   p.v_new = static_cast<const char*>(v_new);
   p.bt = block_tables;
@@ -165,7 +86,8 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.flags = flags;
-  p.rows = (long long)c.batch * c.max_q_len * c.num_kv_heads;
+  p.k_stride = p.v_stride = (long long)c.num_kv_heads * c.head_dim;
+  p.tokens = (int)tokens;
   p.Sq = c.max_q_len;
   p.Hkv = c.num_kv_heads;
   p.bs = c.block_size;
@@ -173,15 +95,11 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
   p.maxb = c.max_blocks_per_seq;
   p.nblocks = c.num_blocks;
   p.scale_mode = c.kv_scale_mode;
-  const long long ctas = (p.rows + kAppendWarps - 1) / kAppendWarps;
-  const int grid = (int)(ctas < 65535 ? ctas : 65535);
-  const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16, kind = store_kind(c);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  switch (c.head_dim) {
-    case 64: e = launch_append_d<64>(p, qk, kind, grid, s); break;
-    case 128: e = launch_append_d<128>(p, qk, kind, grid, s); break;
-    default: e = launch_append_d<256>(p, qk, kind, grid, s); break;
-  }
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  p.heads = 2 * c.num_kv_heads;
+  split_rows(p, c.head_dim, sms);
+  const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
+  return launch_append(p, c.head_dim, qk, store_kind(c), reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
 }

@@ -1,5 +1,5 @@
-// One K or V row of a token and kv head into its place in the cache, as pa_append_kv and
-// pa_append_rotated write it: a warp a row, E = D / 32 consecutive elements a lane.
+// K and V rows into their places in the cache, as pa_append_kv and pa_append_rotated write them: D / 8
+// lanes a row, eight consecutive elements (16 bytes of input) a lane, one to four rows a warp.
 #pragma once
 
 #include "append_block.cuh"
@@ -14,112 +14,343 @@ inline int store_kind(const pa_config& c) {
   return c.kv_dtype == PA_INT4 ? STORE_INT4 : c.kv_dtype == PA_FP8_E4M3 ? STORE_FP8 : STORE_16;
 }
 
+// How queries and keys are made ready on their way (pa_rotary; half = 0: no rotation).
+struct RotateParams {
+  const char* q_weight;
+  const char* k_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  int half, interleaved, table_rows, axes, axis1, axis2;  // pairs from axis1 (axis2) on: next axis
+  float eps;
+};
+
+struct AppendParams {
+  const char* q;
+  const char* k_new;
+  const char* v_new;
+  const int32_t* bt;
+  const int32_t* ctx;
+  const int32_t* qlens;
+  char* q_out;
+  char* k_out;
+  char* k_cache;
+  char* v_cache;
+  void* k_scale;
+  void* v_scale;
+  int32_t* flags;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  int tokens;                              // B * Sq
+  int Sq, Hq, Hkv, bs, bs_shift, maxb, nblocks, scale_mode;
+  int heads;         // rows of a token: q's (Hq, 0 in the plain append), k's, and v's if any are stored
+  int parts, per;    // a token's rows are the work of `parts` warps, `per` steps each
+  FastDiv part_div, token_div;  // by parts and by Sq
+  RotateParams r;
+};
+
+// Head dims 64, 128 and 256, in append.cu (no rotation) and rotate.cu.
+cudaError_t launch_append(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
+cudaError_t launch_rotate(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
+
+// Splits a token's rows over warps: as few steps a warp as fill the GPU with four warps a scheduler,
+// at most eight (the steps share the token's lengths, positions and angles).
+inline void split_rows(AppendParams& p, int head_dim, int sms) {
+  const int rows_per_step = 256 / head_dim;
+  const int steps = ceil_div(p.heads, rows_per_step);
+  const long long spare = (long long)p.tokens * steps / ((long long)sms * 16);
+  p.per = (int)(spare < 1 ? 1 : spare > 8 ? 8 : spare);
+  p.parts = ceil_div(steps, p.per);
+  p.part_div = FastDiv((uint32_t)p.parts);
+  p.token_div = FastDiv((uint32_t)p.Sq);
+}
+
 #if defined(__CUDACC__)
 
-// Elements of E 16-bit numbers at `src` (a multiple of 2 E bytes).
-template <int E>
-__device__ __forceinline__ void load_row16(const char* src, uint32_t (&w)[E / 2]) {
-  if constexpr (E == 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  } else if constexpr (E == 4) {
-    const uint2 v = *reinterpret_cast<const uint2*>(src);
-    w[0] = v.x;
-    w[1] = v.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(src);
-  }
-}
-template <int E>
-__device__ __forceinline__ void store_row16(char* dst, const uint32_t (&w)[E / 2]) {
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  else if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = w[0];
-}
-template <int QK, int E>
-__device__ __forceinline__ void widen_row(const uint32_t (&w)[E / 2], float (&x)[E]) {
+template <int QK>
+__device__ __forceinline__ void widen_row(const uint4& w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
-    const float2 f = pair_values<QK>(w[k]);
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = pair_values<QK>(u[k]);
     x[2 * k] = f.x;
     x[2 * k + 1] = f.y;
   }
 }
-template <int QK, int E>
-__device__ __forceinline__ void narrow_row(const float (&x)[E], uint32_t (&w)[E / 2]) {
+template <int QK>
+__device__ __forceinline__ uint4 narrow_row(const float (&x)[8]) {
+  uint32_t u[4];
 #pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
+  for (int k = 0; k < 4; ++k) {
     if constexpr (QK == Q_BF16) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      u[k] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
       const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      u[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Where a row goes: the cache (whole), its scales (or pairs), the block and the slot in it, and
-// the kv head.
-struct RowPlace {
-  int blk, slot, head;
-};
-
-// The fp8 row x in one of the scale modes of a token, a tensor or none.
-template <int D>
-__device__ __forceinline__ void put_fp8(const float (&x)[D / 32], char* cache, float* scale,
-                                        size_t row, int scale_mode, int lane) {
-  constexpr int E = D / 32;
-  float s = 1.f;
+// Eight E4M3 codes of the lane's elements in one of the scale modes of a token, a tensor or none;
+// the row's scale in *scale_of_row.
+template <int L>
+__device__ __forceinline__ uint2 codes_fp8(const float (&x)[8], const float* scale, int scale_mode,
+                                           float* scale_of_row) {
+  uint32_t c[4];
   if (scale_mode == PA_SCALE_PER_TOKEN) {
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    if (lane == 0) scale[row] = s;
-  } else if (scale_mode == PA_SCALE_PER_TENSOR) {
-    s = __ldg(scale);
-  }
-  uint32_t c[E / 2];
+    for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    *scale_of_row = s;
+    // quotients of at most 448: IEEE ones by one step from the rounded reciprocal (a y below 2^-70
+    // gives a code of zero by either way)
+    const bool plain = s >= 0x1p-60f && s <= 0x1p60f;
+    const float inv = __fdiv_rn(1.f, s);
 #pragma unroll
-  for (int k = 0; k < E / 2; ++k) {
-    const float a = scale_mode == PA_SCALE_NONE ? x[2 * k] : __fdiv_rn(x[2 * k], s);
-    const float b = scale_mode == PA_SCALE_NONE ? x[2 * k + 1] : __fdiv_rn(x[2 * k + 1], s);
-    c[k] = e4m3x2_rn_sat(a, b);
+    for (int k = 0; k < 4; ++k) {
+      const float a = plain ? quotient(x[2 * k], s, inv) : __fdiv_rn(x[2 * k], s);
+      const float b = plain ? quotient(x[2 * k + 1], s, inv) : __fdiv_rn(x[2 * k + 1], s);
+      c[k] = e4m3x2_rn_sat(a, b);
+    }
+  } else {
+    const float s = scale_mode == PA_SCALE_PER_TENSOR ? __ldg(scale) : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      c[k] = scale_mode == PA_SCALE_PER_TENSOR
+                 ? e4m3x2_rn_sat(__fdiv_rn(x[2 * k], s), __fdiv_rn(x[2 * k + 1], s))
+                 : e4m3x2_rn_sat(x[2 * k], x[2 * k + 1]);
   }
-  char* d = cache + row * D + (size_t)lane * E;
-  if constexpr (E == 8)
-    *reinterpret_cast<uint2*>(d) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  else if constexpr (E == 4)
-    *reinterpret_cast<uint32_t*>(d) = c[0] | (c[1] << 16);
-  else
-    *reinterpret_cast<uint16_t*>(d) = (uint16_t)c[0];
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// The 4-bit row x.
-template <int D, int QK>
-__device__ __forceinline__ void put_int4(const float (&x)[D / 32], char* cache, void* pairs,
-                                         size_t row, const RowPlace& at, int Hkv, int bs, int lane) {
-  constexpr int E = D / 32;
-  uint32_t pair;
-  const uint32_t codes = quantise_row<QK, E>(x, &pair);
-  char* d = cache + row * (D / 2) + (size_t)lane * (E / 2);
-  if constexpr (E == 8)
-    *reinterpret_cast<uint32_t*>(d) = codes;
-  else if constexpr (E == 4)
-    *reinterpret_cast<uint16_t*>(d) = (uint16_t)codes;
-  else
-    *reinterpret_cast<uint8_t*>(d) = (uint8_t)codes;
-  if (lane == 0)
-    reinterpret_cast<uint32_t*>(pairs)[((size_t)at.blk * Hkv + at.head) * bs + at.slot] = pair;
+// The row over the root of its mean square, times the weight.  The whole warp is here.
+template <int QK, int L>
+__device__ __forceinline__ void normalise(float (&x)[8], const uint4& weight, float eps) {
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum = __fmaf_rn(x[e], x[e], sum);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  const float inv = __frsqrt_rn(__fmaf_rn(sum, 1.f / (8 * L), eps));
+  float f[8];
+  widen_row<QK>(weight, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * f[e];
+}
+
+template <int D, int QK, int KIND, bool ROT>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+  constexpr int L = D / 8, RPS = 32 / L;  // lanes of a row, rows of a step
+  constexpr int U = 4;                    // steps whose rows are loaded together
+  const int lane = threadIdx.x & 31, sub = lane / L, c0 = lane % L * 8;
+  const long long warps = (long long)gridDim.x * 8, all = (long long)p.tokens * p.parts;
+  grid_dependency_wait();
+  for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < all; w += warps) {
+    int token, part;
+    if (all <= INT32_MAX) {
+      token = (int)p.part_div.div((uint32_t)w);
+      part = (int)w - token * p.parts;
+    } else {
+      token = (int)(w / p.parts);
+      part = (int)(w % p.parts);
+    }
+    const int b = (int)p.token_div.div((uint32_t)token), i = token - b * p.Sq;
+    const int n = __ldg(p.ctx + b), ql = __ldg(p.qlens + b);
+    const long long cap = (long long)p.maxb << p.bs_shift;
+    if (ql < 0 || ql > p.Sq || n < ql || (long long)n > cap) {
+      if (lane == 0 && i == 0 && part == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
+      continue;
+    }
+    if (i >= ql) continue;
+    const int pos = n - ql + i, first = part * p.per * RPS, end = min(p.heads, first + p.per * RPS);
+    const int k_head = ROT ? p.Hq : 0, v_head = k_head + p.Hkv;
+    // the token's angles: of channels c0 .. c0 + 7 (interleaved: of their four pairs)
+    float cs[8], sn[8];
+    bool turns = false, second = false;
+    if constexpr (ROT) {
+      if (p.r.half > 0 && first < v_head) {
+        int at[3] = {pos, pos, pos};
+        bool bad = false;
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+          if (a >= p.r.axes) break;
+          if (p.r.positions) at[a] = __ldg(p.r.positions + (size_t)a * p.tokens + token);
+          bad |= at[a] < 0 || at[a] >= p.r.table_rows;
+        }
+        if (bad) {
+          if (lane == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_POSITION);
+          continue;
+        }
+        turns = c0 < 2 * p.r.half;
+        second = !p.r.interleaved && c0 >= p.r.half;
+        const int pair = p.r.interleaved ? c0 / 2 : second ? c0 - p.r.half : c0;
+        const int count = p.r.interleaved ? 4 : 8;
+        if (turns) {
+          const float* row = p.r.cos_sin + (size_t)at[0] * (2 * p.r.half) + pair;
+          if (p.r.axes == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+              if (e < count) {
+                const float4 c = __ldg(reinterpret_cast<const float4*>(row + e));
+                const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.r.half + e));
+                cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
+                sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+              }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < count) {
+                const int a = pair + e < p.r.axis1 ? at[0] : pair + e < p.r.axis2 ? at[1] : at[2];
+                const float* x = p.r.cos_sin + (size_t)a * (2 * p.r.half) + pair + e;
+                cs[e] = __ldg(x);
+                sn[e] = __ldg(x + p.r.half);
+              }
+          }
+        }
+      } else if (p.r.half > 0) {  // (values alone: the token is not written either if its position is bad)
+        bool bad = false;
+        for (int a = 0; a < p.r.axes; ++a) {
+          const int x = p.r.positions ? __ldg(p.r.positions + (size_t)a * p.tokens + token) : pos;
+          bad |= x < 0 || x >= p.r.table_rows;
+        }
+        if (bad) continue;
+      }
+    }
+    int blk = -1;
+    if (p.k_cache && end > k_head) {
+      blk = __ldg(p.bt + (size_t)b * p.maxb + (pos >> p.bs_shift));
+      if (blk < 0 || blk >= p.nblocks) {
+        if (lane == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
+        blk = -1;
+      }
+    }
+    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    if constexpr (ROT) {
+      if (p.r.q_weight) wq = __ldg(reinterpret_cast<const uint4*>(p.r.q_weight) + lane % L);
+      if (p.r.k_weight) wk = __ldg(reinterpret_cast<const uint4*>(p.r.k_weight) + lane % L);
+    }
+    const int slot = pos & (p.bs - 1);
+    const size_t crow0 = ((size_t)max(blk, 0) * p.bs + slot) * p.Hkv;
+    for (int base = first; base < end; base += U * RPS) {
+      uint4 in[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {  // (in place: a row is read here and written below, by the same lanes)
+        const int h = base + k * RPS + sub;
+        if (h < end) {
+          const char* src;
+          if (ROT && h < k_head)
+            src = p.q + ((size_t)token * p.q_stride + (size_t)h * D) * 2;
+          else if (h < v_head)
+            src = p.k_new + ((size_t)token * p.k_stride + (size_t)(h - k_head) * D) * 2;
+          else
+            src = p.v_new + ((size_t)token * p.v_stride + (size_t)(h - v_head) * D) * 2;
+          in[k] = *reinterpret_cast<const uint4*>(src + c0 * 2);
+        } else {
+          in[k] = make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h0 = base + k * RPS, h = h0 + sub;
+        if (h0 >= end) break;
+        const bool is_q = ROT && h < k_head, is_v = h >= v_head;
+        uint4 out = in[k];
+        float x[8];
+        if (ROT || KIND != STORE_16) widen_row<QK>(in[k], x);
+        if constexpr (ROT) {
+          if (h0 < v_head) {  // (all lanes: some rows of the step are not values)
+            const bool norm = !is_v && (is_q ? p.r.q_weight : p.r.k_weight) != nullptr;
+            if (__any_sync(kFull, norm)) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = x[e];
+              normalise<QK, L>(y, is_q ? wq : wk, p.r.eps);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = norm ? y[e] : x[e];
+            }
+            if (p.r.half > 0) {
+              const bool turn = turns && !is_v;
+              if (p.r.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                  const float u = x[e], v = x[e + 1];
+                  x[e] = turn ? u * cs[e / 2] - v * sn[e / 2] : u;
+                  x[e + 1] = turn ? v * cs[e / 2] + u * sn[e / 2] : v;
+                }
+              } else {
+                const int away = p.r.half / 8;  // lanes to the pair's other channel
+                const int from = turns ? (second ? lane - away : lane + away) : lane;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float y = __shfl_sync(kFull, x[e], from);
+                  const float z = second ? x[e] * cs[e] + y * sn[e] : x[e] * cs[e] - y * sn[e];
+                  x[e] = turn ? z : x[e];
+                }
+              }
+            }
+            if (!is_v) out = narrow_row<QK>(x);
+            if (h < end) {
+              if (is_q)
+                *reinterpret_cast<uint4*>(p.q_out + (((size_t)token * p.Hq + h) * D + c0) * 2) = out;
+              else if (!is_v && p.k_out)
+                *reinterpret_cast<uint4*>(p.k_out + (((size_t)token * p.Hkv + h - k_head) * D + c0) * 2) = out;
+            }
+          }
+        }
+        if (!p.k_cache || h0 + RPS <= k_head) continue;
+        const bool stores = h < end && !is_q && blk >= 0;
+        const int g = h - (is_v ? v_head : k_head);
+        const size_t crow = crow0 + (stores ? g : 0);
+        char* const cache = is_v ? p.v_cache : p.k_cache;
+        void* const scale = is_v ? p.v_scale : p.k_scale;
+        if constexpr (KIND == STORE_16) {
+          if (stores) *reinterpret_cast<uint4*>(cache + (crow * D + c0) * 2) = out;
+        } else if constexpr (KIND == STORE_FP8) {
+          float s;
+          const uint2 c = codes_fp8<L>(x, static_cast<const float*>(scale), p.scale_mode, &s);
+          if (stores) {
+            *reinterpret_cast<uint2*>(cache + crow * D + c0) = c;
+            if (c0 == 0 && p.scale_mode == PA_SCALE_PER_TOKEN) static_cast<float*>(scale)[crow] = s;
+          }
+        } else {
+          uint32_t pair;
+          const uint32_t c = quantise_row<QK, L>(x, &pair);
+          if (stores) {
+            *reinterpret_cast<uint32_t*>(cache + (crow * D + c0) / 2) = c;
+            if (c0 == 0)
+              static_cast<uint32_t*>(scale)[((size_t)blk * p.Hkv + g) * p.bs + slot] = pair;
+          }
+        }
+      }
+    }
+  }
+  grid_dependents_launch();
+}
+
+template <int D, bool ROT>
+cudaError_t launch_append_d(const AppendParams& p, int qk, int kind, cudaStream_t s) {
+  const long long ctas = ((long long)p.tokens * p.parts + 7) / 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas < (1 << 30) ? ctas : 1 << 30));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+#define PA_APPEND(KIND_)                                                                      \
+  if (kind == KIND_)                                                                          \
+    return qk == Q_BF16 ? cudaLaunchKernelEx(&cfg, append_kernel<D, Q_BF16, KIND_, ROT>, p)   \
+                        : cudaLaunchKernelEx(&cfg, append_kernel<D, Q_FP16, KIND_, ROT>, p);
+  PA_APPEND(STORE_16)
+  PA_APPEND(STORE_FP8)
+  PA_APPEND(STORE_INT4)
+#undef PA_APPEND
+  return cudaErrorNotSupported;
 }
 
 #endif  // __CUDACC__

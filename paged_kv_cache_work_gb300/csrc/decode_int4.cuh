@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
                        const __grid_constant__ CUtensorMap kpmap,
                        const __grid_constant__ CUtensorMap vpmap, const KernelParams p) {
   using M = DecodeInt4Smem<T>;
-  constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, NT = T::NT, SUB = M::SUB, NST = M::NST;
+  constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, SUB = M::SUB, NST = M::NST;
   static_assert(NST == 3, "two tiles in flight");
   extern __shared__ char smem_raw[];
   char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);

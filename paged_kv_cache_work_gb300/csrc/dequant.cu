@@ -1,7 +1,9 @@
 // pa_dequant_kv: a batch's rows of an fp8 or 4-bit cache read back as 16-bit values into contiguous
 // buffers, as pa_gather_kv lays out its copies.
 //
-// A CTA a page (of a sequence): eight values a thread at a time, one 16-byte store each.
+// Every CTA sums the lengths for itself and takes an equal run of the batch's rows.  A thread takes
+// eight values at a time (8 or 4 bytes in, 16 out), several such groups of its CTA's rows at once: for
+// each it looks up the page and the scale, so that pages of any size stream alike.
 #include "append_row.cuh"
 
 namespace pa {
@@ -9,6 +11,7 @@ namespace {
 
 constexpr int kDequantThreads = 256;
 constexpr int kDequantMaxBatch = 8192;
+constexpr int kDequantCtas = 4;  // of an SM
 
 struct DequantParams {
   const char* k_cache;
@@ -23,109 +26,154 @@ struct DequantParams {
   int32_t* flags;
   long long max_rows;
   int batch, Hkv, bs, bs_shift, maxb, nblocks, scale_mode;
+  FastDiv head_div;  // by Hkv
 };
 
 template <int D, int QK, int KIND>
-__global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const DequantParams p) {
-  __shared__ long long sums[2][kDequantThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31;
+__global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(const DequantParams p) {
+  constexpr int G8 = D / 8;                        // groups of eight values in a row
+  constexpr int U = KIND == STORE_INT4 ? 4 : 2;    // groups of K, and as many of V, in flight
+  extern __shared__ int32_t off[];                 // [batch + 1] rows before each sequence
+  __shared__ int sums[kDequantThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long cap = (long long)p.maxb << p.bs_shift;
-  const bool reports = blockIdx.x == 0 && blockIdx.y == 0;
   grid_dependency_wait();
-  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    // rows before this sequence's, and of all
-    long long before = 0, all = 0;
-    bool bad = false;
-    for (int j = tid; j < p.batch; j += kDequantThreads) {
-      int n = __ldg(p.ctx + j);
-      if (n < 0 || (long long)n > cap) {
-        bad = true;
-        n = 0;
-      }
-      all += n;
-      if (j < b) before += n;
+  int run = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.batch; b0 += kDequantThreads) {
+    const int b = b0 + tid;
+    int n = b < p.batch ? __ldg(p.ctx + b) : 0;
+    if (n < 0 || (long long)n > cap) {
+      bad = true;
+      n = 0;
     }
+    int x = n;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(kFull, before, o);
-      all += __shfl_xor_sync(kFull, all, o);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
     }
     __syncthreads();
-    if (lane == 0) {
-      sums[0][tid >> 5] = before;
-      sums[1][tid >> 5] = all;
-    }
-    bad = __syncthreads_or(bad);
-    before = all = 0;
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int before = run;
+#pragma unroll
     for (int w = 0; w < kDequantThreads / 32; ++w) {
-      before += sums[0][w];
-      all += sums[1][w];
+      before += w < warp ? sums[w] : 0;
+      run += sums[w];
     }
-    const bool overflow = all > p.max_rows;
-    if (reports && b == 0 && tid == 0 && p.flags && (bad || overflow))
-      atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
-    if (blockIdx.x == 0 && tid == 0 && p.row_offsets) {
-      p.row_offsets[b] = (int32_t)before;
-      if (b == p.batch - 1) p.row_offsets[p.batch] = (int32_t)all;
-    }
-    if (overflow) continue;
-    int n = __ldg(p.ctx + b);
-    if (n < 0 || (long long)n > cap) n = 0;
-    for (int page = blockIdx.x; ((long long)page << p.bs_shift) < n; page += gridDim.x) {
-      const int blk = __ldg(p.bt + (size_t)b * p.maxb + page);
-      if (blk < 0 || blk >= p.nblocks) {
-        if (tid == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
-        continue;
+    if (b < p.batch) off[b] = before + x - n;
+  }
+  if (tid == 0) off[p.batch] = run;
+  bad = __syncthreads_or(bad);
+  const bool overflow = run > p.max_rows;
+  if (blockIdx.x == 0) {
+    if (tid == 0 && p.flags && (bad || overflow)) atomicOr(p.flags, PA_FLAG_BAD_LENGTHS);
+    if (p.row_offsets)
+      for (int b = tid; b <= p.batch; b += kDequantThreads) p.row_offsets[b] = off[b];
+  }
+  if (overflow) return;
+  // this CTA's rows (a row: a token's heads), sequence by sequence
+  const int r0 = (int)((long long)run * blockIdx.x / gridDim.x);
+  const int r1 = (int)((long long)run * (blockIdx.x + 1) / gridDim.x);
+  if (r0 >= r1) return;
+  int seq = 0;  // the last sequence that starts at or before r0 (empty ones share their successor's start)
+  for (int step = 1 << (31 - __clz(p.batch)); step > 0; step >>= 1)
+    if (seq + step < p.batch && off[seq + step] <= r0) seq += step;
+  float tensor_scale[2] = {1.f, 1.f};
+  if (KIND == STORE_FP8 && p.scale_mode == PA_SCALE_PER_TENSOR) {
+    tensor_scale[0] = __ldg(static_cast<const float*>(p.k_scale));
+    tensor_scale[1] = __ldg(static_cast<const float*>(p.v_scale));
+  }
+  bool bad_block = false;
+  for (int at = r0; at < r1; ++seq) {
+    const int start = off[seq], rows = min(off[seq + 1], r1) - at, t0 = at - start;
+    const int32_t* const table = p.bt + (size_t)seq * p.maxb;
+    const uint32_t per_row = (uint32_t)p.Hkv * G8;
+    const long long groups = (long long)rows * per_row;
+    const size_t out0 = (size_t)at * per_row;
+    for (long long e0 = tid; e0 < groups; e0 += U * kDequantThreads) {
+      uint2 raw[U][2];
+      uint32_t pair[U][2];
+      float sc[U][2];
+      bool ok[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long e = e0 + u * kDequantThreads;
+        ok[u] = e < groups;
+        if (!ok[u]) continue;
+        // e = (row, head, group); a run of fewer than 2^31 row-heads goes through one multiplication
+        const long long rh = e / G8;
+        int r, g;
+        if (groups / G8 <= INT32_MAX) {
+          r = (int)p.head_div.div((uint32_t)rh);
+          g = (int)((uint32_t)rh - (uint32_t)r * (uint32_t)p.Hkv);
+        } else {
+          r = (int)(rh / p.Hkv);
+          g = (int)(rh % p.Hkv);
+        }
+        const int tok = t0 + r, slot = tok & (p.bs - 1);
+        const int blk = __ldg(table + (tok >> p.bs_shift));
+        if (blk < 0 || blk >= p.nblocks) {
+          bad_block = true;
+          ok[u] = false;
+          continue;
+        }
+        const size_t row = ((size_t)blk * p.bs + slot) * p.Hkv + g, from = row * G8 + (uint32_t)(e % G8);
+        if constexpr (KIND == STORE_INT4) {
+          raw[u][0].x = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache) + from);
+          raw[u][1].x = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache) + from);
+          const size_t i = ((size_t)blk * p.Hkv + g) * p.bs + slot;
+          pair[u][0] = __ldg(static_cast<const uint32_t*>(p.k_scale) + i);
+          pair[u][1] = __ldg(static_cast<const uint32_t*>(p.v_scale) + i);
+        } else {
+          raw[u][0] = __ldg(reinterpret_cast<const uint2*>(p.k_cache) + from);
+          raw[u][1] = __ldg(reinterpret_cast<const uint2*>(p.v_cache) + from);
+          sc[u][0] = tensor_scale[0];
+          sc[u][1] = tensor_scale[1];
+          if (p.scale_mode >= PA_SCALE_PER_TOKEN) {
+            const size_t i = p.scale_mode == PA_SCALE_PER_TOKEN ? row : (size_t)blk * p.Hkv + g;
+            sc[u][0] = __ldg(static_cast<const float*>(p.k_scale) + i);
+            sc[u][1] = __ldg(static_cast<const float*>(p.v_scale) + i);
+          }
+        }
       }
-      const int rows = min(p.bs, n - (page << p.bs_shift));
-      constexpr int G8 = D / 8;  // groups of eight values in a row
-      const int groups = rows * p.Hkv * G8;
-      for (int t = 0; t < 2; ++t) {
-        const char* cache = t ? p.v_cache : p.k_cache;
-        const void* scale = t ? p.v_scale : p.k_scale;
-        char* out = (t ? p.v_out : p.k_out) + (size_t)(before + ((long long)page << p.bs_shift)) * p.Hkv * D * 2;
-        for (int e = tid; e < groups; e += kDequantThreads) {
-          const int r = e / G8, slot = r / p.Hkv, g = r % p.Hkv;
-          const size_t at = (size_t)blk * p.bs * p.Hkv * G8 + e;  // the group among the cache's
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!ok[u]) continue;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
           float x[8];
           if constexpr (KIND == STORE_INT4) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(cache) + at);
-            const float2 f = pair_values<QK>(
-                __ldg(static_cast<const uint32_t*>(scale) + ((size_t)blk * p.Hkv + g) * p.bs + slot));
+            const float2 f = pair_values<QK>(pair[u][t]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __fmaf_rn((float)((w >> (4 * k)) & 15u), f.x, f.y);
+            for (int k = 0; k < 8; ++k)
+              x[k] = __fmaf_rn((float)((raw[u][t].x >> (4 * k)) & 15u), f.x, f.y);
           } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) + at);
-            float s = 1.f;
-            if (p.scale_mode == PA_SCALE_PER_TENSOR)
-              s = __ldg(static_cast<const float*>(scale));
-            else if (p.scale_mode == PA_SCALE_PER_TOKEN)
-              s = __ldg(static_cast<const float*>(scale) + ((size_t)blk * p.bs + slot) * p.Hkv + g);
-            else if (p.scale_mode == PA_SCALE_PER_BLOCK)
-              s = __ldg(static_cast<const float*>(scale) + (size_t)blk * p.Hkv + g);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t c = ((k < 2 ? w.x : w.y) >> (16 * (k & 1))) & 0xffffu;
+              const uint32_t c = ((k < 2 ? raw[u][t].x : raw[u][t].y) >> (16 * (k & 1))) & 0xffffu;
               const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-              x[2 * k] = f.x * s;
-              x[2 * k + 1] = f.y * s;
+              x[2 * k] = f.x * sc[u][t];
+              x[2 * k + 1] = f.y * sc[u][t];
             }
           }
-          uint32_t o[4];
-          narrow_row<QK, 8>(x, o);
-          *reinterpret_cast<uint4*>(out + (size_t)e * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(t ? p.v_out : p.k_out)[out0 + e0 + u * kDequantThreads] = narrow_row<QK>(x);
         }
       }
     }
+    at += rows;
   }
+  if (bad_block && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
   grid_dependents_launch();
 }
 
 template <int D>
-cudaError_t launch_dequant_d(const DequantParams& p, int qk, int kind, dim3 grid, cudaStream_t s) {
+cudaError_t launch_dequant_d(const DequantParams& p, int qk, int kind, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(grid);
+  cfg.dynamicSmemBytes = (size_t)(p.batch + 1) * 4;
   cfg.blockDim = dim3(kDequantThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -175,8 +223,8 @@ extern "C" pa_status pa_dequant_kv(const pa_config* cfg, const void* k_cache, co
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(row_offsets, 4) ||
       !aligned(flags, 4))
     return PA_ERR_INVALID_ARG;
-  // a page's groups and the row offsets are int32
-  if ((long long)c.num_kv_heads * c.head_dim > (1 << 19) ||
+  // the row offsets are int32
+  if ((long long)c.num_kv_heads * c.head_dim > (1 << 24) ||
       (long long)c.batch * c.max_blocks_per_seq * c.block_size > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   DequantParams p{};
@@ -198,7 +246,15 @@ extern "C" pa_status pa_dequant_kv(const pa_config* cfg, const void* k_cache, co
   p.maxb = c.max_blocks_per_seq;
   p.nblocks = c.num_blocks;
   p.scale_mode = c.kv_scale_mode;
-  const dim3 grid(c.max_blocks_per_seq < 65535 ? c.max_blocks_per_seq : 65535, c.batch);
+  p.head_div = FastDiv((uint32_t)c.num_kv_heads);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  // a CTA for every few thousand values that there may be, as many as fit at once
+  const double most = (double)c.batch * c.max_blocks_per_seq * c.block_size * c.num_kv_heads * c.head_dim;
+  const double ctas = most / (8.0 * kDequantThreads) + 1;
+  const int grid = (int)(ctas < (double)sms * kDequantCtas ? ctas : (double)sms * kDequantCtas);
   const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16, kind = store_kind(c);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

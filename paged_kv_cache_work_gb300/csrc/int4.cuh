@@ -1,7 +1,7 @@
 // Rows of a 4-bit cache: codes c in 0 .. 15, two a byte, and a pair (step, low) of the queries' type
 // for each token and kv head; a value is low + step c.
 //
-// A warp quantises a row whose lanes hold D / 32 consecutive elements each.  low is the row's least
+// D / 8 lanes quantise a row, eight consecutive elements each.  low is the row's least
 // element rounded down to the pair's type (an element itself when the row has that type), step the
 // least number of the type that is not below (max - low) / 15, so that every quotient lies in
 // [0, 15] and none is clipped.  One row of pairs for a page and kv head lies together: the decode
@@ -51,26 +51,28 @@ __device__ __forceinline__ float quotient(float y, float s, float r) {
   return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
 }
 
-// The warp's row, E elements a lane: its codes (the lane's first in the lowest four bits) and pair.
-template <int QK, int E>
-__device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], uint32_t* pair) {
+// A row over L lanes (of a warp that is here as a whole), eight elements a lane: the lane's codes (its
+// first element's in the lowest four bits) and the row's pair.
+template <int QK, int L>
+__device__ __forceinline__ uint32_t quantise_row(const float (&x)[8], uint32_t* pair) {
   float lo = x[0], hi = x[0];
   bool nan = false;
 #pragma unroll
-  for (int k = 0; k < E; ++k) {
+  for (int k = 0; k < 8; ++k) {
     lo = fminf(lo, x[k]);
     hi = fmaxf(hi, x[k]);
     nan |= x[k] != x[k];
   }
+  lo = nan ? -INFINITY : lo;  // (a NaN's row has no finite range either)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = L / 2; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
   }
   const uint32_t low_bits = round_down<QK>(lo);
   const float low = pair_values<QK>(low_bits << 16).y;
   const float range = hi - low;
-  if (__any_sync(kFull, nan) || !(range < INFINITY)) {
+  if (!(range < INFINITY)) {
     *pair = 0x7fffu | low_bits << 16;  // step NaN (in both types)
     return 0;
   }
@@ -82,7 +84,7 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], uint32_t* 
   const bool plain = step >= 0x1p-60f && step <= 0x1p60f;
   const float inv = __fdiv_rn(1.f, step);
 #pragma unroll
-  for (int k = 0; k < E; ++k) {
+  for (int k = 0; k < 8; ++k) {
     const float y = x[k] - low;
     // (a y below 2^-70 gives a quotient below a half by either way of dividing)
     const float q = plain ? quotient(y, step, inv) : __fdiv_rn(y, step);
