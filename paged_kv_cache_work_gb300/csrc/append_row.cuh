@@ -2,6 +2,8 @@
 // lanes a row, eight consecutive elements (16 bytes of input) a lane, one to four rows a warp.
 #pragma once
 
+#include <type_traits>
+
 #include "append_block.cuh"
 #include "int4.cuh"
 
@@ -41,8 +43,8 @@ struct AppendParams {
   long long q_stride, k_stride, v_stride;  // elements between tokens
   int tokens;                              // B * Sq
   int Sq, Hq, Hkv, bs, bs_shift, maxb, nblocks, scale_mode;
-  int heads;         // rows of a token: q's (Hq, 0 in the plain append), k's, and v's if any are stored
-  int parts, per;    // a token's rows are the work of `parts` warps, `per` steps each
+  int q_steps, k_steps, v_steps;  // steps of a token's q, k and v rows (none where none are wanted)
+  int parts, per;    // they are the work of `parts` warps, `per` steps each
   FastDiv part_div, token_div;  // by parts and by Sq
   RotateParams r;
 };
@@ -51,13 +53,17 @@ struct AppendParams {
 cudaError_t launch_append(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
 cudaError_t launch_rotate(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
 
-// Splits a token's rows over warps: as few steps a warp as fill the GPU with four warps a scheduler,
-// at most eight (the steps share the token's lengths, positions and angles).
-inline void split_rows(AppendParams& p, int head_dim, int sms) {
+// Splits a token's rows over warps: as few steps a warp as fill the GPU with eight warps a scheduler,
+// at most 24 (the steps share the token's lengths, positions and angles).  A step is one to four
+// rows of one kind.
+inline void split_rows(AppendParams& p, int head_dim, int sms, bool stores) {
   const int rows_per_step = 256 / head_dim;
-  const int steps = ceil_div(p.heads, rows_per_step);
-  const long long spare = (long long)p.tokens * steps / ((long long)sms * 16);
-  p.per = (int)(spare < 1 ? 1 : spare > 8 ? 8 : spare);
+  p.q_steps = ceil_div(p.Hq, rows_per_step);
+  p.k_steps = ceil_div(p.Hkv, rows_per_step);
+  p.v_steps = stores ? p.k_steps : 0;
+  const int steps = p.q_steps + p.k_steps + p.v_steps;
+  const long long spare = (long long)p.tokens * steps / ((long long)sms * 32);
+  p.per = (int)(spare < 1 ? 1 : spare > 24 ? 24 : spare);
   p.parts = ceil_div(steps, p.per);
   p.part_div = FastDiv((uint32_t)p.parts);
   p.token_div = FastDiv((uint32_t)p.Sq);
@@ -134,7 +140,7 @@ __device__ __forceinline__ void normalise(float (&x)[8], const uint4& weight, fl
   for (int e = 0; e < 8; ++e) sum = __fmaf_rn(x[e], x[e], sum);
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  const float inv = __frsqrt_rn(__fmaf_rn(sum, 1.f / (8 * L), eps));
+  const float inv = rsqrtf(__fmaf_rn(sum, 1.f / (8 * L), eps));
   float f[8];
   widen_row<QK>(weight, f);
 #pragma unroll
@@ -142,11 +148,12 @@ __device__ __forceinline__ void normalise(float (&x)[8], const uint4& weight, fl
 }
 
 template <int D, int QK, int KIND, bool ROT>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, KIND == STORE_16 && !ROT ? 4 : 3) append_kernel(const AppendParams p) {
   constexpr int L = D / 8, RPS = 32 / L;  // lanes of a row, rows of a step
   constexpr int U = 4;                    // steps whose rows are loaded together
   const int lane = threadIdx.x & 31, sub = lane / L, c0 = lane % L * 8;
   const long long warps = (long long)gridDim.x * 8, all = (long long)p.tokens * p.parts;
+  const int k_step = ROT ? p.q_steps : 0, v_step = k_step + p.k_steps, steps = v_step + p.v_steps;
   grid_dependency_wait();
   for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < all; w += warps) {
     int token, part;
@@ -165,13 +172,13 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
       continue;
     }
     if (i >= ql) continue;
-    const int pos = n - ql + i, first = part * p.per * RPS, end = min(p.heads, first + p.per * RPS);
-    const int k_head = ROT ? p.Hq : 0, v_head = k_head + p.Hkv;
-    // the token's angles: of channels c0 .. c0 + 7 (interleaved: of their four pairs)
+    const int pos = n - ql + i, first = part * p.per, end = min(steps, first + p.per);
+    // the token's angles: of channels c0 .. c0 + 7 (interleaved: of their four pairs); the sine is
+    // negative where the pair's other channel is subtracted
     float cs[8], sn[8];
-    bool turns = false, second = false;
+    bool turns = false, all_turn = false;
     if constexpr (ROT) {
-      if (p.r.half > 0 && first < v_head) {
+      if (p.r.half > 0) {
         int at[3] = {pos, pos, pos};
         bool bad = false;
 #pragma unroll
@@ -184,43 +191,40 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
           if (lane == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_POSITION);
           continue;
         }
+        all_turn = 2 * p.r.half == D;
         turns = c0 < 2 * p.r.half;
-        second = !p.r.interleaved && c0 >= p.r.half;
+        const bool second = c0 >= p.r.half;  // (of half-split pairs)
         const int pair = p.r.interleaved ? c0 / 2 : second ? c0 - p.r.half : c0;
-        const int count = p.r.interleaved ? 4 : 8;
-        if (turns) {
-          const float* row = p.r.cos_sin + (size_t)at[0] * (2 * p.r.half) + pair;
-          if (p.r.axes == 1) {
+        if (turns && first < v_step) {
+          auto axis = [&](int x) { return x < p.r.axis1 ? at[0] : x < p.r.axis2 ? at[1] : at[2]; };
 #pragma unroll
-            for (int e = 0; e < 8; e += 4)
-              if (e < count) {
-                const float4 c = __ldg(reinterpret_cast<const float4*>(row + e));
-                const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.r.half + e));
-                cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
-                sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
-              }
-          } else {
+          for (int e = 0; e < 8; e += 4) {
+            if (e == 4 && p.r.interleaved) break;
+            const int x = pair + e, lo = axis(x), hi = axis(x + 3);
+            const float* row = p.r.cos_sin + (size_t)lo * (2 * p.r.half) + x;
+            if (p.r.axes == 1 || (lo == hi && axis(x + 1) == lo && axis(x + 2) == lo)) {
+              const float4 c = __ldg(reinterpret_cast<const float4*>(row));
+              const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.r.half));
+              cs[e] = c.x, cs[e + 1] = c.y, cs[e + 2] = c.z, cs[e + 3] = c.w;
+              sn[e] = s.x, sn[e + 1] = s.y, sn[e + 2] = s.z, sn[e + 3] = s.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < count) {
-                const int a = pair + e < p.r.axis1 ? at[0] : pair + e < p.r.axis2 ? at[1] : at[2];
-                const float* x = p.r.cos_sin + (size_t)a * (2 * p.r.half) + pair + e;
-                cs[e] = __ldg(x);
-                sn[e] = __ldg(x + p.r.half);
+              for (int k = 0; k < 4; ++k) {
+                const float* y = p.r.cos_sin + (size_t)axis(x + k) * (2 * p.r.half) + x + k;
+                cs[e + k] = __ldg(y);
+                sn[e + k] = __ldg(y + p.r.half);
               }
+            }
+          }
+          if (!p.r.interleaved && !second) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
           }
         }
-      } else if (p.r.half > 0) {  // (values alone: the token is not written either if its position is bad)
-        bool bad = false;
-        for (int a = 0; a < p.r.axes; ++a) {
-          const int x = p.r.positions ? __ldg(p.r.positions + (size_t)a * p.tokens + token) : pos;
-          bad |= x < 0 || x >= p.r.table_rows;
-        }
-        if (bad) continue;
       }
     }
     int blk = -1;
-    if (p.k_cache && end > k_head) {
+    if (p.k_cache && end > k_step) {
       blk = __ldg(p.bt + (size_t)b * p.maxb + (pos >> p.bs_shift));
       if (blk < 0 || blk >= p.nblocks) {
         if (lane == 0 && p.flags) atomicOr(p.flags, PA_FLAG_BAD_BLOCK_ID);
@@ -234,98 +238,96 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     }
     const int slot = pos & (p.bs - 1);
     const size_t crow0 = ((size_t)max(blk, 0) * p.bs + slot) * p.Hkv;
-    for (int base = first; base < end; base += U * RPS) {
-      uint4 in[U];
+    // steps [s0, s1) of the rows of one kind, `rows` of them, from `src` on
+    enum { ROW_Q, ROW_K, ROW_V };
+    auto run = [&](auto kind_, int s0, int s1, int rows, const char* src, char* dense, char* cache,
+                   void* scale) {
+      constexpr int ROWS = decltype(kind_)::value;
+      int h = s0 * RPS + sub;
+      src += (size_t)h * (D * 2) + c0 * 2;
+      dense += (size_t)h * (D * 2) + c0 * 2;
+      const uint4 weight = ROWS == ROW_Q ? wq : wk;
+      const bool norm = ROT && ROWS != ROW_V && (ROWS == ROW_Q ? p.r.q_weight : p.r.k_weight) != nullptr;
+      const bool writes = ROT && (ROWS == ROW_Q || (ROWS == ROW_K && p.k_out));
+      for (; s0 < s1; s0 += U, h += U * RPS, src += U * RPS * D * 2, dense += U * RPS * D * 2) {
+        uint4 in[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {  // (in place: a row is read here and written below, by the same lanes)
-        const int h = base + k * RPS + sub;
-        if (h < end) {
-          const char* src;
-          if (ROT && h < k_head)
-            src = p.q + ((size_t)token * p.q_stride + (size_t)h * D) * 2;
-          else if (h < v_head)
-            src = p.k_new + ((size_t)token * p.k_stride + (size_t)(h - k_head) * D) * 2;
-          else
-            src = p.v_new + ((size_t)token * p.v_stride + (size_t)(h - v_head) * D) * 2;
-          in[k] = *reinterpret_cast<const uint4*>(src + c0 * 2);
-        } else {
+        for (int k = 0; k < U; ++k) {  // (in place: a row is read here and written below, by the same lanes)
           in[k] = make_uint4(0, 0, 0, 0);
+          if (s0 + k < s1 && h + k * RPS < rows) in[k] = *reinterpret_cast<const uint4*>(src + k * RPS * D * 2);
         }
-      }
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h0 = base + k * RPS, h = h0 + sub;
-        if (h0 >= end) break;
-        const bool is_q = ROT && h < k_head, is_v = h >= v_head;
-        uint4 out = in[k];
-        float x[8];
-        if (ROT || KIND != STORE_16) widen_row<QK>(in[k], x);
-        if constexpr (ROT) {
-          if (h0 < v_head) {  // (all lanes: some rows of the step are not values)
-            const bool norm = !is_v && (is_q ? p.r.q_weight : p.r.k_weight) != nullptr;
-            if (__any_sync(kFull, norm)) {
-              float y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = x[e];
-              normalise<QK, L>(y, is_q ? wq : wk, p.r.eps);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = norm ? y[e] : x[e];
-            }
+        for (int k = 0; k < U; ++k) {
+          if (s0 + k >= s1) break;
+          const int g = h + k * RPS;
+          const bool real = g < rows;
+          uint4 out = in[k];
+          float x[8];
+          if ((ROT && ROWS != ROW_V) || KIND != STORE_16) widen_row<QK>(in[k], x);
+          if constexpr (ROT && ROWS != ROW_V) {
+            if (norm) normalise<QK, L>(x, weight, p.r.eps);
             if (p.r.half > 0) {
-              const bool turn = turns && !is_v;
+              float y[8];  // the row turned
               if (p.r.interleaved) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                  const float u = x[e], v = x[e + 1];
-                  x[e] = turn ? u * cs[e / 2] - v * sn[e / 2] : u;
-                  x[e + 1] = turn ? v * cs[e / 2] + u * sn[e / 2] : v;
+                  y[e] = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
+                  y[e + 1] = x[e + 1] * cs[e / 2] + x[e] * sn[e / 2];
                 }
               } else {
                 const int away = p.r.half / 8;  // lanes to the pair's other channel
-                const int from = turns ? (second ? lane - away : lane + away) : lane;
+                const int from = !turns ? lane : c0 >= p.r.half ? lane - away : lane + away;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float y = __shfl_sync(kFull, x[e], from);
-                  const float z = second ? x[e] * cs[e] + y * sn[e] : x[e] * cs[e] - y * sn[e];
-                  x[e] = turn ? z : x[e];
-                }
+                for (int e = 0; e < 8; ++e)
+                  y[e] = __fmaf_rn(__shfl_sync(kFull, x[e], from), sn[e], x[e] * cs[e]);
+              }
+              if (all_turn) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = y[e];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = turns ? y[e] : x[e];
               }
             }
-            if (!is_v) out = narrow_row<QK>(x);
-            if (h < end) {
-              if (is_q)
-                *reinterpret_cast<uint4*>(p.q_out + (((size_t)token * p.Hq + h) * D + c0) * 2) = out;
-              else if (!is_v && p.k_out)
-                *reinterpret_cast<uint4*>(p.k_out + (((size_t)token * p.Hkv + h - k_head) * D + c0) * 2) = out;
+            out = narrow_row<QK>(x);
+            if (real && writes) *reinterpret_cast<uint4*>(dense + k * RPS * D * 2) = out;
+          }
+          if constexpr (ROWS != ROW_Q) {
+            if (!p.k_cache) continue;
+            const bool stores = real && blk >= 0;
+            const size_t crow = crow0 + (stores ? g : 0);
+            if constexpr (KIND == STORE_16) {
+              if (stores) *reinterpret_cast<uint4*>(cache + (crow * D + c0) * 2) = out;
+            } else if constexpr (KIND == STORE_FP8) {
+              float s;
+              const uint2 c = codes_fp8<L>(x, static_cast<const float*>(scale), p.scale_mode, &s);
+              if (stores) {
+                *reinterpret_cast<uint2*>(cache + crow * D + c0) = c;
+                if (c0 == 0 && p.scale_mode == PA_SCALE_PER_TOKEN) static_cast<float*>(scale)[crow] = s;
+              }
+            } else {
+              uint32_t pair;
+              const uint32_t c = quantise_row<QK, L>(x, &pair);
+              if (stores) {
+                *reinterpret_cast<uint32_t*>(cache + (crow * D + c0) / 2) = c;
+                if (c0 == 0)
+                  static_cast<uint32_t*>(scale)[((size_t)blk * p.Hkv + g) * p.bs + slot] = pair;
+              }
             }
-          }
-        }
-        if (!p.k_cache || h0 + RPS <= k_head) continue;
-        const bool stores = h < end && !is_q && blk >= 0;
-        const int g = h - (is_v ? v_head : k_head);
-        const size_t crow = crow0 + (stores ? g : 0);
-        char* const cache = is_v ? p.v_cache : p.k_cache;
-        void* const scale = is_v ? p.v_scale : p.k_scale;
-        if constexpr (KIND == STORE_16) {
-          if (stores) *reinterpret_cast<uint4*>(cache + (crow * D + c0) * 2) = out;
-        } else if constexpr (KIND == STORE_FP8) {
-          float s;
-          const uint2 c = codes_fp8<L>(x, static_cast<const float*>(scale), p.scale_mode, &s);
-          if (stores) {
-            *reinterpret_cast<uint2*>(cache + crow * D + c0) = c;
-            if (c0 == 0 && p.scale_mode == PA_SCALE_PER_TOKEN) static_cast<float*>(scale)[crow] = s;
-          }
-        } else {
-          uint32_t pair;
-          const uint32_t c = quantise_row<QK, L>(x, &pair);
-          if (stores) {
-            *reinterpret_cast<uint32_t*>(cache + (crow * D + c0) / 2) = c;
-            if (c0 == 0)
-              static_cast<uint32_t*>(scale)[((size_t)blk * p.Hkv + g) * p.bs + slot] = pair;
           }
         }
       }
-    }
+    };
+    if (ROT && first < k_step)
+      run(std::integral_constant<int, ROW_Q>(), first, min(end, k_step), p.Hq,
+          p.q + (size_t)token * p.q_stride * 2, p.q_out + (size_t)token * p.Hq * (D * 2), nullptr, nullptr);
+    if (first < v_step && end > k_step)
+      run(std::integral_constant<int, ROW_K>(), max(first - k_step, 0), min(end, v_step) - k_step, p.Hkv,
+          p.k_new + (size_t)token * p.k_stride * 2, p.k_out + (size_t)token * p.Hkv * (D * 2), p.k_cache,
+          p.k_scale);
+    if (end > v_step)
+      run(std::integral_constant<int, ROW_V>(), max(first - v_step, 0), end - v_step, p.Hkv,
+          p.v_new + (size_t)token * p.v_stride * 2, nullptr, p.v_cache, p.v_scale);
   }
   grid_dependents_launch();
 }

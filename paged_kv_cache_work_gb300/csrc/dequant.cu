@@ -11,7 +11,13 @@ namespace {
 
 constexpr int kDequantThreads = 256;
 constexpr int kDequantMaxBatch = 8192;
-constexpr int kDequantCtas = 4;  // of an SM
+// CTAs of an SM and groups of K (and as many of V) that a thread has in flight.  Us a pass over 64
+// contexts of 8,192 to 16,384 tokens of an fp8 cache with a scale a token (one kv head of 128), 8 of
+// 2,048 to 16,384 of a 4-bit cache (16 heads of 256), and a 4-bit step (append too): 4 CTAs of 4 groups
+// 118, 267 and 9.6; 6 of 2 103, 267 and 10.1; 6 of 1 103, 281 and 12.8; 8 of 1 110, 265 and 13.5; 2 of
+// 8 153, 267 and 11.7.
+constexpr int dequant_ctas(int kind) { return kind == STORE_INT4 ? 4 : 6; }
+constexpr int dequant_groups(int kind) { return kind == STORE_INT4 ? 4 : 2; }
 
 struct DequantParams {
   const char* k_cache;
@@ -30,9 +36,9 @@ struct DequantParams {
 };
 
 template <int D, int QK, int KIND>
-__global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(const DequantParams p) {
+__global__ void __launch_bounds__(kDequantThreads, dequant_ctas(KIND)) dequant_kernel(const DequantParams p) {
   constexpr int G8 = D / 8;                        // groups of eight values in a row
-  constexpr int U = KIND == STORE_INT4 ? 4 : 2;    // groups of K, and as many of V, in flight
+  constexpr int U = dequant_groups(KIND);
   extern __shared__ int32_t off[];                 // [batch + 1] rows before each sequence
   __shared__ int sums[kDequantThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -86,32 +92,28 @@ __global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(
     tensor_scale[1] = __ldg(static_cast<const float*>(p.v_scale));
   }
   bool bad_block = false;
-  for (int at = r0; at < r1; ++seq) {
-    const int start = off[seq], rows = min(off[seq + 1], r1) - at, t0 = at - start;
+  // a thread's group of its row is always the same, its rows kDequantThreads / G8 apart
+  constexpr int S = kDequantThreads / G8;
+  const uint32_t group = tid % G8;
+  const int most_rows = INT32_MAX / 2 / p.Hkv;  // (row-heads are counted in 32 bits)
+  for (int at = r0; at < r1;) {
+    while (off[seq + 1] <= at) ++seq;
+    const int t0 = at - off[seq], rows = min(min(off[seq + 1], r1) - at, most_rows);
     const int32_t* const table = p.bt + (size_t)seq * p.maxb;
-    const uint32_t per_row = (uint32_t)p.Hkv * G8;
-    const long long groups = (long long)rows * per_row;
-    const size_t out0 = (size_t)at * per_row;
-    for (long long e0 = tid; e0 < groups; e0 += U * kDequantThreads) {
+    const int heads = rows * p.Hkv;
+    uint4* const ko = reinterpret_cast<uint4*>(p.k_out) + (size_t)at * p.Hkv * G8 + group;
+    uint4* const vo = reinterpret_cast<uint4*>(p.v_out) + (size_t)at * p.Hkv * G8 + group;
+    for (int h0 = tid / G8; h0 < heads; h0 += U * S) {
       uint2 raw[U][2];
       uint32_t pair[U][2];
       float sc[U][2];
       bool ok[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const long long e = e0 + u * kDequantThreads;
-        ok[u] = e < groups;
+        const int rh = h0 + u * S;
+        ok[u] = rh < heads;
         if (!ok[u]) continue;
-        // e = (row, head, group); a run of fewer than 2^31 row-heads goes through one multiplication
-        const long long rh = e / G8;
-        int r, g;
-        if (groups / G8 <= INT32_MAX) {
-          r = (int)p.head_div.div((uint32_t)rh);
-          g = (int)((uint32_t)rh - (uint32_t)r * (uint32_t)p.Hkv);
-        } else {
-          r = (int)(rh / p.Hkv);
-          g = (int)(rh % p.Hkv);
-        }
+        const int r = (int)p.head_div.div((uint32_t)rh), g = rh - r * p.Hkv;
         const int tok = t0 + r, slot = tok & (p.bs - 1);
         const int blk = __ldg(table + (tok >> p.bs_shift));
         if (blk < 0 || blk >= p.nblocks) {
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(
           ok[u] = false;
           continue;
         }
-        const size_t row = ((size_t)blk * p.bs + slot) * p.Hkv + g, from = row * G8 + (uint32_t)(e % G8);
+        const size_t row = ((size_t)blk * p.bs + slot) * p.Hkv + g, from = row * G8 + group;
         if constexpr (KIND == STORE_INT4) {
           raw[u][0].x = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache) + from);
           raw[u][1].x = __ldg(reinterpret_cast<const uint32_t*>(p.v_cache) + from);
@@ -146,9 +148,9 @@ __global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(
           float x[8];
           if constexpr (KIND == STORE_INT4) {
             const float2 f = pair_values<QK>(pair[u][t]);
+            code_values(raw[u][t].x, x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              x[k] = __fmaf_rn((float)((raw[u][t].x >> (4 * k)) & 15u), f.x, f.y);
+            for (int k = 0; k < 8; ++k) x[k] = __fmaf_rn(x[k], f.x, f.y);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kDequantThreads, kDequantCtas) dequant_kernel(
               x[2 * k + 1] = f.y * sc[u][t];
             }
           }
-          reinterpret_cast<uint4*>(t ? p.v_out : p.k_out)[out0 + e0 + u * kDequantThreads] = narrow_row<QK>(x);
+          __stcs((t ? vo : ko) + (size_t)(h0 + u * S) * G8, narrow_row<QK>(x));
         }
       }
     }
@@ -254,7 +256,8 @@ extern "C" pa_status pa_dequant_kv(const pa_config* cfg, const void* k_cache, co
   // a CTA for every few thousand values that there may be, as many as fit at once
   const double most = (double)c.batch * c.max_blocks_per_seq * c.block_size * c.num_kv_heads * c.head_dim;
   const double ctas = most / (8.0 * kDequantThreads) + 1;
-  const int grid = (int)(ctas < (double)sms * kDequantCtas ? ctas : (double)sms * kDequantCtas);
+  const int most_ctas = sms * dequant_ctas(store_kind(c));
+  const int grid = ctas < most_ctas ? (int)ctas : most_ctas;
   const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16, kind = store_kind(c);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -25,6 +25,27 @@ __device__ __forceinline__ float2 pair_values(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// The eight codes of a word as fp32: two at a time masked into the mantissas of 1024 (64) in f16.
+__device__ __forceinline__ void code_values(uint32_t w, float (&c)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t even, odd;
+    asm("{\n .reg .b32 t;\n lop3.b32 t, %1, 0x000f000f, %2, 0xea;\n sub.rn.f16x2 %0, t, %2;\n}"
+        : "=r"(even)
+        : "r"(w), "r"(0x64006400u));
+    asm("{\n .reg .b32 t;\n lop3.b32 t, %1, 0x00f000f0, %2, 0xea;\n sub.rn.f16x2 %0, t, %2;\n}"
+        : "=r"(odd)
+        : "r"(w), "r"(0x54005400u));
+    const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&even));
+    const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&odd));
+    c[2 * k] = e.x;
+    c[2 * k + 4] = e.y;
+    c[2 * k + 1] = o.x;
+    c[2 * k + 5] = o.y;
+    w >>= 8;
+  }
+}
+
 // The largest number of the pair's type that is <= x / the least that is >= x (bits).
 template <int QK>
 __device__ __forceinline__ uint16_t round_down(float x) {
@@ -55,15 +76,14 @@ __device__ __forceinline__ float quotient(float y, float s, float r) {
 // first element's in the lowest four bits) and the row's pair.
 template <int QK, int L>
 __device__ __forceinline__ uint32_t quantise_row(const float (&x)[8], uint32_t* pair) {
-  float lo = x[0], hi = x[0];
-  bool nan = false;
+  float lo = x[0], hi = x[0], zero = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     lo = fminf(lo, x[k]);
     hi = fmaxf(hi, x[k]);
-    nan |= x[k] != x[k];
+    zero = __fmaf_rn(x[k], 0.f, zero);
   }
-  lo = nan ? -INFINITY : lo;  // (a NaN's row has no finite range either)
+  lo = zero == 0.f ? lo : -INFINITY;  // (NaN or infinity: no finite range)
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
