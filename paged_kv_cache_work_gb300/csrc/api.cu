@@ -159,22 +159,6 @@ bool kv_tensor_map(CUtensorMap* m, const void* base, const pa_config& c, int box
   return r == CUDA_SUCCESS;
 }
 
-// Descriptor of a 4-bit cache's pairs [num_blocks, Hkv, block_size] (four bytes each) with a box of
-// one page's and head's.
-bool pair_tensor_map(CUtensorMap* m, const void* base, const pa_config& c, int box_rows) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)c.block_size, (cuuint64_t)c.num_kv_heads,
-                        (cuuint64_t)c.num_blocks, 1};
-  cuuint64_t strides[3] = {dims[0] * 4, dims[0] * dims[1] * 4, dims[0] * dims[1] * dims[2] * 4};
-  cuuint32_t box[4] = {(cuuint32_t)box_rows, 1, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  std::memset(m, 0, sizeof(*m));
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_64B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 extern "C" {
@@ -226,14 +210,10 @@ pa_status pa_decode(const pa_config* cfg, const void* q, const void* k_cache, co
 
   const int tile_rows = v.path == 4 ? int4_tile_tokens(cfg->head_dim, v.mp) : v.tt;
   const int box_rows = v.path == 3 ? 16 : cfg->block_size < tile_rows ? cfg->block_size : tile_rows;
-  CUtensorMap maps[4];
+  CUtensorMap maps[2];
   if (!kv_tensor_map(&maps[0], k_cache, *cfg, box_rows, v.path >= 1) ||
       !kv_tensor_map(&maps[1], v_cache, *cfg, box_rows, v.path >= 1))
     return PA_ERR_CUDA;
-  if (v.path == 4 && (!pair_tensor_map(&maps[2], k_scale, *cfg, box_rows) ||
-                      !pair_tensor_map(&maps[3], v_scale, *cfg, box_rows)))
-    return PA_ERR_CUDA;
-
   DecodeArgs a;
   a.p = problem_args(*cfg, block_tables, context_lens, q_lens);
   a.q = q;

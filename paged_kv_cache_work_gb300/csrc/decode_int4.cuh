@@ -2,8 +2,8 @@
 // chunks going to the warps of a CTA in turn, which attend on their own (int4_attention.cuh) and
 // merge at the item's end, as in the streaming decode over fp8 pages.
 //
-// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V) and of
-// their pairs, into a ring of the warp's own, with no barrier between warps while data streams.
+// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V), and
+// their pairs by a cp.async of a lane, into a ring of the warp's own, with no barrier between warps while data streams.
 #pragma once
 
 #include "int4_attention.cuh"
@@ -19,10 +19,7 @@ struct DecodeInt4Smem {
   static constexpr int NST = 3;                               // stages of a warp's ring
   static constexpr int TILE = TK * T::ROW;                    // bytes of a K (or V) tile
   static constexpr int STAGE = 2 * TILE;                      // (a multiple of its swizzle's period)
-  // A stage's pairs, K rows' before V rows': a box's begin on 128 bytes, as a tensor copy's
-  // destination has to, so those of 16-token boxes lie 128 bytes apart.
-  static constexpr int VPAIRS = SUB * 128;
-  static constexpr int PAIRS = 2 * VPAIRS;
+  static constexpr int PAIRS = 2 * TK * 4;                    // a stage's pairs, K rows' before V rows'
   static constexpr int RING = NW * NST * STAGE;
   static constexpr int STATES = NW * T::O_SLOT;
   static constexpr int OFF_ML = round_up(cmax(RING, STATES), 128);
@@ -34,8 +31,7 @@ struct DecodeInt4Smem {
   static constexpr int BYTES = OFF_PEND + 16 + 1024;  // (alignment)
   static constexpr int CT1 = 3, CT2 = 2;
   static constexpr int CTAS_PER_SM = T::D == 256 ? 2 : T::NT == 1 ? CT1 : CT2;
-  static_assert(OFF_PAIRS % 128 == 0 && PAIRS % 128 == 0 && 16 * T::ROW % 128 == 0 &&
-                    STAGE % (8 * T::ROW) == 0 && STAGE % 128 == 0,
+  static_assert(16 * T::ROW % 128 == 0 && STAGE % (8 * T::ROW) == 0 && STAGE % 128 == 0,
                 "a tensor copy's destination");
   static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "shared memory");
 };
@@ -43,9 +39,7 @@ struct DecodeInt4Smem {
 template <class T>
 __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>::CTAS_PER_SM)
     decode_int4_kernel(const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ CUtensorMap kpmap,
-                       const __grid_constant__ CUtensorMap vpmap, const KernelParams p) {
+                       const __grid_constant__ CUtensorMap vmap, const KernelParams p) {
   using M = DecodeInt4Smem<T>;
   constexpr int D = T::D, ROWS = T::ROWS, NW = M::NW, SUB = M::SUB, NST = M::NST;
   static_assert(NST == 3, "two tiles in flight");
@@ -61,17 +55,18 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
   float4* const factors = reinterpret_cast<float4*>(smem + M::OFF_FACTORS) + warp * M::TK;
   float2* const ml = reinterpret_cast<float2*>(smem + M::OFF_ML);  // [NW][ROWS] (max, sum)
   if (lane == 0) {  // (a warp's barriers are its own)
-    for (int s = 0; s < NST; ++s) mbar_init(&bar[s], SUB);
+    for (int s = 0; s < NST; ++s) mbar_init(&bar[s], SUB + 32);
     fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
-    tma_prefetch_desc(&kpmap);
-    tma_prefetch_desc(&vpmap);
   }
   __syncwarp();
   const int box = min(p.bs, M::TK);  // tokens of a box: a page's, or a tile's
-  const int t = lane % M::TK, pair_at = 4 * t + (box < M::TK && t >= 16 ? 64 : 0);  // a lane's token
-  const uint32_t box_bytes = 2u * (uint32_t)(box * (T::ROW + 4));
+  const int t = lane % M::TK;  // a lane's token
+  const uint32_t box_bytes = 2u * (uint32_t)(box * T::ROW);
+  // a lane's 16 bytes of pairs: K's or V's, chunk, four tokens
+  const uint32_t* const pair_from =
+      reinterpret_cast<const uint32_t*>(lane < 4 * SUB ? p.k_scale : p.v_scale) + 4 * (lane & 3);
   const int4 first = first_item_of(p, blockIdx.x, gridDim.x, lane);
   int it = 0, items = 1, list = 0;  // this CTA's items begin at p.items[list]
   int4 item_next = first;
@@ -127,22 +122,24 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
     auto issue = [&](int j, int s) {
       if (j >= my) return;
       if (SUB * j >= base + 32) look_up(SUB * j);
-      const int c = lane - (SUB * j - base);
+      const int lane0 = SUB * j - base, c = lane - lane0, tok = t0 + (warp + NW * j) * M::TK;
       if (c >= 0 && c < SUB) {
         if (blk >= 0 && (16 * c & (box - 1)) == 0) {
           mbar_arrive_expect_tx(&bar[s], box_bytes);
-          const int slot_in = (t0 + (warp + NW * j) * M::TK + 16 * c) & (p.bs - 1);
+          const int slot_in = (tok + 16 * c) & (p.bs - 1);
           char* const dst = ring + s * M::STAGE + c * 16 * T::ROW;
           tma_load_4d(dst, &kmap, &bar[s], 0, g, slot_in, blk);
           tma_load_4d(dst + M::TILE, &vmap, &bar[s], 0, g, slot_in, blk);
-          char* const to = pairs + s * M::PAIRS + c * 128;
-          tma_load_4d(to, &kpmap, &bar[s], slot_in, g, blk, 0);
-          tma_load_4d(to + M::VPAIRS, &vpmap, &bar[s], slot_in, g, blk, 0);
         } else {
           mbar_arrive(&bar[s]);
         }
       }
       __syncwarp();
+      const int cp = (lane >> 2) % SUB, bk = __shfl_sync(kFull, blk, lane0 + cp);
+      if (lane < 8 * SUB && bk >= 0)
+        cp_async_16(pairs + s * M::PAIRS + lane * 16,
+                    pair_from + ((((size_t)bk * p.Hkv + g) << p.bs_shift) + ((tok + 16 * cp) & (p.bs - 1))));
+      cp_async_arrive_noinc(&bar[s]);
     };
     if (my > 0) look_up(0);
     __syncwarp();
@@ -181,9 +178,8 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
       const int tok = t0 + (warp + NW * j) * M::TK;
       const uint32_t kt = smem_addr(ring + st * M::STAGE);
       // a lane a token: its factors
-      const char* const pair = pairs + st * M::PAIRS + pair_at;
-      const float2 kp = pair_values<T::QK>(*reinterpret_cast<const uint32_t*>(pair));
-      const float2 vp = pair_values<T::QK>(*reinterpret_cast<const uint32_t*>(pair + M::VPAIRS));
+      const uint32_t* const pair = reinterpret_cast<const uint32_t*>(pairs + st * M::PAIRS) + t;
+      const float2 kp = pair_values<T::QK>(pair[0]), vp = pair_values<T::QK>(pair[M::TK]);
       float4 f = make_float4(kp.x, __fmaf_rn(8.f, kp.x, kp.y), vp.x, __fmaf_rn(8.f, vp.x, vp.y));
       const float unit = att.vref;
       const bool fits = fabsf(vp.x) <= unit && fabsf(vp.x) >= unit * kVRange;
@@ -263,7 +259,7 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
 }
 
 template <int D, int NT, int QK>
-cudaError_t launch_int4_instance(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid,
+cudaError_t launch_int4_instance(const KernelParams& prm, const CUtensorMap (&maps)[2], int grid,
                                  cudaStream_t s) {
   using T = Int4Attention<D, NT, QK>;
   using M = DecodeInt4Smem<T>;
@@ -281,12 +277,12 @@ cudaError_t launch_int4_instance(const KernelParams& prm, const CUtensorMap (&ma
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], prm);
+  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], prm);
 }
 
 // Both row tiles of a head dim.
 template <int D>
-cudaError_t launch_int4_dim(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid, int mp,
+cudaError_t launch_int4_dim(const KernelParams& prm, const CUtensorMap (&maps)[2], int grid, int mp,
                             int qk, cudaStream_t s) {
   if (mp == 8)
     return qk == Q_BF16 ? launch_int4_instance<D, 1, Q_BF16>(prm, maps, grid, s)

@@ -3,7 +3,7 @@
 
 namespace pa {
 
-cudaError_t launch_int4_d64(const KernelParams& prm, const CUtensorMap (&maps)[4], int grid, int mp,
+cudaError_t launch_int4_d64(const KernelParams& prm, const CUtensorMap (&maps)[2], int grid, int mp,
                            int qk, cudaStream_t s) {
   return launch_int4_dim<64>(prm, maps, grid, mp, qk, s);
 }

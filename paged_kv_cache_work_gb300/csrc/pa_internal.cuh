@@ -328,9 +328,8 @@ struct DecodeArgs {
   int q_kind, kv_kind;
 };
 
-// maps: of the K and V caches and, for a 4-bit cache, of their pairs.  Returns cudaErrorNotSupported
-// when no kernel instance matches.
-cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t s);
+// maps: of the K and V caches.  Returns cudaErrorNotSupported when no kernel instance matches.
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[2], cudaStream_t s);
 
 cudaError_t launch_reduce(const DecodeArgs& a, cudaStream_t s);
 

@@ -32,9 +32,9 @@ cudaError_t launch_tc_fp8_block_d128(const KernelParams&, const CUtensorMap&, co
 
 cudaError_t launch_stream(const KernelParams&, const CUtensorMap&, const CUtensorMap&, int, int, int,
                           cudaStream_t);
-cudaError_t launch_int4_d64(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
-cudaError_t launch_int4_d128(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
-cudaError_t launch_int4_d256(const KernelParams&, const CUtensorMap (&)[4], int, int, int, cudaStream_t);
+cudaError_t launch_int4_d64(const KernelParams&, const CUtensorMap (&)[2], int, int, int, cudaStream_t);
+cudaError_t launch_int4_d128(const KernelParams&, const CUtensorMap (&)[2], int, int, int, cudaStream_t);
+cudaError_t launch_int4_d256(const KernelParams&, const CUtensorMap (&)[2], int, int, int, cudaStream_t);
 int int4_ctas_per_sm_d64(int);
 int int4_ctas_per_sm_d128(int);
 int int4_ctas_per_sm_d256(int);
@@ -109,7 +109,7 @@ KernelParams make_kernel_params(const DecodeArgs& a) {
   return p;
 }
 
-cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t s) {
+cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap (&maps)[2], cudaStream_t s) {
   const CUtensorMap &kmap = maps[0], &vmap = maps[1];
   const KernelParams prm = make_kernel_params(a);
   const int scales = staged_scales(a.scale_mode);
