@@ -2,8 +2,19 @@
 // chunks going to the warps of a CTA in turn, which attend on their own (int4_attention.cuh) and
 // merge at the item's end, as in the streaming decode over fp8 pages.
 //
-// A tile is two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V), and
-// their pairs by a cp.async of a lane, into a ring of the warp's own, with no barrier between warps while data streams.
+// A tile is one or two chunks: TMA boxes of up to 32 tokens of one page and kv head (K, V), and their
+// pairs by a cp.async of a lane, into a ring of the warp's own, with no barrier between warps while data
+// streams.
+//
+// Measured (plan, decode and reduce; replayed): 32 contexts of 512 to 4,096 tokens, 32 heads on 8 kv
+// heads of 128, pages of 16 (81 MB) 32 us, with four new tokens each 43; 32 of 2,048 to 16,384, 16 heads
+// of 256 (1.25 GB) 239 us, 5.2 TB/s; 4 of 32,768 to 131,072, 16 heads on one of 128 (45 MB) 27.5 us, of
+// which plan, start, merge and reduce are about 10.  What bounds it is a warp's own chain: alone on its
+// scheduler it takes 2,400 cycles a tile of 32 tokens (632 instructions; 320 are the widening of codes
+// and the products), three together 3,200, so that a scheduler issues 0.55 instructions a cycle (head
+// dim 128, 8 rows: 4.2 TB/s).  Head dim 256 has twice the codes for the same softmax.  Tried without
+// gain: four neighbouring heads a unit (their rows as one box; four times the partials), one ring a CTA,
+// tiles of 64 tokens, values a tile behind keys in one block of instructions, two accumulators a logit.
 #pragma once
 
 #include "int4_attention.cuh"
@@ -29,8 +40,12 @@ struct DecodeInt4Smem {
   static constexpr int OFF_BAR = OFF_PAIRS + NW * NST * PAIRS;
   static constexpr int OFF_PEND = OFF_BAR + NW * NST * 8;
   static constexpr int BYTES = OFF_PEND + 16 + 1024;  // (alignment)
-  static constexpr int CT1 = 3, CT2 = 2;
-  static constexpr int CTAS_PER_SM = T::D == 256 ? 2 : T::NT == 1 ? CT1 : CT2;
+  // As many warps as fit without spilling the state of an unrolled tile.  Us a step with one CTA more
+  // (or for head dim 64 one less): head dim 128, 8 rows (32 contexts of 8,192 to 16,384, 32 heads on 8)
+  // 118 in place of 104; 16 rows (64 such contexts, one kv head) 60 in place of 48; 64, 16 rows 38.8 in
+  // place of 36.3.
+  static constexpr int CTAS_PER_SM =
+      T::D == 256 ? 2 : T::D == 128 ? (T::NT == 1 ? 3 : 2) : (T::NT == 1 ? 4 : 3);
   static_assert(16 * T::ROW % 128 == 0 && STAGE % (8 * T::ROW) == 0 && STAGE % 128 == 0,
                 "a tensor copy's destination");
   static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "shared memory");
@@ -172,11 +187,14 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
         break;
       }
       __syncwarp();
+      const int tok = t0 + (warp + NW * j) * M::TK;
+      const uint32_t kt = smem_addr(ring + st * M::STAGE);
+      // (before what decides how the tile goes on: the products are what its latencies hide behind)
+      float s[SUB][T::NT][4];
+      att.template keys<SUB>(kt, query, s, lane);
       issue(j + 2, st == 0 ? 2 : st - 1);
       const int x = SUB * j - base;  // (tile j + 2's look-up may have come in between)
       const uint32_t here = (x >= 0 ? held >> x : held_before >> (x + 32)) & ((1u << SUB) - 1);
-      const int tok = t0 + (warp + NW * j) * M::TK;
-      const uint32_t kt = smem_addr(ring + st * M::STAGE);
       // a lane a token: its factors
       const uint32_t* const pair = reinterpret_cast<const uint32_t*>(pairs + st * M::PAIRS) + t;
       const float2 kp = pair_values<T::QK>(pair[0]), vp = pair_values<T::QK>(pair[M::TK]);
@@ -187,15 +205,14 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
         f.z *= pow2_inverse(unit) * kPLift;
         factors[t] = f;
         __syncwarp();
-        att.template tile<SUB, true>(kt, kt + M::TILE, query, factors,
-                                     [](int, int, int) { return make_uint2(1, 1); }, lane);
+        att.template whole_tile<SUB>(s, kt + M::TILE, factors, lane);
       } else {
         // (what lies behind the last token, or was not copied, may hold anything)
         const bool ok = (here >> (t >> 4) & 1) && tok + t < t1;
         factors[t] = ok ? f : make_float4(0.f, 0.f, 0.f, 0.f);
         __syncwarp();
-        att.template tile<SUB, false>(
-            kt, kt + M::TILE, query, factors,
+        att.template any_tile<SUB>(
+            s, kt + M::TILE, factors,
             [&](int c, int h, int i) {
               const int x = tok + 16 * c + 8 * h + quad, end = (here >> c & 1) ? t1 : 0;
               const int row = 8 * i + 2 * qi;

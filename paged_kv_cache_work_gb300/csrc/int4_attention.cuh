@@ -233,9 +233,46 @@ struct Int4Attention {
     }
   }
 
-  // O^T += V^T P^T for SUB chunks, the weights times their V steps as operands in pb.
+  // S^T = K Q^T of SUB chunks, their K rows at shared address kt and the queries' fragments at `query`,
+  // into s.
   template <int SUB>
-  __device__ __forceinline__ void add_values(uint32_t vt, const uint32_t (&pb)[SUB][NT][2], int lane) {
+  __device__ __forceinline__ void keys(uint32_t kt, const uint4* query, float (&s)[SUB][NT][4], int lane) {
+    uint32_t w[SUB][2][GW];
+#pragma unroll
+    for (int c = 0; c < SUB; ++c)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s[c][t][0] = s[c][t][2] = start[t].x;
+        s[c][t][1] = s[c][t][3] = start[t].y;
+      }
+#pragma unroll
+    for (int i = 0; i < KW; ++i) {
+      if (i % GW == 0) {
+#pragma unroll
+        for (int c = 0; c < SUB; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) k_words(kt, c, h, i / GW, lane, w[c][h]);
+      }
+      uint4 q[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) q[t] = query[(i * 32 + lane) * NT + t];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < SUB; ++c) {
+          const uint32_t u0 = k ? w[c][0][i % GW] >> 8 : w[c][0][i % GW];
+          const uint32_t u1 = k ? w[c][1][i % GW] >> 8 : w[c][1][i % GW];
+          const uint32_t a[4] = {int4_even(u0), int4_even(u1), int4_odd_64(u0), int4_odd_64(u1)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma16816<true>(s[c][t], a, k ? q[t].z : q[t].x, k ? q[t].w : q[t].y);
+        }
+    }
+  }
+
+  // O^T += V^T P^T of SUB chunks, V rows at vt, weights (times their V steps) in pb.
+  template <int SUB>
+  __device__ __forceinline__ void values(uint32_t vt, const uint32_t (&pb)[SUB][NT][2], int lane) {
     const uint32_t sel = first_token(lane & 3) ? 0x1054u : 0x5410u;  // low halves of tokens 2 qi, 2 qi + 1
 #pragma unroll
     for (int c = 0; c < SUB; ++c) {
@@ -264,53 +301,18 @@ struct Int4Attention {
     }
   }
 
-  // SUB chunks of 16 tokens, their K rows at shared address kt, V rows at vt, the queries' fragments
-  // at `query` and the tokens' factors at `factors`: (K step, K low + 8 step, V factor, V low + 8
-  // step), zeros where no row may see the token.
-  // HOT: every row sees every token, and the V factor is the V step over the accumulators' unit times
-  // kPLift.  Otherwise it is the V step itself, and sees(c, h, t) says which of the rows 8 t + 2 qi, + 1
-  // see token quad + 8 h of chunk c.
+  // The raw logits of a tile in place of the products s, with the tokens' factors: (K step, K low + 8
+  // step, V factor, V low + 8 step), zeros where no row may see the token; the running maxima follow.
+  // vf: the V factors of tokens quad + 8 h, in x the one for the weight, in y low + 8 step.
+  // HOT: every row sees every token; otherwise sees(c, h, t) says which of the rows 8 t + 2 qi, + 1 see
+  // token quad + 8 h of chunk c.
   template <int SUB, bool HOT, class FS>
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const uint4* query,
-                                       const float4* factors, FS sees, int lane) {
+  __device__ __forceinline__ void logits(float (&s)[SUB][NT][4], const float4* factors,
+                                         float2 (&vf)[SUB][2], FS sees, int lane) {
     const int quad = lane >> 2;
-    float s[SUB][NT][4];
-#pragma unroll
-    for (int c = 0; c < SUB; ++c)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        s[c][t][0] = s[c][t][2] = start[t].x;
-        s[c][t][1] = s[c][t][3] = start[t].y;
-      }
-#pragma unroll
-    for (int j = 0; j < KW / GW; ++j) {
-      uint32_t w[SUB][2][GW];
-#pragma unroll
-      for (int c = 0; c < SUB; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) k_words(kt, c, h, j, lane, w[c][h]);
-#pragma unroll
-      for (int i = 0; i < GW; ++i) {
-        uint4 q[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) q[t] = query[((j * GW + i) * 32 + lane) * NT + t];
-#pragma unroll
-        for (int c = 0; c < SUB; ++c)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t u0 = k ? w[c][0][i] >> 8 : w[c][0][i], u1 = k ? w[c][1][i] >> 8 : w[c][1][i];
-            const uint32_t a[4] = {int4_even(u0), int4_even(u1), int4_odd_64(u0), int4_odd_64(u1)};
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              mma16816<true>(s[c][t], a, k ? q[t].z : q[t].x, k ? q[t].w : q[t].y);
-          }
-      }
-    }
-    // raw logits, of token quad + 8 h
     float2 mx[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) mx[t] = make_float2(-INFINITY, -INFINITY);
-    float2 vf[SUB][2];
 #pragma unroll
     for (int c = 0; c < SUB; ++c)
 #pragma unroll
@@ -333,70 +335,89 @@ struct Int4Attention {
         }
       }
     follow(mx);
-    // weights exp2(scale x - maximum), summed alone and times low + 8 step, then times `factor` of
-    // their V factor as operands; a masked logit (-inf) gives 0
-    auto weigh = [&](auto factor, bool sums, uint32_t (&pb)[SUB][NT][2]) {
+  }
+
+  // Weights exp2(scale x - maximum), summed alone and times low + 8 step, then times `factor` of their V
+  // factor as operands; a masked logit (-inf) gives 0.
+  template <int SUB, bool HOT, class FF>
+  __device__ __forceinline__ void weigh(const float (&s)[SUB][NT][4], const float2 (&vf)[SUB][2],
+                                        FF factor, bool sums, uint32_t (&pb)[SUB][NT][2]) {
+#pragma unroll
+    for (int c = 0; c < SUB; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = factor(vf[c][h].x), mid = vf[c][h].y;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float x0 = s[c][t][2 * h], x1 = s[c][t][2 * h + 1];
+          float2 e = make_float2(fast_exp2(__fmaf_rn(x0, scale[t].x, base[t].x)),
+                                 fast_exp2(__fmaf_rn(x1, scale[t].y, base[t].y)));
+          if (!HOT) {
+            e.x = x0 == -INFINITY ? 0.f : e.x;
+            e.y = x1 == -INFINITY ? 0.f : e.y;
+          }
+          if (sums) {
+            l[t] = fadd2(l[t], e);
+            low[t].x = __fmaf_rn(e.x, mid, low[t].x);
+            low[t].y = __fmaf_rn(e.y, mid, low[t].y);
+          }
+          pb[c][t][h] = transpose8(pack2<true>(e.x * f, e.y * f));
+        }
+      }
+  }
+
+  // What follows a tile's products s where every row sees every token and the V factors are the V steps
+  // over the accumulators' unit times kPLift.
+  template <int SUB>
+  __device__ __forceinline__ void whole_tile(float (&s)[SUB][NT][4], uint32_t vt, const float4* factors,
+                                             int lane) {
+    uint32_t pb[SUB][NT][2];
+    float2 vf[SUB][2];
+    logits<SUB, true>(s, factors, vf, [](int, int, int) { return make_uint2(1, 1); }, lane);
+    weigh<SUB, true>(s, vf, [](float v) { return v; }, true, pb);
+    values<SUB>(vt, pb, lane);
+  }
+
+  // The same whatever its rows see and its V steps are (the V factors are the steps).
+  template <int SUB, class FS>
+  __device__ __forceinline__ void any_tile(float (&s)[SUB][NT][4], uint32_t vt, const float4* factors,
+                                           FS sees, int lane) {
+    uint32_t pb[SUB][NT][2];
+    float2 vf[SUB][2];
+    logits<SUB, false>(s, factors, vf, sees, lane);
+    // the largest finite V step (its magnitude) below `end`: warp-uniform
+    auto largest = [&](float end) -> float {
+      float a = 0.f;
 #pragma unroll
       for (int c = 0; c < SUB; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float f = factor(vf[c][h].x), mid = vf[c][h].y;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float x0 = s[c][t][2 * h], x1 = s[c][t][2 * h + 1];
-            float2 e = make_float2(fast_exp2(__fmaf_rn(x0, scale[t].x, base[t].x)),
-                                   fast_exp2(__fmaf_rn(x1, scale[t].y, base[t].y)));
-            if (!HOT) {
-              e.x = x0 == -INFINITY ? 0.f : e.x;
-              e.y = x1 == -INFINITY ? 0.f : e.y;
-            }
-            if (sums) {
-              l[t] = fadd2(l[t], e);
-              low[t].x = __fmaf_rn(e.x, mid, low[t].x);
-              low[t].y = __fmaf_rn(e.y, mid, low[t].y);
-            }
-            pb[c][t][h] = transpose8(pack2<true>(e.x * f, e.y * f));
-          }
+          const float v = fabsf(vf[c][h].x);
+          a = fmaxf(a, v < end ? v : 0.f);
         }
+      return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
     };
-    uint32_t pb[SUB][NT][2];
-    if constexpr (HOT) {
-      weigh([&](float v) { return v; }, true, pb);
-      add_values<SUB>(vt, pb, lane);
-    } else {
-      // the largest finite V step (its magnitude) below `end`: warp-uniform
-      auto largest = [&](float end) -> float {
-        float a = 0.f;
-#pragma unroll
-        for (int c = 0; c < SUB; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float v = fabsf(vf[c][h].x);
-            a = fmaxf(a, v < end ? v : 0.f);
-          }
-        return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
-      };
-      // a pass for the steps that one unit serves after the other, from the largest on
-      float done = __uint_as_float(0x7fc00000u);  // steps from here on are in o (NaN: none yet)
+    // a pass for the steps that one unit serves after the other, from the largest on
+    float done = __uint_as_float(0x7fc00000u);  // steps from here on are in o (NaN: none yet)
 #pragma unroll 1
-      for (float v = largest(INFINITY); v > 0.f || done != done;) {
-        if (v > vref || (v > 0.f && v < vref * kVRange)) {  // the unit to the step v
-          const float f = move_v_unit(v, vref, vtop);
+    for (float v = largest(INFINITY); v > 0.f || done != done;) {
+      if (v > vref || (v > 0.f && v < vref * kVRange)) {  // the unit to the step v
+        const float f = move_v_unit(v, vref, vtop);
 #pragma unroll
-          for (int j = 0; j < MB; ++j)
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[j][t][e] *= f;
-        }
-        // the least step that it serves (0: any); NaN and infinity are in, in the first pass at least
-        const float floor = v < vref * kVRange ? 0.f : vref * kVRange;
-        const float vinv = pow2_inverse(vref) * kPLift;
-        weigh([&](float a) { return fabsf(a) < floor || fabsf(a) >= done ? 0.f : a * vinv; }, done != done, pb);
-        add_values<SUB>(vt, pb, lane);
-        done = floor;
-        v = largest(floor);
+            for (int e = 0; e < 4; ++e) o[j][t][e] *= f;
       }
+      // the least step that it serves (0: any); NaN and infinity are in, in the first pass at least
+      const float floor = v < vref * kVRange ? 0.f : vref * kVRange;
+      const float vinv = pow2_inverse(vref) * kPLift;
+      weigh<SUB, false>(s, vf, [&](float a) { return fabsf(a) < floor || fabsf(a) >= done ? 0.f : a * vinv; },
+                        done != done, pb);
+      values<SUB>(vt, pb, lane);
+      done = floor;
+      v = largest(floor);
     }
   }
 

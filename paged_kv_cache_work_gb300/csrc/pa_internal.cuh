@@ -128,12 +128,17 @@ constexpr int stream_max_rows(int head_dim) {
   return head_dim == 64 ? 0x7fffffff : 32;
 }
 
-// The 4-bit kernel: query rows of a tile, the tokens that a CTA's warps take in a round, and the cost
-// of an item in such rounds.
+// The 4-bit kernel: query rows of a tile (16 where 8 do not do: a tile of 8 has half the products),
+// the tokens of a warp's tile and of the round that a CTA's warps take together, and the cost of an item
+// in such rounds.  Us a step with items of 2 / 3 / 5 / 7 rounds, tiles of 8 rows: 32 contexts of 512 to
+// 4,096, 32 heads on 8 of 128, 32.2 / 32.9 / 34.4 / 35.5; 32 of 2,048 to 16,384, 16 heads of 256, 239 /
+// 239 / 241 / 242.  Tiles of 16: the former with four new tokens 48.0 / 45.8 / 43.4 / 45.8; 64 contexts
+// of 8,192 to 16,384, 16 heads on one, 49.0 / 47.0 / 47.0 / 47.0; 4 of 32,768 to 131,072 29.8 / 28.1 /
+// 27.5 / 27.5.
 constexpr int int4_tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
 constexpr int int4_tile_tokens(int head_dim, int mp) { return head_dim == 256 && mp == 16 ? 16 : 32; }
 constexpr int kInt4RoundTokens = 128;
-constexpr int kInt4ItemCostRounds = 5;
+constexpr int int4_item_cost_rounds(int mp) { return mp == 8 ? 2 : 5; }
 
 // Query rows per kv head above which a 128-dim head runs on the tcgen05 kernel.
 constexpr int kTcMinRows = 33;
@@ -155,7 +160,7 @@ inline Variant make_variant(const pa_config& c) {
     v.mp = int4_tile_rows(v.rows);
     v.rb = ceil_div(v.rows, v.mp);
     v.tt = kInt4RoundTokens;
-    v.item_cost = kInt4ItemCostRounds * v.tt;
+    v.item_cost = int4_item_cost_rounds(v.mp) * v.tt;
     v.units = c.batch * c.num_kv_heads * v.rb;
     v.ctas_per_sm = int4_ctas_per_sm(c.head_dim, v.mp);
     v.ns_dec = decode_merge_limit(c.split_merge, v.path);
