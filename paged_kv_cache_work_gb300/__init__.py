@@ -396,30 +396,20 @@ def decode_selected(cfg: PaConfig, q, k_cache, v_cache, k_scale, v_scale, block_
         _maybe(name, dev, 1, flags, i32), _stream(stream)))
 
 
-def _token_stride(call: str, t, rows: int, heads: int, dim: int) -> int:
-    """Elements between the tokens of [B, Sq, heads, dim] rows, each token's dense (0 for an address:
-    the rows lie dense)."""
-    if isinstance(t, int):
-        return 0
-    shape, stride = tuple(t.shape), t.stride()
-    if len(shape) != 4 or shape[0] * shape[1] < rows or shape[2:] != (heads, dim) or stride[3] != 1 \
-            or (heads > 1 and stride[2] != dim):
-        raise PaError(call, ERR_INVALID_ARG)
-    step = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else heads * dim
-    if shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * step:
-        raise PaError(call, ERR_INVALID_ARG)
-    return step
-
-
-def _rows(call: str, device: int, t, dtypes) -> int:
-    """Address of rows that need not lie dense (_token_stride looks at how they lie)."""
-    if isinstance(t, int):
-        return t
+def _rows(call: str, device: int, tokens: int, heads: int, dim: int, t, dtypes):
+    """(address, elements between tokens) of rows [B, Sq, heads, dim] that lie dense within a token
+    (an address passes as it is, with 0: dense)."""
     try:
-        if t.dtype in dtypes and t.get_device() == device:
-            return t.data_ptr()
+        shape, stride = t.shape, t.stride()
+        if t.dtype in dtypes and t.get_device() == device and len(shape) == 4 and stride[3] == 1 \
+                and shape[3] == dim and shape[2] == heads and (stride[2] == dim or heads == 1):
+            b, sq = shape[0], shape[1]
+            step = stride[1] if sq > 1 else stride[0] if b > 1 else 0
+            if b * sq >= tokens and (b == 1 or sq == 1 or stride[0] == sq * step):
+                return t.data_ptr(), step
     except AttributeError:
-        pass
+        if isinstance(t, int):
+            return t, 0
     raise PaError(call, ERR_INVALID_ARG)
 
 
@@ -434,39 +424,41 @@ def append_rotated(cfg: PaConfig, q, k_new, v_new, block_tables, context_lens, q
     rotated pairs follow each axis.  With k_cache and v_cache None nothing goes into pages."""
     dev, i32, _, f32, kinds = _types()
     name, B, D = "pa_append_rotated", cfg.batch, cfg.head_dim
-    kind, cache_kind = kinds.get(cfg.q_dtype, ()), kinds.get(cfg.kv_dtype, ())
-    tokens, hq, hkv = B * cfg.max_q_len, cfg.num_q_heads, cfg.num_kv_heads
-    r = PaRotary(eps=eps, interleaved=int(interleaved))
-    r.q_weight = _maybe(name, dev, D, q_weight, kind)
-    r.k_weight = _maybe(name, dev, D, k_weight, kind)
+    kind, hq, hkv = kinds.get(cfg.q_dtype, ()), cfg.num_q_heads, cfg.num_kv_heads
+    tokens = B * cfg.max_q_len
+    table, rows, turned, where, axes, pairs = None, 0, 0, None, 0, (0, 0, 0)
     if cos_sin is not None:
-        if len(getattr(cos_sin, "shape", ())) != 2:
+        shape = getattr(cos_sin, "shape", ())
+        if len(shape) != 2:
             raise PaError(name, ERR_INVALID_ARG)
-        r.table_rows, r.rotary_dim = cos_sin.shape
-        r.cos_sin = _dense(name, dev, r.table_rows * r.rotary_dim, cos_sin, f32)
-        pairs = list(axis_pairs) if axis_pairs is not None else [r.rotary_dim // 2]
-        if not 1 <= len(pairs) <= 3:
+        rows, turned = shape
+        table = _dense(name, dev, rows * turned, cos_sin, f32)
+        pairs = (turned // 2,) if axis_pairs is None else tuple(axis_pairs)
+        axes = len(pairs)
+        if not 1 <= axes <= 3:
             raise PaError(name, ERR_INVALID_ARG)
-        r.num_axes = len(pairs)
-        r.axis_pairs[:len(pairs)] = pairs
-        r.positions = _maybe(name, dev, len(pairs) * tokens, positions, i32)
-    r.q_stride = _token_stride(name, q, tokens, hq, D)
-    r.k_stride = _token_stride(name, k_new, tokens, hkv, D)
-    stores = k_cache is not None or v_cache is not None
-    pages = scales = (None, None)
-    vp = table = None
-    if stores:
-        r.v_stride = _token_stride(name, v_new, tokens, hkv, D)
-        vp = _rows(name, dev, v_new, kind)
-        table = _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32)
-        cache = _cache_elements(cfg)
-        pages = tuple(_dense(name, dev, cache, t, cache_kind) for t in (k_cache, v_cache))
-        scales = tuple(_scale(name, dev, cfg, t, f32) for t in (k_scale, v_scale))
+        pairs += (0,) * (3 - axes)
+        if positions is not None:
+            where = _dense(name, dev, axes * tokens, positions, i32)
+    qp, qs = _rows(name, dev, tokens, hq, D, q, kind)
+    kp, ks = _rows(name, dev, tokens, hkv, D, k_new, kind)
+    vp = vs = blocks = kc = vc = k_sc = v_sc = None
+    if k_cache is not None or v_cache is not None:
+        cache_kind, cache = kinds.get(cfg.kv_dtype, ()), _cache_elements(cfg)
+        vp, vs = _rows(name, dev, tokens, hkv, D, v_new, kind)
+        blocks = _dense(name, dev, B * cfg.max_blocks_per_seq, block_tables, i32)
+        kc, vc = _dense(name, dev, cache, k_cache, cache_kind), _dense(name, dev, cache, v_cache, cache_kind)
+        if cfg.kv_scale_mode != SCALE_NONE:
+            k_sc, v_sc = _scale(name, dev, cfg, k_scale, f32), _scale(name, dev, cfg, v_scale, f32)
+    rotary = PaRotary(
+        None if q_weight is None else _dense(name, dev, D, q_weight, kind),
+        None if k_weight is None else _dense(name, dev, D, k_weight, kind), eps, turned,
+        1 if interleaved else 0, table, rows, where, axes, pairs, qs, ks, vs or 0)
     _check(name, load().pa_append_rotated(
-        ctypes.byref(cfg), ctypes.byref(r), _rows(name, dev, q, kind), _rows(name, dev, k_new, kind),
-        vp, table, _dense(name, dev, B, context_lens, i32), _dense(name, dev, B, q_lens, i32),
-        _dense(name, dev, tokens * hq * D, q_out, kind), _maybe(name, dev, tokens * hkv * D, k_out, kind),
-        *pages, *scales, _maybe(name, dev, 1, flags, i32), _stream(stream)))
+        ctypes.byref(cfg), ctypes.byref(rotary), qp, kp, vp, blocks, _dense(name, dev, B, context_lens, i32),
+        _dense(name, dev, B, q_lens, i32), _dense(name, dev, tokens * hq * D, q_out, kind),
+        None if k_out is None else _dense(name, dev, tokens * hkv * D, k_out, kind), kc, vc, k_sc, v_sc,
+        None if flags is None else _dense(name, dev, 1, flags, i32), _stream(stream)))
 
 
 def dequant_kv(cfg: PaConfig, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, k_out,
