@@ -242,6 +242,56 @@ def test_flags(cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,sq,hq,hkv,d", [(1, 1, 1, 1, 64), (1, 2000, 9, 3, 128), (700, 1, 7, 7, 64), (2, 1500, 2, 1, 256)])
+@pytest.mark.parametrize("kv", ["16", "4"])
+def test_every_split_of_a_tokens_rows(B, sq, hq, hkv, d, kv, cuda_device, pa):
+    """Few tokens and many (a token's rows on many warps or one), odd head counts: queries and keys
+    against fp32 torch, and pages as the append writes them."""
+    rng = np.random.default_rng(9)
+    t, dev, bs = torch.bfloat16, cuda_device, 64
+    ql = rng.integers(0, sq + 1, B)
+    ql[0] = sq
+    ctx = ql + rng.integers(0, 100, B)
+    bt, nblocks = plain.tables(rng, ctx, bs)
+    cfg = config(B, sq, hq, hkv, d, bs, bt.shape[1], nblocks, "bf16", kv)
+    g = torch.Generator(device=dev).manual_seed(1)
+    x = torch.randn((B, sq, hq + 2 * hkv, d), generator=g, device=dev).to(t)
+    q, k, v = x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
+    w = (1 + 0.2 * torch.randn(d, generator=g, device=dev)).to(t)
+    cs = angles(int(ctx.max()) + 1, d).to(dev)
+    byte = kv == "4"
+    shape = (nblocks, bs, hkv, d // 2 if byte else d)
+    fresh = lambda: (torch.zeros(shape, dtype=torch.uint8 if byte else t, device=dev),  # noqa: E731
+                     torch.zeros((nblocks, hkv, bs, 2), dtype=t, device=dev) if byte else None)
+    (kc, ks), (vc, vs), (rk, rks), (rv, rvs) = (fresh() for _ in range(4))
+    qo, ko = torch.zeros(B, sq, hq, d, dtype=t, device=dev), torch.zeros(B, sq, hkv, d, dtype=t, device=dev)
+    args, flags = (ints(bt, dev), ints(ctx, dev), ints(ql, dev)), ints([0], dev)
+    pa.append_rotated(cfg, q, k, v, *args, qo, kc, vc, ks, vs, cos_sin=cs, q_weight=w, k_weight=w, k_out=ko, flags=flags)
+    assert int(flags.item()) == 0
+    i = torch.arange(sq, device=dev)
+    real = i < args[2][:, None]
+    pos = ((args[1] - args[2])[:, None] + i).clamp(max=cs.shape[0] - 1)
+    c, s = (a[:, :, None].double() for a in cs[pos].chunk(2, -1))
+
+    def turned(y):
+        y = y.double()
+        y = y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6) * w.double()
+        a, b = y.chunk(2, -1)
+        z = torch.cat((a * c - b * s, b * c + a * s), -1)
+        return z, torch.cat((a.abs() + b.abs(),) * 2, -1)
+
+    for got, src in ((qo, q), (ko, k)):
+        z, size = turned(src)
+        tol = 2.0 ** -8 * z.abs() + FP32 * size * 1.01
+        ok = (got.double() - z).abs() <= tol * (1 + 2.0 ** -9)
+        assert bool((ok | ~real[..., None, None]).all()) and bool((got[~real] == 0).all())
+    # the pages: values as the append writes them, keys (16 bits) as k_out has them
+    pa.append_kv(cfg, ko, v.contiguous(), *args, rk, rv, rks, rvs)
+    assert torch.equal(vc, rv) and (vs is None or torch.equal(vs, rvs))
+    assert byte or torch.equal(kc, rk)
+
+
+@pytest.mark.gpu
 def test_replays_in_a_graph(cuda_device, pa):
     p = Problem(8, 3, 2, 8, 2, 128, 16, "bf16", "8token", 128, 1, False, "both", True)
     want = {n: t.clone() for n, t in p.call(cuda_device).items() if n in ("qo", "kc", "vc", "ks")}

@@ -306,6 +306,48 @@ def test_decode_large_and_small_queries(size, cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sm_scale", [0.0, -0.11, 1e-30])
+def test_decode_any_logit_scale(sm_scale, cuda_device, pa):
+    """Zero weighs all seen keys alike; a negative one favours the smallest products."""
+    p = problem(14, 2, 3, 12, 2, 128, 16, (90, 33), (3, 2))
+    cfg = config(2, 3, 12, 2, 128, 16, p["bt"].shape[1], p["nblocks"], causal=1)
+    cfg.sm_scale = sm_scale
+    out, lse = run(p, cfg, cuda_device)
+    clean = [torch.nan_to_num(s, nan=0.0) for s in (p["ks"], p["vs"])]
+    k, v = plain.values(p["kc"], clean[0]), plain.values(p["vc"], clean[1])
+    pair = clean[1].double().numpy().transpose(0, 2, 1, 3)
+    mid = pair[..., 1:] + 8 * pair[..., :1]
+    ref = plain.attend(p["q"], k, v, np.abs(v - mid) + np.abs(mid), p["bt"], p["ctx"], p["ql"], 1,
+                       float(np.float32(sm_scale)), p["nblocks"])
+    check(out, lse, *ref, "bf16")
+
+
+@pytest.mark.gpu
+def test_decode_rows_apart(cuda_device, pa):
+    """A NaN or infinite query element reaches its own row alone, padding rows among its tile's."""
+    p = problem(15, 2, 4, 4, 1, 64, 16, (100, 40), (4, 1))
+    p["q"][0, 1, 2, 5], p["q"][0, 2, 0, 60] = float("nan"), float("inf")
+    p["q"][1, 1:] = float("nan")  # (rows behind the sequence's last)
+    cfg = config(2, 4, 4, 1, 64, 16, p["bt"].shape[1], p["nblocks"], causal=1)
+    out, _ = run(p, cfg, cuda_device)
+    bad = torch.isnan(out.float()).any(-1)
+    assert bad[0, 1, 2] and bad[0, 2, 0] and int(bad.sum()) == 2
+    assert (out[1, 1:] == 0).all()
+
+
+@pytest.mark.gpu
+def test_pages_shared_by_sequences(cuda_device, pa):
+    """A common prefix: the same pages in several tables."""
+    p = problem(16, 3, 1, 8, 2, 128, 16, (200, 200, 200), (1, 1, 1))
+    p["bt"][1, :12], p["bt"][2, :12] = p["bt"][0, :12], p["bt"][0, :12]
+    p["q"][1:] = p["q"][:1]
+    p["bt"][1] = p["bt"][0]
+    cfg = config(3, 1, 8, 2, 128, 16, p["bt"].shape[1], p["nblocks"])
+    out, lse = run(p, cfg, cuda_device)
+    check(out, lse, *reference(p, 0, 128), "bf16")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_decode_bad_blocks_and_lengths(d, cuda_device, pa):
     """A page outside the pool holds no keys; a bad length stops the step."""
@@ -404,6 +446,70 @@ def test_append_then_decode_then_read(d, bs, dtype, cuda_device, pa):
         v = plain.values(codes[j], pairs[j])
         want = np.concatenate([v[bt[b, np.arange(end[b]) // bs], np.arange(end[b]) % bs] for b in range(B)])
         assert np.abs(rows[j].double().cpu().numpy() - want).max() <= torch.finfo(t).eps / 2 * np.abs(want).max() * 1.01
+
+
+@pytest.mark.gpu
+def test_blocks_past_32_bits(cuda_device, pa):
+    """Codes at byte offsets past 2^32: append, decode and read-back give what a small pool gives."""
+    rng = np.random.default_rng(40)
+    dev, t, hq, hkv, d, bs = cuda_device, torch.bfloat16, 16, 16, 256, 1024
+    high = 2 ** 32 // (bs * hkv * d // 2) + 3
+    new = [torch.from_numpy(rng.standard_normal((1, 40, hkv, d))).to(t).to(dev) for _ in "kv"]
+    q = torch.from_numpy(rng.standard_normal((1, 1, hq, d))).to(t).to(dev)
+    ctx, ql = ints([40], dev), ints([40], dev)
+    res = []
+    for nblocks, blk in ((2, 1), (high + 1, high)):
+        codes = [torch.empty((nblocks, bs, hkv, d // 2), dtype=torch.uint8, device=dev) for _ in "kv"]
+        pairs = [torch.empty((nblocks, hkv, bs, 2), dtype=t, device=dev) for _ in "kv"]
+        bt = ints([[blk]], dev)
+        cfg = config(1, 40, hq, hkv, d, bs, 1, nblocks)
+        pa.append_kv(cfg, *new, bt, ctx, ql, *codes, *pairs)
+        one = config(1, 1, hq, hkv, d, bs, 1, nblocks)
+        out, lse = torch.empty_like(q), torch.empty(1, 1, hq, device=dev)
+        ws = torch.empty(pa.workspace_size(one), dtype=torch.uint8, device=dev)
+        args = bt, ctx, ints([1], dev)
+        pa.plan(one, *args, ws)
+        pa.decode(one, q, *codes, *pairs, *args, out, lse, ws)
+        pa.reduce(one, out, lse, ws)
+        assert pa.read_flags(ws) == 0
+        rows = [torch.empty(40, hkv, d, dtype=t, device=dev) for _ in "kv"]
+        pa.dequant_kv(one, *codes, *pairs, bt, ctx, *rows)
+        res.append([x.clone() for x in (out, lse, *rows)])
+        del codes, pairs
+    assert torch.isfinite(res[0][0].float()).all()
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_two_graphs_on_one_workspace(cuda_device, pa):
+    """Two captured steps that share a workspace, replayed in turn on one stream."""
+    dev = cuda_device
+    ps = [problem(50 + i, 2, 1, 8, 2, 128, 16, c, (1, 1)) for i, c in enumerate(((300, 20), (64, 500)))]
+    want = []
+    for p in ps:
+        cfg = config(2, 1, 8, 2, 128, 16, p["bt"].shape[1], p["nblocks"])
+        want.append(run(p, cfg, dev))
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=dev)
+    graphs, keep = [], []
+    for p in ps:
+        cfg = config(2, 1, 8, 2, 128, 16, p["bt"].shape[1], p["nblocks"])
+        x = [p[n].to(dev) for n in ("q", "kc", "vc", "ks", "vs")]
+        args = ints(p["bt"], dev), ints(p["ctx"], dev), ints(p["ql"], dev)
+        out, lse = torch.empty_like(x[0]), torch.empty(x[0].shape[:3], device=dev)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.plan(cfg, *args, ws)
+            pa.decode(cfg, *x, *args, out, lse, ws)
+            pa.reduce(cfg, out, lse, ws)
+        graphs.append(g)
+        keep.append((cfg, x, args, out, lse))
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (_, _, _, out, lse), (o, l) in zip(keep, want):
+        assert torch.equal(out.view(torch.int16), o.view(torch.int16)) and torch.equal(lse, l)
 
 
 @pytest.mark.gpu
