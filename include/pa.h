@@ -47,7 +47,9 @@
  * (quantising them to fp8 where the cache is fp8), and pa_gather_kv copies a batch's
  * cached K and V rows out of the pages into contiguous buffers (the workspace copy of
  * the HSTU paged attention), with the same calling convention.  pa_build_tables grows and
- * shrinks block tables from the requests' lengths.  A step that attends over a part of its
+ * shrinks block tables from the requests' lengths.  pa_append_rotated makes a projection's queries and
+ * keys ready (norms, rotary positions) as it appends, and pa_dequant_kv reads a quantised cache back as
+ * 16-bit rows.  A step that attends over a part of its
  * cached pages keeps channel bounds of every page's keys (pa_update_bounds), scores the pages
  * with them (pa_score_blocks), selects pages by score (pa_select_blocks) and attends over the
  * selected ones (pa_decode_selected).
@@ -167,16 +169,17 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
 
 /* Run the persistent decode over the work list pa_plan left in ws.
  *   q        [B, Sq, Hq, D]            q_dtype
- *   k_cache  [num_blocks, block_size, Hkv, D]   kv_dtype (uint8 codes for fp8)
+ *   k_cache  [num_blocks, block_size, Hkv, D]   kv_dtype (uint8 codes for fp8; see "4-bit caches")
  *   v_cache  same layout as k_cache
- *   k_scale, v_scale  NULL unless fp8 with a scale mode (see pa_scale_mode)
+ *   k_scale, v_scale  NULL unless there is a scale mode (see pa_scale_mode); 16-byte aligned pairs for
+ *            a 4-bit cache
  *   out      [B, Sq, Hq, D]            q_dtype; written for every unit done in one piece,
  *            with no keys, or merged here (see pa_split_merge)
  *   lse      [B, Sq, Hq] fp32 natural-log LSE, or NULL
  * The tables and lengths must be the ones given to pa_plan, with the same contents.  A CTA
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
- * fp8 cache) and of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
- * query rows per kv head) derives its first work item from the lengths (the planner's rules) and
+ * fp8 cache), of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
+ * query rows per kv head) and of the 4-bit decode derives its first work item from the lengths (the planner's rules) and
  * starts on it while the planner may still be running; it waits for the planner before the rest of
  * its list and before writing anything, and raises PA_FLAG_STALE_PLAN if the planner's first item
  * differs.  The other decode kernels wait for the planner first.

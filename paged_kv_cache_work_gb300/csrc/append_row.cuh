@@ -147,6 +147,13 @@ __device__ __forceinline__ void normalise(float (&x)[8], const uint4& weight, fl
   for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * f[e];
 }
 
+// A warp takes up to 24 steps of one token's rows, q's before k's before v's, each a row (or two, four)
+// of one kind; loops by kind keep what only queries or keys need out of the others' instructions.
+//   Measured (replayed): rotating append of 8 prompts of up to 4,096 tokens, 32 heads on 8 of 128, three
+// axes, 16-bit cache (405 MB) 83.7 us, 4.8 TB/s, bound by instructions (0.53 of a slot a cycle; 130 us
+// with steps of mixed kinds and eight a warp); one token of 32 sequences 2.8 us; 8 chunks of up to 512
+// rows into a 4-bit cache, 8 heads of 128, about 10 us, most of it the chain of a row's minimum, maximum,
+// step and quotients.  Three CTAs an SM: two take 102 us, four (64 registers) 88.
 template <int D, int QK, int KIND, bool ROT>
 __global__ void __launch_bounds__(256, KIND == STORE_16 && !ROT ? 4 : 3) append_kernel(const AppendParams p) {
   constexpr int L = D / 8, RPS = 32 / L;  // lanes of a row, rows of a step
