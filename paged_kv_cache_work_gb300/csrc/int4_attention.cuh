@@ -352,16 +352,17 @@ struct Int4Attention {
           const float x0 = s[c][t][2 * h], x1 = s[c][t][2 * h + 1];
           float2 e = make_float2(fast_exp2(__fmaf_rn(x0, scale[t].x, base[t].x)),
                                  fast_exp2(__fmaf_rn(x1, scale[t].y, base[t].y)));
-          if (!HOT) {
-            e.x = x0 == -INFINITY ? 0.f : e.x;
-            e.y = x1 == -INFINITY ? 0.f : e.y;
+          float2 m = make_float2(mid, mid), g = make_float2(f, f);
+          if (!HOT) {  // (nothing of a token that its row does not see, whatever its V pair holds)
+            if (x0 == -INFINITY) e.x = m.x = g.x = 0.f;
+            if (x1 == -INFINITY) e.y = m.y = g.y = 0.f;
           }
           if (sums) {
             l[t] = fadd2(l[t], e);
-            low[t].x = __fmaf_rn(e.x, mid, low[t].x);
-            low[t].y = __fmaf_rn(e.y, mid, low[t].y);
+            low[t].x = __fmaf_rn(e.x, m.x, low[t].x);
+            low[t].y = __fmaf_rn(e.y, m.y, low[t].y);
           }
-          pb[c][t][h] = transpose8(pack2<true>(e.x * f, e.y * f));
+          pb[c][t][h] = transpose8(pack2<true>(e.x * g.x, e.y * g.y));
         }
       }
   }

@@ -371,6 +371,22 @@ def test_decode_nan_stays_nan(cuda_device, pa):
     assert torch.isnan(out[0, 1]).all() and torch.isfinite(out[0, 0]).all() and torch.isfinite(out[1]).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [(float("nan"), 0.5), (0.25, float("nan")), (0.25, float("inf")), (float("inf"), 0.5)])
+@pytest.mark.parametrize("d,hq,dtype", [(64, 4, "bf16"), (128, 4, "fp16"), (128, 9, "bf16"), (256, 8, "fp16")])
+def test_decode_values_that_are_none(d, hq, dtype, bad, cuda_device, pa):
+    """A value's pair that is not finite reaches the rows that see it, and no other: those get what they
+    got without it."""
+    p = problem(17, 2, 3, hq, 1, d, 16, (64, 40), (3, 3), dtype)
+    cfg = config(2, 3, hq, 1, d, 16, p["bt"].shape[1], p["nblocks"], dtype, causal=1)
+    ref, ref_lse, size = reference(p, 1, d)
+    p["vs"][p["bt"][0, 3], 0, 14] = torch.tensor(bad).to(p["vs"].dtype)  # position 62: the last two rows
+    out, lse = run(p, cfg, cuda_device)
+    assert not torch.isfinite(out[0, 1:]).any()
+    out[0, 1:] = torch.from_numpy(ref[0, 1:]).to(out)
+    check(out, lse, ref, ref_lse, size, dtype)
+
+
 # ---- together --------------------------------------------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,bs,dtype", [(128, 16, "bf16"), (64, 64, "fp16"), (256, 32, "bf16")])
