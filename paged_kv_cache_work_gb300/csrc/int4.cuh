@@ -66,10 +66,11 @@ __device__ __forceinline__ uint16_t round_up_nonneg(float x) {
 
 // y / s correctly rounded for y = 0 or y in [2^-70, 2^70] and s in [2^-60, 2^60]: with the
 // reciprocal r correctly rounded, one step of Markstein's ("Computation of elementary functions on
-// the IBM RISC System/6000 processor", 1990): q = y r, q + (y - q s) r.
+// the IBM RISC System/6000 processor", 1990): q = y r, q + (y - q s) r, as q - (q s - y) r, which
+// leaves a zero its sign.
 __device__ __forceinline__ float quotient(float y, float s, float r) {
   const float q = __fmul_rn(y, r);
-  return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
+  return __fmaf_rn(-__fmaf_rn(q, s, -y), r, q);
 }
 
 // A row over L lanes (of a warp that is here as a whole), eight elements a lane: the lane's codes (its

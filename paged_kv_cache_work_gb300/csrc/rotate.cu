@@ -5,7 +5,7 @@
 //
 // The kernel is the append's (append_row.cuh): D / 8 lanes a row and eight consecutive elements a
 // lane, the mean square a shuffle sum, a pair's other channel in the same lane (interleaved) or
-// rotary_dim / 16 lanes away.  A warp takes up to eight steps of one token's rows, for which it reads
+// rotary_dim / 16 lanes away.  A warp takes up to 24 steps of one token's rows, for which it reads
 // the lengths, positions and angles once.  All in fp32; one rounding to q_dtype at the end, or the
 // cache's own quantisation.
 #include "append_row.cuh"

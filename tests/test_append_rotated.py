@@ -292,6 +292,30 @@ def test_every_split_of_a_tokens_rows(B, sq, hq, hkv, d, kv, cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_zeros_keep_their_signs(d, dtype, cuda_device, pa):
+    """fp8 codes of zeros, and of what a code cannot hold, have the sign of the value, by the plain append
+    and by the rotating one."""
+    t, dev = KINDS[dtype][0], cuda_device
+    x = torch.randn(2, 3, 2, d, generator=torch.Generator().manual_seed(5)).to(t)
+    x[..., ::5], x[..., 1::5], x[..., 2::5] = -0.0, 0.0, -float(torch.finfo(t).smallest_normal)
+    want = (x.float() / (x.float().abs().amax(-1, keepdim=True) / 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert (want[..., 0] == 0x80).all() and (want[..., 1] == 0).all()
+    cfg = config(2, 3, 2, 2, d, 16, 1, 2, dtype, "8token")
+    x, bt, n = x.to(dev), ints([[0], [1]], dev), ints([3, 3], dev)
+    for rotated in (False, True):
+        cache = [torch.zeros(2, 16, 2, d, dtype=torch.uint8, device=dev) for _ in "kv"]
+        scale = [torch.zeros(2, 16, 2, device=dev) for _ in "kv"]
+        if rotated:
+            pa.append_rotated(cfg, x, x, x, bt, n, n, torch.empty_like(x), *cache, *scale)
+        else:
+            pa.append_kv(cfg, x, x, bt, n, n, *cache, *scale)
+        for c in cache:
+            assert torch.equal(c[:, :3].cpu(), want)
+
+
+@pytest.mark.gpu
 def test_replays_in_a_graph(cuda_device, pa):
     p = Problem(8, 3, 2, 8, 2, 128, 16, "bf16", "8token", 128, 1, False, "both", True)
     want = {n: t.clone() for n, t in p.call(cuda_device).items() if n in ("qo", "kc", "vc", "ks")}
