@@ -405,7 +405,8 @@ def _rows(call: str, device: int, tokens: int, heads: int, dim: int, t, dtypes):
                 and shape[3] == dim and shape[2] == heads and (stride[2] == dim or heads == 1):
             b, sq = shape[0], shape[1]
             step = stride[1] if sq > 1 else stride[0] if b > 1 else 0
-            if b * sq >= tokens and (b == 1 or sq == 1 or stride[0] == sq * step):
+            # (tokens that share one row, as an expanded tensor's: 0 would say dense)
+            if b * sq >= tokens and (step or b * sq == 1) and (b == 1 or sq == 1 or stride[0] == sq * step):
                 return t.data_ptr(), step
     except AttributeError:
         if isinstance(t, int):

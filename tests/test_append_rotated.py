@@ -464,3 +464,14 @@ def test_binding_refuses_rows_that_do_not_fit():
     for bad in (x.transpose(2, 3), x[:, :, :4], x.float(), x[..., ::2]):
         with pytest.raises(pa.PaError):
             pa.append_rotated(cfg, bad, x, x, x, x, x, x, None, None, k_out=x)
+
+
+def test_binding_refuses_rows_that_are_one_row():
+    """An expanded tensor's tokens share one row, which the strides of a call cannot say (0 is dense)."""
+    x = torch.zeros(4, 1, 8, 128, dtype=torch.bfloat16)
+    for t, tokens in ((x[:1].expand(4, 1, 8, 128), 4), (x[:1].expand(1, 1, 8, 128).expand(4, 1, 8, 128), 2),
+                      (x[:1, :1].expand(1, 3, 8, 128), 3), (x[:1, :1].expand(2, 3, 8, 128), 6)):
+        with pytest.raises(pa.PaError):
+            pa._rows("pa_append_rotated", -1, tokens, 8, 128, t, (torch.bfloat16,))
+    assert pa._rows("pa_append_rotated", -1, 4, 8, 128, x, (torch.bfloat16,)) == (x.data_ptr(), 1024)
+    assert pa._rows("pa_append_rotated", -1, 1, 8, 128, x[:1], (torch.bfloat16,))[0] == x.data_ptr()
