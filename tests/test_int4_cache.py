@@ -336,6 +336,22 @@ def test_decode_rows_apart(cuda_device, pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("d,hq,hkv,ctas", [(64, 8, 2, 0), (128, 4, 1, 3), (128, 32, 8, 0), (256, 6, 1, 5)])
+def test_decode_padded_batches(d, hq, hkv, ctas, causal, cuda_device, pa):
+    """Sequences with fewer new rows than the batch's most: the rows behind, whatever their queries hold,
+    are zero with lse -inf, in whole and split units."""
+    p = problem(18, 5, 4, hq, hkv, d, 16, (900, 1200, 33, 640, 512), (1, 3, 4, 0, 2))
+    ref = reference(p, causal, d)
+    for b, n in enumerate(p["ql"]):
+        p["q"][b, n:] = (float("nan"), float("inf"), 1e30, 3.0, float("-inf"))[b]
+    cfg = config(5, 4, hq, hkv, d, 16, p["bt"].shape[1], p["nblocks"], causal=causal, num_ctas=ctas)
+    out, lse = run(p, cfg, cuda_device)
+    check(out, lse, *ref, "bf16")
+    assert all((out[b, n:] == 0).all() for b, n in enumerate(p["ql"]))
+
+
+@pytest.mark.gpu
 def test_pages_shared_by_sequences(cuda_device, pa):
     """A common prefix: the same pages in several tables."""
     p = problem(16, 3, 1, 8, 2, 128, 16, (200, 200, 200), (1, 1, 1))
