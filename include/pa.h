@@ -180,15 +180,15 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
  * fp8 cache), of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
  * query rows per kv head) and of the 4-bit decode derives its first work item from the lengths (the planner's rules) and
- * starts on it while the planner may still be running; it waits for the planner before the rest of
+ * starts on it while the planner is still running; it waits for the planner before the rest of
  * its list and before writing anything, and raises PA_FLAG_STALE_PLAN if the planner's first item
- * differs.  The other decode kernels wait for the planner first.
- * The kernels launch with programmatic dependent launch, so pa_decode reads q, the caches,
- * the scales, the tables and the lengths once the launch before it in the stream has let its dependents
- * start (a pa_plan call does so after its own wait on the launch before it): a kernel between
- * pa_plan and pa_decode that writes any of them must not let its dependents start early.
- * A decode that completed leaves the merge counters as pa_plan set them, so pa_decode may
- * run again on the same plan.
+ * differs.  Where the planner runs no longer, and the other decode kernels always, a CTA first waits for
+ * the launch before it.
+ * The kernels launch with programmatic dependent launch.  A kernel of the caller's between pa_plan and
+ * pa_decode that writes q, the caches, the scales, the tables or the lengths may do so too, if it lets its
+ * dependents start no earlier than its own wait on the launch before it.
+ * A decode that completed leaves the merge counters as pa_plan set them, so pa_decode may run again on
+ * the same plan: a model may plan once a step, and append, decode and reduce for each of its layers.
  *
  * Rounding.  Logits, the softmax's maxima and sums, and the outputs' accumulators are fp32.  A
  * weight is rounded once, to the type of the second product's operands: bf16 for a bf16 cache,
@@ -295,7 +295,8 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  * (the new tokens are the last q_lens[b] of the context_lens[b] tokens, the positions the
  * decode's causal mask gives them), i.e. slot pos % block_size of physical block
  * block_tables[b][pos / block_size] ("HSTU Paged Attention", RecSDK issue 1281, background:
- * the paged KV cache).  Call it before pa_plan / pa_decode with the same tables and lengths.
+ * the paged KV cache).  Call it with the tables and lengths of the pa_decode that is to read the rows,
+ * before that call (and before or behind its pa_plan).
  *   16-bit cache (kv_dtype == q_dtype): the row's bits are copied unchanged.
  *   fp8 cache: OCP E4M3 codes of row / scale, rounded to nearest (ties to even), magnitudes
  *   past 448 saturating to 448; scale modes of "Optimize paged-attention metadata decode"
@@ -379,7 +380,7 @@ typedef struct {
  *                                                           its axis's position
  * z of a query goes to q_out, z of a key to k_out (both rounded to q_dtype) and, quantised from fp32
  * as pa_append_kv quantises, into its page; values go into their pages as they are.  Keys, values,
- * scales, tables and lengths are those of pa_append_kv, for every cache but one with
+ * scales, tables, lengths and the order of calls are those of pa_append_kv, for every cache but one with
  * PA_SCALE_PER_BLOCK (PA_ERR_UNSUPPORTED: a page's scale needs all its new rows; take k_out and give
  * it to pa_append_kv).
  *

@@ -41,6 +41,17 @@ struct KernelParams {
   int batch, tt, tt_shift, item_cost;
 };
 
+// Whether what this grid reads may be read before its own grid_dependency_wait: only while the planner
+// runs.  The launch before this one is the planner then (no other starts before the planner has
+// completed, or lets this grid start before it has waited for it), and what the grid reads was written
+// before the planner's own wait.  On a kept plan, behind an append say, the mark is 0: such a grid waits
+// first.  (The mark is read past L1.  Asked at the start and looked at behind the set-up, it adds 0.2 to
+// 0.5 us to a 4-bit or streaming decode of 12 to 140 us, and nothing that can be measured to a tcgen05
+// one.)
+static __device__ __forceinline__ bool planner_runs(const KernelParams& p) {
+  return *static_cast<const volatile int32_t*>(p.flags - HDR_FLAGS + HDR_PLANNING) != 0;
+}
+
 // The first work item of CTA c of C, derived from the lengths with the planner's own rules
 // and integer arithmetic (the concatenated token space of plan.cu: each unit its tile-padded
 // length plus the item cost, cut into C equal tile-aligned pieces), so that a CTA can start

@@ -69,12 +69,14 @@ __global__ void __launch_bounds__(DecodeInt4Smem<T>::NTHREADS, DecodeInt4Smem<T>
   uint4* const query = reinterpret_cast<uint4*>(smem + M::OFF_QUERY);
   float4* const factors = reinterpret_cast<float4*>(smem + M::OFF_FACTORS) + warp * M::TK;
   float2* const ml = reinterpret_cast<float2*>(smem + M::OFF_ML);  // [NW][ROWS] (max, sum)
+  const bool planning = planner_runs(p);
   if (lane == 0) {  // (a warp's barriers are its own)
     for (int s = 0; s < NST; ++s) mbar_init(&bar[s], SUB + 32);
     fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
+  if (!planning) grid_dependency_wait();
   __syncwarp();
   const int box = min(p.bs, M::TK);  // tokens of a box: a page's, or a tile's
   const int t = lane % M::TK;  // a lane's token

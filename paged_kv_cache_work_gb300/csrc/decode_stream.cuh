@@ -52,12 +52,14 @@ __global__ void __launch_bounds__(T::NTHREADS, DecodeStreamSmem<T>::CTAS_PER_SM)
   int* const pend = reinterpret_cast<int*>(smem + M::OFF_BAR + NW * T::NST * 8);  // [4]
   float* const obuf = reinterpret_cast<float*>(smem);              // [NW][ROWS][OSTR]
   float2* const ml = reinterpret_cast<float2*>(smem + M::OFF_ML);  // [NW][ROWS] (max, sum)
+  const bool planning = planner_runs(p);
   if (lane == 0) {  // (a warp's barriers are its own)
     for (int s = 0; s < T::NST; ++s) mbar_init(&bar[s], kStreamArrivals<T>);
     fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
+  if (!planning) grid_dependency_wait();
   __syncwarp();
   const int4 first = first_item_of(p, blockIdx.x, gridDim.x, lane);
   int it = 0, items = 1, list = 0;  // this CTA's items begin at p.items[list]

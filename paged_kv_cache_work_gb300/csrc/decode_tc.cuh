@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
   float* mlbuf = reinterpret_cast<float*>(smem + T::OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool planning = planner_runs(p);
   if (tid == 0) {
     // readers of a ring slot: the widening warps (fp8 V), or the commit of the S (K) or PV
     // (V) that read it when the ring is not released through s_full / pv_done; full: the
@@ -782,7 +783,9 @@ __global__ void __launch_bounds__(TcTraits<D_, MP, KVK, SC>::NTHREADS, 1)
   // copies and MMAs start while the planner may still be running.  The lengths, the tables,
   // the queries and the caches were written before the planner ran (this grid starts only
   // once the planner has passed its own wait), so they may be read now; the planner's list
-  // and every write wait for the planner (ItemList::planned).
+  // and every write wait for the planner (ItemList::planned).  Where the planner does not run
+  // (any more, or a kept plan's), all waits for the launch before.
+  if (!planning) grid_dependency_wait();
   volatile int* s_first = abort_flag + 8;  // 4 ints
   if (warp == T::W_SOFT) {
     const int4 f = first_item_of(p, blockIdx.x, gridDim.x, lane);

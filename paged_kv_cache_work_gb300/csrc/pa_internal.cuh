@@ -206,7 +206,7 @@ inline Variant make_variant(const pa_config& c) {
 // Workspace layout (byte offsets from ws, every section 256-byte aligned).
 //   header     int32[64]: [0] flags, [1] chunk, [2] active CTAs, [3] items,
 //                         [4] units left to the reduce kernel, [5] how many of them have
-//                         at most kReduceWarpPieces pieces
+//                         at most kReduceWarpPieces pieces, [6] 1 while the planner runs
 //   item_off   int32[C + 1]      first work item of each CTA
 //   first_item int4[C]           each CTA's first work item again ((0, 0, 0, -1) if none), so
 //                                that a CTA reads it together with its offsets
@@ -251,7 +251,8 @@ inline WsLayout ws_layout(const pa_config& c, const Variant& v) {
 }
 
 enum HeaderSlot {
-  HDR_FLAGS = 0, HDR_CHUNK = 1, HDR_ACTIVE = 2, HDR_ITEMS = 3, HDR_NRED = 4, HDR_NRED_SMALL = 5
+  HDR_FLAGS = 0, HDR_CHUNK = 1, HDR_ACTIVE = 2, HDR_ITEMS = 3, HDR_NRED = 4, HDR_NRED_SMALL = 5,
+  HDR_PLANNING = 6
 };
 
 // Split units of at most this many pieces are merged by the reduce kernel one warp per row

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads, 1) plan_kernel(const PlanPara
   __shared__ int32_t s_start[kPlanSmemSeqs + 1];
   __shared__ int32_t s_len[kPlanSmemSeqs];
   grid_dependency_wait();     // lengths may come from the previous kernel in the stream
+  if (threadIdx.x == 0) *static_cast<volatile int32_t*>(p.hdr + HDR_PLANNING) = 1;
   grid_dependents_launch();   // the decode grid can stage its prologue meanwhile
   const int tid = threadIdx.x;
   const bool in_smem = p.batch <= kPlanSmemSeqs;
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads, 1) plan_kernel(const PlanPara
     p.hdr[HDR_ITEMS] = nitems;
     p.hdr[HDR_NRED] = nred;
     p.hdr[HDR_NRED_SMALL] = nsmall;
+    p.hdr[HDR_PLANNING] = 0;
   }
 }
 
