@@ -422,7 +422,7 @@ def append_rotated(cfg: PaConfig, q, k_new, v_new, block_tables, context_lens, q
     sines) a step's queries and keys, into q_out and k_out, and write its K/V rows into their pages,
     in one pass (see pa_append_rotated in pa.h).  q, k_new and v_new may be slices of one projection's
     output.  positions [axes, B, Sq] default to the cache positions; axis_pairs: how many of the
-    rotated pairs follow each axis.  With k_cache and v_cache None nothing goes into pages."""
+    rotated pairs follow each axis (either without cos_sin is refused).  With k_cache and v_cache None nothing goes into pages."""
     dev, i32, _, f32, kinds = _types()
     name, B, D = "pa_append_rotated", cfg.batch, cfg.head_dim
     kind, hq, hkv = kinds.get(cfg.q_dtype, ()), cfg.num_q_heads, cfg.num_kv_heads
@@ -441,6 +441,8 @@ def append_rotated(cfg: PaConfig, q, k_new, v_new, block_tables, context_lens, q
         pairs += (0,) * (3 - axes)
         if positions is not None:
             where = _dense(name, dev, axes * tokens, positions, i32)
+    elif positions is not None or axis_pairs is not None:  # (of angles that were not given)
+        raise PaError(name, ERR_INVALID_ARG)
     qp, qs = _rows(name, dev, tokens, hq, D, q, kind)
     kp, ks = _rows(name, dev, tokens, hkv, D, k_new, kind)
     vp = vs = blocks = kc = vc = k_sc = v_sc = None

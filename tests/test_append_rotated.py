@@ -475,3 +475,27 @@ def test_binding_refuses_rows_that_are_one_row():
             pa._rows("pa_append_rotated", -1, tokens, 8, 128, t, (torch.bfloat16,))
     assert pa._rows("pa_append_rotated", -1, 4, 8, 128, x, (torch.bfloat16,)) == (x.data_ptr(), 1024)
     assert pa._rows("pa_append_rotated", -1, 1, 8, 128, x[:1], (torch.bfloat16,))[0] == x.data_ptr()
+
+
+def test_binding_refuses_positions_without_angles(monkeypatch):
+    """Positions or axes say how to turn: without cos_sin nothing turns, and the call is refused."""
+    class Lib:
+        calls = 0
+
+        def pa_append_rotated(self, *args):
+            Lib.calls += 1
+            return pa.OK
+
+        def pa_status_string(self, status):
+            return b"refused"
+
+    monkeypatch.setattr(pa, "load", Lib)
+    rows = lambda **kw: pa.append_rotated(base(), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,  # noqa: E731
+                                          stream=0, **kw)
+    for kw in (dict(positions=FAKE), dict(axis_pairs=(64,)), dict(positions=FAKE, axis_pairs=(32, 32))):
+        with pytest.raises(pa.PaError) as e:
+            rows(**kw)
+        assert e.value.status == pa.ERR_INVALID_ARG
+    assert Lib.calls == 0
+    rows(), rows(interleaved=True)
+    assert Lib.calls == 2
