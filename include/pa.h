@@ -207,7 +207,8 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  *
  * Keys that a row does not see may hold anything; the values (V) of a key that some of a
  * sequence's rows see and others do not have to be finite, as a weight of zero meets them in the
- * same product. */
+ * same product.  (Not so for a 4-bit cache, whose codes are finite: a pair that is not reaches the rows
+ * that see its token, and no other.  A NaN logit is NaN in its row's out and lse, split or not.) */
 PA_API pa_status pa_decode(const pa_config *cfg, const void *q, const void *k_cache, const void *v_cache,
                     const void *k_scale, const void *v_scale, const int32_t *block_tables,
                     const int32_t *context_lens, const int32_t *q_lens, void *out, float *lse,

@@ -485,7 +485,8 @@ __device__ __forceinline__ void merge_unit(const KernelParams& p, int u, float* 
     if (rg >= p.M) continue;
     const float m = stat[2 * r], W = stat[2 * r + 1];
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (W > 0.f) {
+    const bool any = W != 0.f;  // a piece holds a key of the row (NaN stays NaN)
+    if (any) {
 #pragma unroll 4
       for (int s = 0; s < ns; ++s) {
         const size_t part = (size_t)piece_slot(first, s) * MP + r;
@@ -504,12 +505,12 @@ __device__ __forceinline__ void merge_unit(const KernelParams& p, int u, float* 
         O.w = __fmaf_rn(w, o.w, O.w);
       }
     }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
+    const float inv = any ? 1.f / W : 0.f;
     const size_t row = ((size_t)b * p.Sq + rg / p.G) * p.Hq + g * p.G + rg % p.G;
-    const float4 v = W > 0.f ? make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv)
+    const float4 v = any ? make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv)
                              : make_float4(0.f, 0.f, 0.f, 0.f);
     store_out4<QK>(p.out, row * D + d, v);
-    if (d == 0 && p.lse) p.lse[row] = W > 0.f ? (m + fast_log2(W)) * kLn2 : -INFINITY;
+    if (d == 0 && p.lse) p.lse[row] = any ? (m + fast_log2(W)) * kLn2 : -INFINITY;
   }
   if (tid == 0) p.unit_cnt[u] = 0;
   named_barrier_sync(1, NT);  // the shared buffers are reused next

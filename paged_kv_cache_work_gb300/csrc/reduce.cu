@@ -250,7 +250,8 @@ __device__ __forceinline__ void merge_row(const ReduceParams& p, int u, int2 inf
   }
   const int bq = u / (p.Hkv * p.RB), g = (u / p.RB) % p.Hkv;
   const size_t row = ((size_t)bq * p.Sq + rg / p.G) * p.Hq + g * p.G + rg % p.G;
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const bool any = W != 0.f;  // a piece holds a key of the row (NaN stays NaN)
+  const float inv = any ? 1.f / W : 0.f;
 #pragma unroll
   for (int v = 0; v < B::NV; ++v) {
     const int c = lane + 32 * v;
@@ -258,7 +259,7 @@ __device__ __forceinline__ void merge_row(const ReduceParams& p, int u, int2 inf
       store_out4<QK>(p.out, row * D + 4 * c,
                      make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv));
   }
-  if (lane == 0 && p.lse) p.lse[row] = W > 0.f ? (m + fast_log2(W)) * kLn2 : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[row] = any ? (m + fast_log2(W)) * kLn2 : -INFINITY;
 }
 
 template <int D, int QK>
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(const ReduceP
       float mb = ls;
 #pragma unroll
       for (int o2 = 16; o2 > 0; o2 >>= 1) mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o2));
-      if (mb == -INFINITY) continue;  // no key of this row in the batch (uniform)
+      if (__all_sync(kFull, ls == -INFINITY)) continue;  // no key of this row in the batch
       const float mn = fmaxf(m, mb);
       const float sc = m == -INFINITY ? 0.f : fast_exp2(m - mn);
       m = mn;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(const ReduceP
     const int c = threadIdx.x;
 #pragma unroll
     for (int k = 0; k < kReduceWarps; ++k) {
-      if (s_m[k] == -INFINITY) continue;
+      if (s_w[k] == 0.f) continue;  // (its maximum may be -inf with keys of NaN weight)
       const float sc = fast_exp2(s_m[k] - mt);
       Wt += sc * s_w[k];
       if (c < D4) {
@@ -426,10 +427,10 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(const ReduceP
     const int b = u / (p.Hkv * p.RB), g = (u / p.RB) % p.Hkv;
     const size_t row = ((size_t)b * p.Sq + rg / p.G) * p.Hq + g * p.G + rg % p.G;
     if (c < D4) {
-      const float inv = Wt > 0.f ? 1.f / Wt : 0.f;
+      const float inv = Wt != 0.f ? 1.f / Wt : 0.f;
       store_out4<QK>(p.out, row * D + 4 * c, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
     }
-    if (c == 0 && p.lse) p.lse[row] = Wt > 0.f ? (mt + fast_log2(Wt)) * kLn2 : -INFINITY;
+    if (c == 0 && p.lse) p.lse[row] = Wt != 0.f ? (mt + fast_log2(Wt)) * kLn2 : -INFINITY;
     __syncthreads();  // shared results are rewritten by the next row
   }
 }

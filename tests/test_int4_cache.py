@@ -403,6 +403,28 @@ def test_decode_values_that_are_none(d, hq, dtype, bad, cuda_device, pa):
     check(out, lse, ref, ref_lse, size, dtype)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("merge", [pa.MERGE_IN_DECODE, pa.MERGE_IN_REDUCE])
+@pytest.mark.parametrize("ctas", [1, 2, 9, 40])
+@pytest.mark.parametrize("d,hq", [(128, 4), (256, 10), (64, 2)])
+def test_decode_nan_survives_merges(d, hq, ctas, merge, cuda_device, pa):
+    """However a unit is split and wherever it is merged (4,200 tokens come to 33 pieces), a NaN query
+    and a key's NaN pair are NaN in out and lse of the rows that they reach, and in no other's."""
+    p = problem(19, 3, 2, hq, 1, d, 16, (4200, 4200, 150), (2, 2, 2))
+    ref, ref_lse, size = reference(p, 1, d)
+    p["q"][0, 1, hq - 1, 7] = float("nan")
+    p["ks"][p["bt"][1, 4199 // 16], 0, 4199 % 16] = float("nan")  # the last position: the last row's alone
+    cfg = config(3, 2, hq, 1, d, 16, p["bt"].shape[1], p["nblocks"], causal=1, num_ctas=ctas, split_merge=merge)
+    out, lse = run(p, cfg, cuda_device)
+    lost = np.zeros((3, 2, hq), bool)
+    lost[0, 1, hq - 1] = lost[1, 1] = True
+    assert (torch.isnan(out.float()).all(-1).cpu().numpy() == lost).all()
+    assert (torch.isnan(lse).cpu().numpy() == lost).all()
+    mask = torch.from_numpy(lost).to(out.device)
+    out[mask], lse[mask] = torch.from_numpy(ref).to(out)[mask], torch.from_numpy(ref_lse).to(lse)[mask]
+    check(out, lse, ref, ref_lse, size, "bf16")
+
+
 # ---- together --------------------------------------------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,bs,dtype", [(128, 16, "bf16"), (64, 64, "fp16"), (256, 32, "bf16")])
