@@ -499,3 +499,35 @@ def test_binding_refuses_positions_without_angles(monkeypatch):
     assert Lib.calls == 0
     rows(), rows(interleaved=True)
     assert Lib.calls == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_any_scale_of_a_tensor(dtype, rotated, cuda_device, pa):
+    """Codes under a tensor's scale are those of IEEE quotients, whatever the scale and the elements are."""
+    t, dev, d = KINDS[dtype][0], cuda_device, 128
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(1, 64, 1, d, generator=g).float() * 2.0 ** torch.randint(-90, 90, (1, 64, 1, d), generator=g)
+    x = x.clamp(-float(torch.finfo(t).max), float(torch.finfo(t).max)).to(t)
+    edge = [0.0, -0.0, float("inf"), float("-inf"), float("nan"), float(torch.finfo(t).max), -float(torch.finfo(t).max),
+            float(torch.finfo(t).smallest_normal), -float(torch.finfo(t).smallest_normal) / 4, 448.0, -464.0, 2.0 ** -10]
+    x[0, 0, 0, :len(edge)] = torch.tensor(edge).to(t)
+    cfg = config(1, 64, 1, 1, d, 64, 1, 1, dtype, "8tensor")
+    dx, bt, n = x.to(dev), ints([[0]], dev), ints([64], dev)
+    for s in (0.03, 1.0, 0.7, 2.0 ** -60, 2.0 ** 60, 1.5 * 2.0 ** -61, 2.0 ** 61, 3.1e-30, 1e-38, 1e38, -0.3, 0.0, float("inf"),
+              float("nan")):
+        scale = torch.tensor([s])
+        q = x.float() / scale
+        want = q.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        none = torch.isnan(q)
+        cache = [torch.zeros(1, 64, 1, d, dtype=torch.uint8, device=dev) for _ in "kv"]
+        args = bt, n, n
+        if rotated:
+            pa.append_rotated(cfg, dx, dx, dx, *args, torch.empty_like(dx), *cache, scale.to(dev), scale.to(dev))
+        else:
+            pa.append_kv(cfg, dx, dx, *args, *cache, scale.to(dev), scale.to(dev))
+        for c in cache:
+            c = c.cpu()
+            assert torch.equal(c[~none], want[~none]), s
+            assert ((c[none] & 0x7f) == 0x7f).all(), s
