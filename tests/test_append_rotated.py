@@ -531,3 +531,22 @@ def test_any_scale_of_a_tensor(dtype, rotated, cuda_device, pa):
             c = c.cpu()
             assert torch.equal(c[~none], want[~none]), s
             assert ((c[none] & 0x7f) == 0x7f).all(), s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exp", [-30, -1, 0, 7])
+def test_scale_of_all_ones(exp, cuda_device, pa):
+    """Divisors just below a power of two: the quotient of a power of two lies half a step past one, and
+    past the tie of the least code with zero, where one correction step has no bit to spare."""
+    dev, d = cuda_device, 64
+    s = (2 - 2.0 ** -23) * 2.0 ** exp
+    x = (2.0 ** (exp + 1 + torch.arange(-16.0, 16.0)).repeat(2)).view(1, 1, 1, d).to(torch.bfloat16)
+    x[..., 32:] = -x[..., 32:]
+    scale = torch.tensor([s], dtype=torch.float32)
+    want = (x.float() / scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert int(want[0, 0, 0, 6]) == 1  # 2^-10 and a little
+    cfg = config(1, 1, 1, 1, d, 16, 1, 1, "bf16", "8tensor")
+    cache = [torch.zeros(1, 16, 1, d, dtype=torch.uint8, device=dev) for _ in "kv"]
+    pa.append_kv(cfg, x.to(dev), x.to(dev), ints([[0]], dev), ints([1], dev), ints([1], dev), *cache, scale.to(dev), scale.to(dev))
+    for c in cache:
+        assert torch.equal(c[0, 0].cpu(), want[0, 0])
