@@ -75,7 +75,10 @@ pa_status prepare(const pa_config* cfg, Variant* v, WsLayout* L) {
   // The planner's concatenated token space is indexed with int32.
   const long long per_unit =
       (long long)cfg->max_blocks_per_seq * cfg->block_size + v->tt + v->item_cost;
-  if ((long long)v->units * per_unit >= (1ll << 30)) return PA_ERR_UNSUPPORTED;
+  constexpr long long most = 1ll << 30;
+  const long long heads = (long long)cfg->batch * cfg->num_kv_heads;
+  if (heads >= most || heads * v->rb >= most || per_unit >= most || heads * v->rb * per_unit >= most)
+    return PA_ERR_UNSUPPORTED;
   *L = ws_layout(*cfg, *v);
   return PA_OK;
 }

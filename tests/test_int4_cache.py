@@ -605,6 +605,17 @@ def test_workspace_refusals(lib, kw, expect):
     assert (n.value > 0) == (expect == pa.OK)
 
 
+@pytest.mark.parametrize("kv,mode", [(pa.INT4, pa.SCALE_AFFINE), (pa.BF16, pa.SCALE_NONE), (pa.FP8_E4M3, pa.SCALE_PER_BLOCK)])
+@pytest.mark.parametrize("B,hkv,sq", [(65536, 32, 1 << 15), (65536, 64, 1 << 20), (1 << 16, 1 << 15, 1), (1 << 20, 1 << 12, 1)])
+def test_more_units_than_an_index_holds(lib, kv, mode, B, hkv, sq):
+    """Products that pass 32 bits, some of them to zero."""
+    for maxb, bs in ((1, 16), (1 << 16, 16), (2 ** 31 - 1, 1024)):
+        cfg = small(B=B, hq=hkv, hkv=hkv, sq=sq, maxb=maxb, bs=bs, nblocks=1 << 20, kv=kv, mode=mode)
+        n = ctypes.c_size_t(0)
+        assert lib.pa_workspace_size(ctypes.byref(cfg), ctypes.byref(n)) == pa.ERR_UNSUPPORTED
+        assert n.value == 0
+
+
 def test_a_query_of_4_bits_is_refused(lib):
     cfg, n = small(), ctypes.c_size_t(0)
     cfg.q_dtype = pa.INT4
