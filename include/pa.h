@@ -326,8 +326,11 @@ PA_API pa_status pa_gather_kv(const pa_config *cfg, const void *k_cache, const v
  *     c    = (x - low) / step (fp32 difference and IEEE quotient) rounded to the nearest integer,
  *            ties to even; 0 when step is 0.
  *   So low is the least element itself and a value is read back within step / 2, which is a
- *   thirtieth of the row's range (and half a step of q_dtype in that).  A row that holds a NaN or
- *   an infinity, or whose range passes fp32, gets step NaN and codes 0: all of it reads back NaN.
+ *   thirtieth of the row's range (and half a step of q_dtype in that).  (The keys that
+ *   pa_append_rotated quantises are fp32: there low may lie below the least element.)  A row that
+ *   holds a NaN or an infinity, whose range passes fp32, or whose low or step passes q_dtype's
+ *   largest number (fp16 keys that a rotation or a norm's weights take past 65504), gets step NaN
+ *   and codes 0: all of it reads back NaN.
  * Reads cfg's batch, max_q_len, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
  * num_blocks, q_dtype, kv_dtype and kv_scale_mode.
  *

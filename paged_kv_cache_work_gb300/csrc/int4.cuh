@@ -99,8 +99,9 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[8], uint32_t* 
   }
   const uint32_t step_bits = round_up_nonneg<QK>(__fdiv_rn(range, 15.f));
   const float step = pair_values<QK>(step_bits).x;
-  *pair = step_bits | low_bits << 16;
-  if (step == 0.f) return 0;
+  const bool fits = step < INFINITY;  // (an fp32 row's step may pass fp16)
+  *pair = (fits ? step_bits : 0x7fffu) | low_bits << 16;
+  if (step == 0.f || !fits) return 0;
   uint32_t codes = 0;
   const bool plain = step >= 0x1p-60f && step <= 0x1p60f;
   const float inv = __fdiv_rn(1.f, step);

@@ -550,3 +550,48 @@ def test_scale_of_all_ones(exp, cuda_device, pa):
     pa.append_kv(cfg, x.to(dev), x.to(dev), ints([[0]], dev), ints([1], dev), ints([1], dev), *cache, scale.to(dev), scale.to(dev))
     for c in cache:
         assert torch.equal(c[0, 0].cpu(), want[0, 0])
+
+
+@pytest.mark.gpu
+def test_keys_past_the_type_of_their_pairs(cuda_device, pa):
+    """fp16 keys that a norm's weights take past 65504: those whose low or step does not fit read back as
+    NaN, with codes 0, and so do the rows that see them; others keep their codes."""
+    dev, d, bs = cuda_device, 256, 16
+    x = torch.zeros(1, 4, 1, d)
+    x[0, 0, 0, 5], x[0, 1, 0, 6], x[0, 2, 0, 7] = -1.0, 1.0, 1.0  # 16 in size once normalised
+    x[0, 3] = torch.randn(1, d, generator=torch.Generator().manual_seed(1))
+    w = torch.ones(d)
+    w[5], w[6], w[7] = 8000.0, 8000.0, 65000.0  # -128,000; 128,000 (a step of 8,534); 1,040,000 (69,334)
+    x, w = x.half().to(dev), w.half().to(dev)
+    cfg = config(1, 4, 1, 1, d, bs, 1, 1, "fp16", "4", causal=1)
+    codes = [torch.full((1, bs, 1, d // 2), 255, dtype=torch.uint8, device=dev) for _ in "kv"]
+    pairs = [torch.zeros(1, 1, bs, 2, dtype=torch.float16, device=dev) for _ in "kv"]
+    bt, n, flags, q = ints([[0]], dev), ints([4], dev), ints([0], dev), torch.empty_like(x)
+    pa.append_rotated(cfg, x, x, x, bt, n, n, q, *codes, *pairs, k_weight=w, eps=0.0, flags=flags)
+    assert int(flags.item()) == 0
+    step, low = pairs[0][0, 0, :4].float().cpu().T
+    y = plain.rotate(x[0, :, 0].double().cpu().numpy(), w.double().cpu().numpy(), 0.0, None, None, None, False)
+    beyond = (y.min(1) < -65504) | ((y.max(1) - y.min(1)) / 15 > 65504)
+    assert beyond.tolist() == [True, False, True, True]  # (row 3's element 7 is -100,572)
+    assert torch.isnan(step).tolist() == beyond.tolist()
+    c = plain.unpack(codes[0][0, :4, 0].cpu().numpy())
+    assert (c[beyond] == 0).all()
+    assert float(low[1]) == 0 and 127999 / 15 <= float(step[1]) <= 128000 / 15 * (1 + 2.0 ** -10)
+    assert c[1, 6] == 15 and c[1].sum() == 15
+    assert torch.isfinite(pairs[1][0, 0, :4]).all()
+    k, v = (torch.empty(4, 1, d, dtype=torch.float16, device=dev) for _ in "kv")
+    pa.dequant_kv(cfg, *codes, *pairs, bt, n, k, v)
+    assert torch.isnan(k[[0, 2, 3]]).all() and not torch.isnan(k[1]).any() and torch.isfinite(v).all()
+    for rows, lost in (([1], False), ([0], True), ([2], True), ([3, 1], True)):  # the seen keys, one or two
+        bt2 = ints([[0]], dev)
+        cc, pp = [torch.zeros_like(t) for t in codes], [torch.zeros_like(t) for t in pairs]
+        for a, b in zip(cc + pp, codes + pairs):
+            for i, r in enumerate(rows):
+                if a.dtype == torch.uint8:
+                    a[0, i] = b[0, r]
+                else:
+                    a[0, 0, i] = b[0, 0, r]
+        one = config(1, 1, 1, 1, d, bs, 1, 1, "fp16", "4")
+        out, lse = torch.empty(1, 1, 1, d, dtype=torch.float16, device=dev), torch.empty(1, 1, 1, device=dev)
+        pa.decode_step_static(one, q[:, 3:].contiguous(), *cc, *pp, bt2, ints([len(rows)], dev), ints([1], dev), out, lse)
+        assert bool(torch.isnan(out).all()) == lost and bool(torch.isnan(lse).all()) == lost
