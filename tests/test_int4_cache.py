@@ -425,6 +425,53 @@ def test_decode_nan_survives_merges(d, hq, ctas, merge, cuda_device, pa):
     check(out, lse, ref, ref_lse, size, "bf16")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("d,hq,dtype", [(64, 3, "bf16"), (64, 16, "fp16"), (128, 4, "bf16"), (128, 13, "bf16"),
+                                        (256, 8, "fp16"), (256, 16, "bf16"), (256, 9, "fp16")])
+def test_decode_looks_up_pages_again(d, hq, dtype, bs, cuda_device, pa):
+    """Items whose warps pass their 32nd and 64th chunk of 16 tokens, where a lane's next pages are looked
+    up: as they are, and with pages outside the pool in the chunks on both sides of the first turn."""
+    ctx = (4300, 4231)
+    p = problem(33, 2, 1, hq, 1, d, bs, ctx, (1, 1), dtype)
+    cfg = config(2, 1, hq, 1, d, bs, p["bt"].shape[1], p["nblocks"], dtype, num_ctas=1)
+    out, lse = run(p, cfg, cuda_device)
+    check(out, lse, *reference(p, 0, d), dtype)
+    bt = p["bt"].copy()
+    # a warp's 32nd and 33rd chunk: of warps 0 and 3, in tiles of two chunks (121 and 128, 127 and 134)
+    # and of one (124 and 128, 127 and 131)
+    for chunk in (121, 124, 127, 128, 131, 134):
+        bt[:, chunk * 16 // bs] = (p["nblocks"], -1)
+    out, lse = run(p, cfg, cuda_device, bt, pa.FLAG_BAD_BLOCK_ID)
+    check(out, lse, *reference(p, 0, d, bt), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq", [(64, 2), (128, 20), (256, 8)])
+def test_decode_of_nothing(d, hq, cuda_device, pa):
+    """A batch without a single token, behind a batch with some on the same workspace."""
+    p = problem(35, 3, 2, hq, 1, d, 16, (0, 0, 0), (0, 0, 0))
+    cfg = config(3, 2, hq, 1, d, 16, p["bt"].shape[1], p["nblocks"])
+    out, lse = run(p, cfg, cuda_device)
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+@pytest.mark.gpu
+def test_paged_attention_takes_a_4_bit_cache(cuda_device, pa):
+    """The step on a problem laid out as the workloads are, its config made from it."""
+    from types import SimpleNamespace
+    p = problem(34, 3, 2, 8, 2, 128, 16, (300, 17, 64), (2, 1, 2))
+    g = lambda t: t.to(cuda_device)  # noqa: E731
+    inp = dict(workload=SimpleNamespace(batch=3, max_q_len=2, num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16,
+                                        q_dtype="bf16", kv_dtype="int4", scale_mode="none", causal=True),
+               q=g(p["q"]), k_cache=g(p["kc"]), v_cache=g(p["vc"]), k_scale=g(p["ks"]), v_scale=g(p["vs"]),
+               block_tables=ints(p["bt"], cuda_device), context_lens=ints(p["ctx"], cuda_device),
+               q_lens=ints(p["ql"], cuda_device), sm_scale=128 ** -0.5)
+    out, lse, ws = pa.paged_attention(inp)
+    assert pa.read_flags(ws) == 0
+    check(out, lse, *reference(p, 1, 128), "bf16")
+
+
 # ---- together --------------------------------------------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,bs,dtype", [(128, 16, "bf16"), (64, 64, "fp16"), (256, 32, "bf16")])
@@ -614,6 +661,16 @@ def test_more_units_than_an_index_holds(lib, kv, mode, B, hkv, sq):
         n = ctypes.c_size_t(0)
         assert lib.pa_workspace_size(ctypes.byref(cfg), ctypes.byref(n)) == pa.ERR_UNSUPPORTED
         assert n.value == 0
+
+
+def test_config_of_a_4_bit_workload():
+    from types import SimpleNamespace
+    w = SimpleNamespace(batch=3, max_q_len=2, num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16, q_dtype="fp16",
+                        kv_dtype="int4", scale_mode="none", causal=True)
+    inp = dict(workload=w, q=torch.zeros(1), k_cache=torch.zeros(7, 1), block_tables=torch.zeros(3, 5), sm_scale=0.5)
+    cfg = pa.config_for(inp, num_ctas=4)
+    assert (cfg.kv_dtype, cfg.kv_scale_mode, cfg.q_dtype) == (pa.INT4, pa.SCALE_AFFINE, pa.FP16)
+    assert (cfg.num_blocks, cfg.max_blocks_per_seq, cfg.causal) == (7, 5, 1) and pa.workspace_size(cfg) > 0
 
 
 def test_a_query_of_4_bits_is_refused(lib):
