@@ -201,9 +201,10 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * head at head dim 128 any query goes into two or three E4M3 terms, scaled to fit, where elements
  * below about a thousandth of the row's largest lose bits.  64-dim fp8 caches without page scales
  * run in fp32 throughout.  For a 4-bit cache the codes enter both products as the integers c - 8,
- * the query in f16 times a power of two that makes it fit, a weight times its row's V step in f16
+ * a bf16 query in f16 times a power of two that makes it fit (elements below 2^-22 of its row's
+ * largest lose bits), a weight times its row's V step in f16
  * (11 bits kept as with PA_SCALE_PER_BLOCK), and what low + 8 step adds to logits and outputs is
- * fp32.
+ * fp32; an fp16 output is so off by up to a third more than its own rounding, a bf16 output is not.
  *
  * Keys that a row does not see may hold anything; the values (V) of a key that some of a
  * sequence's rows see and others do not have to be finite, as a weight of zero meets them in the
@@ -400,7 +401,7 @@ typedef struct {
  *   flags          NULL, or a device int32: PA_FLAG_BAD_LENGTHS (nothing of that sequence is
  *                  written), PA_FLAG_BAD_POSITION (nothing of that token is written),
  *                  PA_FLAG_BAD_BLOCK_ID (that token's K and V do not go into a page)
- * Reads cfg's batch, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+ * No other two arrays may overlap, where one of them is written.  Reads cfg's batch, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
  * max_blocks_per_seq, num_blocks, q_dtype, kv_dtype and kv_scale_mode.  Stream-ordered, allocates
  * nothing, never synchronises. */
 PA_API pa_status pa_append_rotated(const pa_config *cfg, const pa_rotary *rotary, const void *q,

@@ -7,8 +7,8 @@
 // streams.
 //
 // Measured (plan, decode and reduce; replayed): 32 contexts of 512 to 4,096 tokens, 32 heads on 8 kv
-// heads of 128, pages of 16 (81 MB) 32 us, with four new tokens each 43; 32 of 2,048 to 16,384, 16 heads
-// of 256 (1.25 GB) 239 us, 5.2 TB/s; 4 of 32,768 to 131,072, 16 heads on one of 128 (45 MB) 27.5 us, of
+// heads of 128, pages of 16 (81 MB) 32.5 us, with four new tokens each 45; 32 of 2,048 to 16,384, 16 heads
+// of 256 (1.25 GB) 239 us, 5.2 TB/s; 4 of 32,768 to 131,072, 16 heads on one of 128 (45 MB) 28.7 us, of
 // which plan, start, merge and reduce are about 10.  What bounds it is a warp's own chain: alone on its
 // scheduler it takes 2,400 cycles a tile of 32 tokens (632 instructions; 320 are the widening of codes
 // and the products), three together 3,200, so that a scheduler issues 0.55 instructions a cycle (head

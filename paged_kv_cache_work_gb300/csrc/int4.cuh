@@ -25,7 +25,9 @@ __device__ __forceinline__ float2 pair_values(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// The eight codes of a word as fp32: two at a time masked into the mantissas of 1024 (64) in f16.
+// The eight codes of a word as fp32: two at a time masked into the mantissas of 1024 (64) in f16 (Kim,
+// Henry, Fahmy and Hassan Awadalla, "Who says elephants can't run: bringing large scale MoE models into
+// cloud scale production", 2022).
 __device__ __forceinline__ void code_values(uint32_t w, float (&c)[8]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -7,8 +7,8 @@
 // its weight.  Both products run transposed on mma.sync m16n8k16, S^T = K Q^T and O^T = V^T P^T, with
 // tokens (channels) along the MMA's 16 rows and query rows along its 8 columns: a tile of up to 8
 // query rows then costs half of what one of 16 does, which is what widening the codes leaves to save.
-// A word of codes is eight channels; two halves of it masked into the mantissa of 1024 (or 64), less
-// 1032 (72), are two f16 operands.  The order of channels inside a k-step is the queries' own affair,
+// A word of codes is eight channels; two halves of it masked into the mantissa of 1024 (or 64; the
+// conversion that int4.cuh cites), less 1032 (72), are two f16 operands.  The order of channels inside a k-step is the queries' own affair,
 // so a K row's words are operands as they lie.  A V operand holds one channel of two tokens: one byte
 // permute brings the halves of two tokens' words together.  P^T comes from S^T through movmatrix.
 //
@@ -17,6 +17,17 @@
 // token's factors from its pairs; of a K word's two masked halves one is taken as 64 + c, the 72 too
 // much being in the logits' accumulators from the start (72 times the sum of those channels' queries);
 // a tile that every row sees whole, with V steps that fit the accumulators' unit, passes no mask.
+//
+// Where bits are given up:
+//   - A weight times its V step is rounded to f16, the operand's type, while the weights' sum is taken
+// before it: 2^-12 of a weight at most.  An operand for the rest would double the second product, which is
+// 91 of a chunk's 316 instructions.  A bf16 output hides it (relative error against 64 bits 0.00164 to
+// 0.00168, 0.00164 to 0.00171 for fp32 arithmetic throughout); an fp16 output's is 2.3e-4 to 2.7e-4 where
+// its own rounding is 2.0e-4 to 2.1e-4.
+//   - A bf16 query goes into f16 times a power of two: elements below 2^-22 of its largest lose bits.  In
+// two f16 terms the first product would take twice as long.
+//   - 64 + c in place of c - 8 costs a logit up to three bits of fp32 (lse within 8e-7 relative; 2e-7
+// for fp32 throughout), and a subtraction less for every other operand of K.
 //
 // Thread (quad, qi) = (lane / 4, lane % 4): tokens quad and quad + 8 of a chunk and query rows
 // 8 t + 2 qi, + 1 of the logits; tokens 2 qi, 2 qi + 1 (+ 8) of V.

@@ -135,6 +135,10 @@ constexpr int stream_max_rows(int head_dim) {
 // 239 / 241 / 242.  Tiles of 16: the former with four new tokens 48.0 / 45.8 / 43.4 / 45.8; 64 contexts
 // of 8,192 to 16,384, 16 heads on one, 49.0 / 47.0 / 47.0 / 47.0; 4 of 32,768 to 131,072 29.8 / 28.1 /
 // 27.5 / 27.5.
+//   A warp's tile is 16 tokens for head dim 256 with 16 rows, whose state takes most of the registers (32
+// tokens spill 136 bytes), else 32: 4 contexts of 32,768 to 131,072, 16 heads on one of 256, 45.1 us with
+// 16 tokens and 50.7 with 32; 64 of 8,192 to 16,384 81.3 and 81.8, with two new tokens 140.8 and 132.4; 32
+// of 512 to 4,096, 16 kv heads of 256, four rows' tokens each 126.5 and 121.6.
 constexpr int int4_tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
 constexpr int int4_tile_tokens(int head_dim, int mp) { return head_dim == 256 && mp == 16 ? 16 : 32; }
 constexpr int kInt4RoundTokens = 128;
