@@ -127,3 +127,54 @@ def test_layers_on_one_plan(kv, sq, hq, hkv, d, rotated, cuda_device, pa):
             give(turn)
             graph.replay()
             same(run, turn)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("merge", [pa.MERGE_IN_DECODE, pa.MERGE_IN_REDUCE])
+@pytest.mark.parametrize("kv,hq,d", [("4", 4, 128), ("4", 16, 256), ("16", 48, 128), ("8block", 8, 64)])
+def test_decodes_of_split_units_on_one_plan(kv, hq, d, merge, cuda_device, pa):
+    """Two caches and queries in turn on one plan, their units in many pieces, in a captured graph: the
+    merges start anew with every decode, and read its own pieces."""
+    dev, bs, hkv, n = cuda_device, 32, 1, (3000, 40, 1111)
+    kind, mode = KINDS[kv]
+    bt, nblocks = plain.tables(np.random.default_rng(5), np.asarray(n), bs)
+    ints = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    make = lambda sq: pa.PaConfig(  # noqa: E731
+        batch=3, max_q_len=sq, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs,
+        max_blocks_per_seq=bt.shape[1], num_blocks=nblocks, q_dtype=pa.BF16, kv_dtype=kind, kv_scale_mode=mode,
+        sm_scale=d ** -0.5, num_ctas=70, split_merge=merge)
+    g = torch.Generator(device=dev).manual_seed(8)
+    args, cfg, cases = (ints(bt), ints(n), ints([1, 1, 1])), make(1), []
+    for _ in range(2):
+        cache = layer_cache(kv, nblocks, bs, hkv, d, dev)
+        new = [torch.randn((3, max(n), hkv, d), generator=g, device=dev).to(torch.bfloat16) for _ in "kv"]
+        pa.append_kv(make(max(n)), *new, args[0], args[1], args[1], *cache)
+        q = torch.randn((3, 1, hq, d), generator=g, device=dev).to(torch.bfloat16)
+        cases.append((q, cache, torch.empty_like(q), torch.empty((3, 1, hq), device=dev)))
+    ws = torch.empty(pa.workspace_size(cfg), dtype=torch.uint8, device=dev)
+
+    def step(fresh):
+        if not fresh:
+            pa.plan(cfg, *args, ws)
+        for q, cache, out, lse in cases:
+            if fresh:
+                pa.plan(cfg, *args, ws)
+            pa.decode(cfg, q, *cache, *args, out, lse, ws)
+            pa.reduce(cfg, out, lse, ws)
+            if fresh:
+                torch.cuda.synchronize()
+
+    step(True)
+    want = [(out.clone(), lse.clone()) for _, _, out, lse in cases]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(False)
+        step(False)
+    for _ in range(5):
+        for _, _, out, lse in cases:
+            out.fill_(7), lse.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert pa.read_flags(ws) == 0
+        for (_, _, out, lse), (o, l) in zip(cases, want):
+            assert torch.equal(out.view(torch.int16), o.view(torch.int16)) and torch.equal(lse, l)
