@@ -95,7 +95,7 @@ extern "C" pa_status pa_append_kv(const pa_config* cfg, const void* k_new, const
   p.maxb = c.max_blocks_per_seq;
   p.nblocks = c.num_blocks;
   p.scale_mode = c.kv_scale_mode;
-  split_rows(p, c.head_dim, sms, store_kind(c), false, true);
+  split_rows(p, c.head_dim, sms, true);
   const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16;
   return launch_append(p, c.head_dim, qk, store_kind(c), reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess

@@ -53,25 +53,23 @@ struct AppendParams {
 cudaError_t launch_append(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
 cudaError_t launch_rotate(const AppendParams& p, int head_dim, int qk, int kind, cudaStream_t s);
 
-// CTAs of eight warps that an SM holds of an instance.
-constexpr int append_ctas(int kind, bool rotates) { return kind == STORE_16 && !rotates ? 4 : 3; }
-
 // Splits a token's rows over warps: as many steps a warp as leave 32 warps an SM (at most 24: the steps
-// share the token's lengths, positions and angles), at least two where single steps would not all be
-// resident at once, the same for each of the token's warps.  A step is one to four rows of one kind.
+// share the token's lengths, positions and angles), at least two past 24 warps an SM (what is resident of
+// most instances at once), the same for each of the token's warps.  A step is one to four rows of one kind.
 // Tokens behind a sequence's last count as the others do: their number is only known on the GPU.
 //   Measured: 32 sequences of 4 tokens, 16 kv heads of 256 (4,096 steps), fp8 per token 2.8 us (3.9 with one
-// step a warp, a part of them in a second wave), 4 bits 3.3 (4.2); rotating 32 of 8, 32 heads on 8 of 128, 4.0
-// (5.6).  4 prompts of 2,048 such fp8 rows 57 us in 16 and 16 steps of a token's 32, 75 in 24 and 8.
-// As many steps as all warps are resident with: 4 chunks of 512, 32 heads on 4, 8.6 us in place of 7.4.
-inline void split_rows(AppendParams& p, int head_dim, int sms, int kind, bool rotates, bool stores) {
+// step a warp, a part of them in a second wave), 4 bits 3.3 (4.2), 16 bits 2.2 (2.45); rotating 32 of 8,
+// 32 heads on 8 of 128, 4.0 (5.6).  4 prompts of 2,048 such fp8 rows 57 us in 16 and 16 steps of a token's
+// 32, 75 in 24 and 8.  As many steps as all warps are resident with: 4 chunks of 512, 32 heads on 4, 8.6 us
+// in place of 7.4.
+inline void split_rows(AppendParams& p, int head_dim, int sms, bool stores) {
   const int rows_per_step = 256 / head_dim;
   p.q_steps = ceil_div(p.Hq, rows_per_step);
   p.k_steps = ceil_div(p.Hkv, rows_per_step);
   p.v_steps = stores ? p.k_steps : 0;
   const int steps = p.q_steps + p.k_steps + p.v_steps;
   const long long all = (long long)p.tokens * steps, spare = all / ((long long)sms * 32);
-  const int least = all > (long long)sms * append_ctas(kind, rotates) * 8 ? 2 : 1;
+  const int least = all > (long long)sms * 24 ? 2 : 1;
   p.parts = ceil_div(steps, (int)(spare < least ? least : spare > 24 ? 24 : spare));
   p.per = ceil_div(steps, p.parts);
   p.part_div = FastDiv((uint32_t)p.parts);
@@ -171,7 +169,7 @@ __device__ __forceinline__ void normalise(float (&x)[8], const uint4& weight, fl
 // rows into a 4-bit cache, 8 heads of 128, about 10 us, most of it the chain of a row's minimum, maximum,
 // step and quotients.  Three CTAs an SM: two take 102 us, four (64 registers) 88.
 template <int D, int QK, int KIND, bool ROT>
-__global__ void __launch_bounds__(256, append_ctas(KIND, ROT)) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, KIND == STORE_16 && !ROT ? 4 : 3) append_kernel(const AppendParams p) {
   constexpr int L = D / 8, RPS = 32 / L;  // lanes of a row, rows of a step
   constexpr int U = 4;                    // steps whose rows are loaded together
   const int lane = threadIdx.x & 31, sub = lane / L, c0 = lane % L * 8;

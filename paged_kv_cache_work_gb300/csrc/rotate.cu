@@ -129,8 +129,8 @@ extern "C" pa_status pa_append_rotated(const pa_config* cfg, const pa_rotary* ro
   p.r.axis1 = half ? r.axis_pairs[0] : 0;
   p.r.axis2 = half && r.num_axes > 1 ? r.axis_pairs[0] + r.axis_pairs[1] : half;
   p.r.eps = r.eps;
+  split_rows(p, c.head_dim, sms, stores);
   const int qk = c.q_dtype == PA_FP16 ? Q_FP16 : Q_BF16, kind = stores ? store_kind(c) : STORE_16;
-  split_rows(p, c.head_dim, sms, kind, true, stores);
   return launch_rotate(p, c.head_dim, qk, kind, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
