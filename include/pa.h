@@ -179,11 +179,11 @@ PA_API pa_status pa_plan(const pa_config *cfg, const int32_t *block_tables, cons
  * The tables and lengths must be the ones given to pa_plan, with the same contents.  A CTA
  * of the tcgen05 decode (33 or more query rows per kv head; head dim 128 or 256, 128 for an
  * fp8 cache), of the streaming decode (PA_SCALE_PER_BLOCK with head dim 64, or with up to 32
- * query rows per kv head) and of the 4-bit decode derives its first work item from the lengths (the planner's rules) and
- * starts on it while the planner is still running; it waits for the planner before the rest of
- * its list and before writing anything, and raises PA_FLAG_STALE_PLAN if the planner's first item
- * differs.  Where the planner runs no longer, and the other decode kernels always, a CTA first waits for
- * the launch before it.
+ * query rows per kv head) and of the 4-bit decode derives its first work item from the lengths
+ * (the planner's rules) and starts on it while the planner is still running; it waits for the
+ * planner before the rest of its list and before writing anything, and raises
+ * PA_FLAG_STALE_PLAN if the planner's first item differs.  Where the planner runs no longer, and
+ * the other decode kernels always, a CTA first waits for the launch before it.
  * The kernels launch with programmatic dependent launch.  A kernel of the caller's between pa_plan and
  * pa_decode that writes q, the caches, the scales, the tables or the lengths may do so too, if it lets its
  * dependents start no earlier than its own wait on the launch before it.
@@ -401,9 +401,9 @@ typedef struct {
  *   flags          NULL, or a device int32: PA_FLAG_BAD_LENGTHS (nothing of that sequence is
  *                  written), PA_FLAG_BAD_POSITION (nothing of that token is written),
  *                  PA_FLAG_BAD_BLOCK_ID (that token's K and V do not go into a page)
- * No other two arrays may overlap, where one of them is written.  Reads cfg's batch, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
- * max_blocks_per_seq, num_blocks, q_dtype, kv_dtype and kv_scale_mode.  Stream-ordered, allocates
- * nothing, never synchronises. */
+ * No other two arrays may overlap, where one of them is written.  Reads cfg's batch, max_q_len,
+ * num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, q_dtype, kv_dtype
+ * and kv_scale_mode.  Stream-ordered, allocates nothing, never synchronises. */
 PA_API pa_status pa_append_rotated(const pa_config *cfg, const pa_rotary *rotary, const void *q,
                                    const void *k_new, const void *v_new,
                                    const int32_t *block_tables, const int32_t *context_lens,

@@ -8,9 +8,10 @@
 // tokens (channels) along the MMA's 16 rows and query rows along its 8 columns: a tile of up to 8
 // query rows then costs half of what one of 16 does, which is what widening the codes leaves to save.
 // A word of codes is eight channels; two halves of it masked into the mantissa of 1024 (or 64; the
-// conversion that int4.cuh cites), less 1032 (72), are two f16 operands.  The order of channels inside a k-step is the queries' own affair,
-// so a K row's words are operands as they lie.  A V operand holds one channel of two tokens: one byte
-// permute brings the halves of two tokens' words together.  P^T comes from S^T through movmatrix.
+// conversion that int4.cuh cites), less 1032 (72), are two f16 operands.  The order of channels inside
+// a k-step is the queries' own affair, so a K row's words are operands as they lie.  A V operand holds
+// one channel of two tokens: one byte permute brings the halves of two tokens' words together.  P^T
+// comes from S^T through movmatrix.
 //
 // What bounds it are the instructions of the few warps whose state fits the registers, so little is
 // done twice: the queries' fragments lie in shared memory, one copy a CTA; a lane a token makes a
